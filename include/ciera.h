@@ -365,6 +365,93 @@ ciera_status_t ciera_hash_update(const ciera_tensor_t* t, uint32_t rank, const v
 ciera_status_t ciera_cache_update(const ciera_tensor_t* t, const void* weights_full,
                                   uint8_t* cache_full, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The experts' products and their 4-bit copies: what a layer's rebuilt weights
+ * are used for.  The conventions above hold; every call here enqueues kernels
+ * only (no scratch, no copies, no allocation), so it may be captured into a
+ * graph, and any number of calls may run at once on streams of their own.
+ * Sums are held in fp32 and rounded once to the output's type; the order of a
+ * sum depends on sizes alone, so equal calls give equal bits.
+ *
+ * A matrix, or a stack of `groups` matrices, row-major: element (g, r, c) at
+ * data + g * group_stride + r * row_stride + c, strides in elements.  Strides
+ * of an input may be anything, 0 included (one matrix shared by all groups);
+ * an output's elements must lie apart (row_stride >= cols, group_stride >=
+ * the extent of one matrix).  data is aligned to its element; rows that start
+ * at multiples of 16 bytes are read faster.  rows, cols and groups are below
+ * 2^30.  An output's address range (first to last element) must not overlap
+ * an input's: INVALID_ARG.  Where a call has nothing to write it returns
+ * without looking at the pointers. */
+typedef struct {
+  void* data;
+  uint32_t dtype; /* ciera_dtype_t */
+  uint32_t groups;
+  uint64_t rows, cols;
+  uint64_t row_stride, group_stride;
+} ciera_matrix_t;
+
+/* A stack of 4-bit matrices in microscaled floating point (blocks of 32 values
+ * of a row share a power of two): per row, cols padded to a multiple of 128 (kp)
+ *   codes  [groups][rows][kp / 2]: value 2i of a row in the low nibble of byte i,
+ *     2i + 1 in the high one; bit 3 the sign, bits 0-2 the magnitude
+ *     0 .5 1 1.5 2 3 4 6; 16-byte aligned
+ *   scales [groups][rows][kp / 32]: byte s of a block stands for 2^(s - 127),
+ *     255 for NaN; 4-byte aligned
+ * both dense.  Codes past cols are zero. */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  uint32_t groups, reserved;
+  uint64_t rows, cols;
+} ciera_mx_t;
+
+/* ciera_mx_sizes -- bytes of the codes and of the scales of a stack.  Host only. */
+ciera_status_t ciera_mx_sizes(uint32_t groups, uint64_t rows, uint64_t cols, uint64_t* code_bytes,
+                              uint64_t* scale_bytes);
+
+/* ciera_mx_quantize -- x (bf16, fp16 or fp32) to 4 bits, blocks along `axis`:
+ * axis 1, along the rows (q has x's rows and cols); axis 0, down the columns (q
+ * is the transpose: q.rows = x.cols, q.cols = x.rows), for weights whose
+ * contraction runs down their columns.  With m a block's largest magnitude its
+ * scale is 2^e, e = max(floor(log2 m) - 2, -127); each value becomes the
+ * nearest of the sixteen times 2^e, of two equally near ones the one with an
+ * even code, magnitudes above 6 * 2^e becoming 6 * 2^e.  A block holding an
+ * infinity or a NaN gets the scale NaN and zero codes.  The end of a last
+ * block, past q.cols, counts as zeros. */
+ciera_status_t ciera_mx_quantize(const ciera_matrix_t* x, uint32_t axis, const ciera_mx_t* q, void* stream);
+
+/* ciera_mx_dequantize -- the values q stands for, rounded to out's type (exact
+ * in bf16 and fp32).  out has q's groups, rows and cols. */
+ciera_status_t ciera_mx_dequantize(const ciera_mx_t* q, const ciera_matrix_t* out, void* stream);
+
+/* Products grouped by expert.  offsets: a device array of groups + 1 int32, in
+ * ascending order from 0 to at most the rows of x; the rows offsets[g] <= i <
+ * offsets[g + 1] belong to group g.  Groups may be empty.  Output rows from
+ * offsets[groups] on are left as they were.  NULL, allowed for one group,
+ * gives it every row.  The array is read on the device: offsets out of order
+ * or range leave out unspecified, but nothing outside the operands is read or
+ * written.
+ *
+ * ciera_mx_mm -- out[i, n] = sum_k a[i, k] b_g[n, k] for the group g of row i:
+ * a has one group, rows x K; b groups x N x K; out rows x N, of any type. */
+ciera_status_t ciera_mx_mm(const ciera_mx_t* a, const ciera_mx_t* b, const int32_t* offsets,
+                           const ciera_matrix_t* out, void* stream);
+
+/* ciera_group_mm -- out[i, n] = sum_k x[i, k] w_g[k, n] (transpose_w 0, w
+ * groups x K x N) or sum_k x[i, k] w_g[n, k] (transpose_w 1, w groups x N x K).
+ * x and w are both bf16 or both fp16, out of their type or fp32.  With y = x w_g
+ * the gradient of x is this product of dy and the same w with the other
+ * transpose_w. */
+ciera_status_t ciera_group_mm(const ciera_matrix_t* x, const ciera_matrix_t* w, uint32_t transpose_w,
+                              const int32_t* offsets, const ciera_matrix_t* out, void* stream);
+
+/* ciera_group_wgrad -- out_g[k, n] = sum over the group's rows i of
+ * x[i, k] dy[i, n]: the gradient of w [groups, K, N] in y = x w_g (exchange x
+ * and dy for w [groups, N, K]).  Types as above; an empty group's gradient is
+ * zero. */
+ciera_status_t ciera_group_wgrad(const ciera_matrix_t* x, const ciera_matrix_t* dy, const int32_t* offsets,
+                                 const ciera_matrix_t* out, void* stream);
+
 const char* ciera_status_str(ciera_status_t s);
 uint32_t ciera_abi_version(void);
 

@@ -22,7 +22,8 @@ CIERA_NOALLOC_SCRATCH_BYTES = 1 << 20  # the static scratch of ciera_encode_noal
 EXPORTS = ["ciera_plan", "ciera_plan_batch", "ciera_select", "ciera_shard", "ciera_encode_scratch_bytes", "ciera_encode",
            "ciera_encode_prepare", "ciera_encode_launch", "ciera_decode_scratch_bytes",
            "ciera_decode", "ciera_decode_prepare", "ciera_decode_launch", "ciera_cache_update",
-           "ciera_hash_update", "ciera_set_sync_polls", "ciera_encode_noalloc", "ciera_decode_launch_bounded",
+           "ciera_hash_update", "ciera_mx_sizes", "ciera_mx_quantize", "ciera_mx_dequantize", "ciera_mx_mm",
+           "ciera_group_mm", "ciera_group_wgrad", "ciera_set_sync_polls", "ciera_encode_noalloc", "ciera_decode_launch_bounded",
            "ciera_status_str", "ciera_abi_version", "ciera_last_error"]
 
 
@@ -67,6 +68,18 @@ class EncodeItem(ctypes.Structure):
 class DecodeItem(ctypes.Structure):
     _fields_ = [("t", Tensor), ("streams", c_void_p), ("slot_bytes", c_uint64),
                 ("out_full", c_void_p), ("cache_full", c_void_p), ("rank_streams", c_void_p)]
+
+
+class Matrix(ctypes.Structure):
+    """A row-major matrix or a stack of them in device memory (strides in elements)."""
+    _fields_ = [("data", c_void_p), ("dtype", c_uint32), ("groups", c_uint32), ("rows", c_uint64),
+                ("cols", c_uint64), ("row_stride", c_uint64), ("group_stride", c_uint64)]
+
+
+class Mx(ctypes.Structure):
+    """A stack of 4-bit matrices: codes and scales in device memory."""
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("groups", c_uint32), ("reserved", c_uint32),
+                ("rows", c_uint64), ("cols", c_uint64)]
 
 
 class Batch(ctypes.Structure):
@@ -114,6 +127,13 @@ def _load() -> ctypes.CDLL:
         "ciera_decode_launch_bounded": (c_int, [POINTER(Batch), c_uint32, c_void_p]),
         "ciera_cache_update": (c_int, [POINTER(Tensor), c_void_p, c_void_p, c_void_p]),
         "ciera_hash_update": (c_int, [POINTER(Tensor), c_uint32, c_void_p, c_void_p, c_void_p]),
+        "ciera_mx_sizes": (c_int, [c_uint32, c_uint64, c_uint64, POINTER(c_uint64), POINTER(c_uint64)]),
+        "ciera_mx_quantize": (c_int, [POINTER(Matrix), c_uint32, POINTER(Mx), c_void_p]),
+        "ciera_mx_dequantize": (c_int, [POINTER(Mx), POINTER(Matrix), c_void_p]),
+        "ciera_mx_mm": (c_int, [POINTER(Mx), POINTER(Mx), c_void_p, POINTER(Matrix), c_void_p]),
+        "ciera_group_mm": (c_int, [POINTER(Matrix), POINTER(Matrix), c_uint32, c_void_p, POINTER(Matrix),
+                                   c_void_p]),
+        "ciera_group_wgrad": (c_int, [POINTER(Matrix), POINTER(Matrix), c_void_p, POINTER(Matrix), c_void_p]),
         "ciera_set_sync_polls": (None, [c_uint32]),
         "ciera_encode_noalloc": (c_int, [POINTER(EncodeItem), c_uint32, c_void_p]),
         "ciera_status_str": (c_char_p, [c_int]),
@@ -366,3 +386,101 @@ def ciera_decode_launch(batch: Batch, stream=None) -> None:
 def ciera_decode_launch_bounded(batch: Batch, max_workgroups: int, stream=None) -> None:
     _check(_lib.ciera_decode_launch_bounded(byref(batch), max_workgroups, _stream(stream)),
            "ciera_decode_launch_bounded")
+
+
+# ------------------------------------------- expert products and 4-bit weights
+
+def _on_current_device(t, what: str) -> None:
+    import torch
+    if t.device.type != "cuda":
+        raise ValueError(f"{what}: on {t.device}, not on a GPU")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def matrix_item(t, what: str = "matrix") -> Matrix:
+    """A 2-D or 3-D torch tensor of bf16, fp16 or fp32 on the current GPU, with
+    any strides but the last, which must be 1 (a Matrix is passed through)."""
+    if isinstance(t, Matrix):
+        return t
+    import torch
+    codes = {torch.bfloat16: CIERA_BF16, torch.float32: CIERA_FP32, torch.float16: CIERA_FP16}
+    if t.dtype not in codes:
+        raise ValueError(f"{what}: dtype {t.dtype}, expected bfloat16, float16 or float32")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{what}: {t.dim()} dimensions, expected 2 or 3")
+    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: values of a row are not adjacent (shape {tuple(t.shape)}, stride {t.stride()})")
+    _on_current_device(t, what)
+    groups, rs = (t.shape[0], t.stride(1)) if t.dim() == 3 else (1, t.stride(0))
+    return Matrix(t.data_ptr(), codes[t.dtype], groups, t.shape[-2], t.shape[-1], rs,
+                  t.stride(0) if t.dim() == 3 else 0)
+
+
+def mx_item(codes, scales, groups: int, rows: int, cols: int) -> Mx:
+    """codes and scales: byte tensors (or addresses) of ciera_mx_sizes bytes."""
+    need = ciera_mx_sizes(groups, rows, cols)
+    ptrs = []
+    for t, n, what in ((codes, need[0], "codes"), (scales, need[1], "scales")):
+        if not isinstance(t, int):
+            if t.element_size() != 1:
+                raise ValueError(f"{what}: dtype {t.dtype}, expected bytes")
+            _on_current_device(t, what)
+        ptrs.append(_ptr(t, what, numel=n))
+    return Mx(ptrs[0], ptrs[1], groups, 0, rows, cols)
+
+
+def _mx(q) -> Mx:
+    return q if isinstance(q, Mx) else q.item
+
+
+def _offsets(offsets, groups: int) -> Optional[int]:
+    if offsets is None or isinstance(offsets, int):
+        return offsets
+    import torch
+    p = _ptr(offsets, "offsets", torch.int32, groups + 1)
+    _on_current_device(offsets, "offsets")
+    return p
+
+
+def ciera_mx_sizes(groups: int, rows: int, cols: int) -> Tuple[int, int]:
+    c, s = c_uint64(), c_uint64()
+    _check(_lib.ciera_mx_sizes(groups, rows, cols, byref(c), byref(s)), "ciera_mx_sizes")
+    return c.value, s.value
+
+
+def ciera_mx_quantize(x, q, axis: int = 1, stream=None) -> None:
+    """x [rows, cols] or [groups, rows, cols] to the 4-bit stack q, blocks along
+    axis 1 (the rows) or 0 (the columns: q is the transpose)."""
+    if axis not in (0, 1):
+        raise ValueError(f"axis: {axis}, expected 0 or 1")
+    _check(_lib.ciera_mx_quantize(byref(matrix_item(x, "x")), axis, byref(_mx(q)), _stream(stream)),
+           "ciera_mx_quantize")
+
+
+def ciera_mx_dequantize(q, out, stream=None) -> None:
+    """The values that the 4-bit stack q stands for."""
+    _check(_lib.ciera_mx_dequantize(byref(_mx(q)), byref(matrix_item(out, "out")), _stream(stream)),
+           "ciera_mx_dequantize")
+
+
+def ciera_mx_mm(a, b, out, offsets=None, stream=None) -> None:
+    """out[i] = a[i] b_g^T for the rows offsets[g] <= i < offsets[g + 1] of every group g of b."""
+    qb = _mx(b)
+    _check(_lib.ciera_mx_mm(byref(_mx(a)), byref(qb), _offsets(offsets, qb.groups), byref(matrix_item(out, "out")),
+                            _stream(stream)), "ciera_mx_mm")
+
+
+def ciera_group_mm(x, w, out, offsets=None, transpose_w: bool = False, stream=None) -> None:
+    """out[i] = x[i] w_g (transpose_w: x[i] w_g^T) for the rows offsets[g] <= i < offsets[g + 1]
+    of every group g of w."""
+    mw = matrix_item(w, "w")
+    _check(_lib.ciera_group_mm(byref(matrix_item(x, "x")), byref(mw), int(transpose_w), _offsets(offsets, mw.groups),
+                               byref(matrix_item(out, "out")), _stream(stream)), "ciera_group_mm")
+
+
+def ciera_group_wgrad(x, dy, out, offsets=None, stream=None) -> None:
+    """out_g = x_g^T dy_g over the rows offsets[g] <= i < offsets[g + 1] of every group g of out."""
+    mo = matrix_item(out, "out")
+    _check(_lib.ciera_group_wgrad(byref(matrix_item(x, "x")), byref(matrix_item(dy, "dy")),
+                                  _offsets(offsets, mo.groups), byref(mo), _stream(stream)), "ciera_group_wgrad")

@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libciera.so")
-SOURCES = ["ciera_api.cpp", "ciera_kernels.hip"]
+SOURCES = ["ciera_api.cpp", "ciera_ops.cpp", "ciera_kernels.hip", "ciera_group.hip", "ciera_mx.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

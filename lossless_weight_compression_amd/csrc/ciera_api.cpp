@@ -15,9 +15,21 @@
 #include <vector>
 
 #include "ciera.h"
+#include "ciera_host.h"
 #include "ciera_internal.h"
 
 using namespace ciera;
+
+namespace ciera {
+
+thread_local char g_last_error[256] = "no error";
+
+ciera_status_t device_error(const char* what, hipError_t e) {
+  snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
+  return CIERA_ERR_DEVICE;
+}
+
+}  // namespace ciera
 
 namespace {
 
@@ -43,14 +55,6 @@ bool overlap(const void* a, uint64_t alen, const void* b, uint64_t blen) {
 }
 uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 uint64_t bitmap_bytes(uint64_t n, uint32_t B) { return ((n + B - 1) / B + 7) / 8; }
-
-// The HIP error behind the calling thread's last CIERA_ERR_DEVICE.
-thread_local char g_last_error[256] = "no error";
-
-ciera_status_t device_error(const char* what, hipError_t e) {
-  snprintf(g_last_error, sizeof(g_last_error), "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
-  return CIERA_ERR_DEVICE;
-}
 
 ciera_status_t check_tensor(const ciera_tensor_t* t) {
   if (!t) return CIERA_ERR_INVALID_ARG;

@@ -10,8 +10,10 @@ buffers, what one rank keeps across iterations and receives each iteration:
   out     -- the rebuilt full tensors
 
 and issues one batched ``ciera_encode`` (a rank's shards of every tensor) or one
-batched ``ciera_decode`` (every tensor from all W slots) per call.  torch is
-used for device memory and streams only.
+batched ``ciera_decode`` (every tensor from all W slots) per call.  ``stack``
+views the same matrix of several experts as one operand of the grouped products,
+``quantize`` makes its 4-bit copy.  torch is used for device memory and streams
+only.
 """
 from __future__ import annotations
 
@@ -93,7 +95,39 @@ class LayerCodec:
         a = self.out_off[i]
         return self.out[a:a + self.numel[i] * self.e].view(self.dtype)
 
+    def stack(self, indices: Sequence[int]) -> torch.Tensor:
+        """The rebuilt tensors of these indices (the same matrix of every expert, say)
+        as one [len, rows, cols] view of ``out``: equal shapes at equal distances."""
+        if self.out is None:
+            raise ValueError("stack: the codec was made without outputs")
+        idx = list(indices)
+        if not idx:
+            raise ValueError("stack: no indices")
+        t = self.tensors[idx[0]]
+        off = [self.out_off[i] for i in idx]
+        step = off[1] - off[0] if len(idx) > 1 else _align(t.rows * t.cols * self.e, 256)
+        if step <= 0 or any(b - a != step for a, b in zip(off, off[1:])):
+            raise ValueError("stack: the tensors do not lie at equal distances")
+        if any((self.tensors[i].rows, self.tensors[i].cols) != (t.rows, t.cols) for i in idx):
+            raise ValueError("stack: the tensors' shapes differ")
+        flat = self.out.view(self.dtype)
+        return torch.as_strided(flat, (len(idx), t.rows, t.cols), (step // self.e, t.cols, 1),
+                                flat.storage_offset() + off[0] // self.e)
+
     # ------------------------------------------------------------------ calls
+    def quantize(self, indices: Sequence[int], axis: int = 0, into: Optional["MxMatrix"] = None,
+                 stream=None) -> "MxMatrix":
+        """4-bit copy of the rebuilt tensors of these indices (one call), as ciera_mx_mm
+        takes it: axis 0 for [in, out] matrices, 1 for [out, in] ones."""
+        w = self.stack(indices)
+        g, r, c = w.shape
+        if axis not in (0, 1):
+            raise ValueError(f"axis: {axis}, expected 0 or 1")
+        shape = (r, c) if axis else (c, r)
+        q = into if into is not None else MxMatrix(*shape, groups=g, device=self.device)
+        q.quantize(w, axis, stream)
+        return q
+
     def seed_cache(self, weights: Sequence[torch.Tensor], stream=None) -> None:
         """cache <- exponents of the given full tensors (exponent reuse switched on)."""
         for i, w in enumerate(weights):
@@ -181,3 +215,33 @@ class PreparedEncode:
 
     def launch(self, stream=None) -> None:
         B.ciera_encode_launch(self.batch, stream=stream)
+
+
+class MxMatrix:
+    """Device memory of a stack of 4-bit matrices ([groups, rows, cols]): ``codes``
+    [groups, rows, kp / 2] and ``scales`` [groups, rows, kp / 32] bytes, kp = cols
+    rounded up to 128, or the caller's own tensors of these sizes."""
+
+    def __init__(self, rows: int, cols: int, groups: int = 1, device="cuda",
+                 codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+        B.ciera_mx_sizes(groups, rows, cols)  # refuses sizes the library does not take
+        kp = _align(cols, 128)
+        self.groups, self.rows, self.cols = groups, rows, cols
+        if (codes is None) != (scales is None):
+            raise ValueError("codes and scales: give both or neither")
+        if codes is None:
+            codes = torch.empty(groups, rows, kp // 2, dtype=torch.uint8, device=device)
+            scales = torch.empty(groups, rows, kp // 32, dtype=torch.uint8, device=device)
+        self.codes, self.scales = codes, scales
+        self.item = B.mx_item(codes, scales, groups, rows, cols)
+
+    def quantize(self, x: torch.Tensor, axis: int = 1, stream=None) -> "MxMatrix":
+        B.ciera_mx_quantize(x, self, axis, stream)
+        return self
+
+    def dequantize(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The values ([groups, rows, cols], bf16 unless ``out`` says otherwise)."""
+        if out is None:
+            out = torch.empty(self.groups, self.rows, self.cols, dtype=torch.bfloat16, device=self.codes.device)
+        B.ciera_mx_dequantize(self, out, stream)
+        return out
