@@ -93,9 +93,10 @@ __device__ __forceinline__ void general_tile(const uint16_t* a, uint64_t lda, in
 template <typename D, bool TRANS, bool FLAT, typename O, int BM, int BN>
 __global__ __launch_bounds__(256) void group_mm_general(GroupMmArgs a) {
   GroupTile t;
-  if (!find_group_tile(a.offsets, a.groups, a.rows, BM, (a.n + BN - 1) / BN, blockIdx.x, &t)) return;
+  int tn;
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
-  const int mleft = t.count - t.m * BM, n0 = t.n * BN, nleft = a.n - n0;
+  const int mleft = t.count - t.m * BM, n0 = tn * BN, nleft = a.n - n0;
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.ldx;
   const uint16_t* w = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0);
   O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
@@ -105,10 +106,11 @@ __global__ __launch_bounds__(256) void group_mm_general(GroupMmArgs a) {
 template <typename D, bool FLAT, typename O, int BM, int BN>
 __global__ __launch_bounds__(256) void group_wgrad_general(GroupWgradArgs a) {
   const uint32_t mt = (a.k + BM - 1) / BM, nt = (a.n + BN - 1) / BN;
-  const uint64_t all = (uint64_t)mt * nt * a.groups, per = all / kXcds, rem = all % kXcds;
-  const uint32_t x = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
-  if (idx >= per + (x < rem ? 1 : 0)) return;
-  const uint64_t tile = x * per + min((uint64_t)x, rem) + idx;
+  uint64_t first;
+  uint32_t many;
+  die_run((uint64_t)mt * nt * a.groups, blockIdx.x % kXcds, &first, &many);
+  if (blockIdx.x / kXcds >= many) return;
+  const uint64_t tile = first + blockIdx.x / kXcds;
   const int g = tile / ((uint64_t)mt * nt);
   const int m0 = (tile / nt % mt) * BM, n0 = (tile % nt) * BN;
   int begin, count;
@@ -120,6 +122,289 @@ __global__ __launch_bounds__(256) void group_wgrad_general(GroupWgradArgs a) {
                                                  a.n - n0);
 }
 
+// 16 zero bytes: what is loaded in place of contraction steps past the end.
+__device__ const i32x4 kZeros = {0, 0, 0, 0};
+
+// 16 bytes per lane from memory straight into LDS, lane l's at `lds` + l.  Written in
+// assembly because the compiler, where it sees such a load, waits for it before the
+// next LDS read of any address; the kernels here wait themselves (arrive).  It has no
+// result register; the clobber keeps LDS reads from moving across it.  m0, which holds
+// the address in LDS, is the compiler's scratch register too, set anew at each use.
+__device__ __forceinline__ void load_lds16(const void* p, i32x4* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "memory");
+}
+__device__ __forceinline__ void load_lds16(const char* base, uint32_t offset, i32x4* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base)
+               : "memory");
+}
+
+// 256 x 256 tiles of C = A B, one after another by the same workgroup: 8 waves of
+// 128 x 64 of a tile each.  Rows start at multiples of 16 bytes and hold multiples of
+// 8 values along their contiguous side.  64 contraction steps at a time (a stage)
+// go from memory into one half of LDS, not passing registers, while the other half
+// is multiplied; the fragments of half a stage are read while those of the half
+// before are multiplied, across the one barrier of a stage too.  The first stage
+// of the next tile is on its way while this one's results are stored.
+template <typename D, bool AKC, bool BKC, typename O>
+struct BigTiles {
+  static constexpr int BM = 256, BN = 256, BK = 64, T = 512;
+  typedef LdsTile<AKC, BM, BK> TA;
+  typedef LdsTile<BKC, BN, BK> TB;
+  typedef typename D::V V;
+  static constexpr int NA = TA::kChunks / T, NB = TB::kChunks / T;
+  static constexpr int kStage = TA::kChunks + TB::kChunks;
+
+  i32x4* lds;
+  int wave, lane, r0, c0;
+  // the tile being loaded
+  const char *pa, *pb;         // its operands at the next stage
+  uint64_t da, db;             // bytes from stage to stage
+  uint32_t oa[NA], ob[NB];     // this lane's chunks of a stage, bytes from there
+  int left;                    // contraction steps not loaded yet
+  // the tile being multiplied
+  f32x4 acc[8][4];
+  V fa[2][4], fb[2][4];
+
+  __device__ __forceinline__ void init(i32x4* l) {
+    lds = l;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    lane = threadIdx.x & 63;
+    r0 = (wave >> 2) * 128;
+    c0 = (wave & 3) * 64;
+  }
+  // a lane's chunk has a fixed place in LDS, so it fetches what the permutation puts
+  // there; rows and columns past the tile's end repeat the last one
+  __device__ __forceinline__ void aim(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
+                                      int klen) {
+    pa = reinterpret_cast<const char*>(a);
+    pb = reinterpret_cast<const char*>(b);
+    da = AKC ? BK * 2 : BK * 2 * lda;
+    db = BKC ? BK * 2 : BK * 2 * ldb;
+    left = klen;
+#pragma unroll
+    for (int i = 0; i < NA; i++) {
+      const int p = i * T + threadIdx.x, line = p / TA::kPerRow, c = TA::swizzle(line, p % TA::kPerRow) * 8;
+      oa[i] = 2 * (AKC ? (uint32_t)min(line, am - 1) * (uint32_t)lda + c : line * (uint32_t)lda + min(c, am - 8));
+    }
+#pragma unroll
+    for (int i = 0; i < NB; i++) {
+      const int p = i * T + threadIdx.x, line = p / TB::kPerRow, c = TB::swizzle(line, p % TB::kPerRow) * 8;
+      ob[i] = 2 * (BKC ? (uint32_t)min(line, bn - 1) * (uint32_t)ldb + c : line * (uint32_t)ldb + min(c, bn - 8));
+    }
+  }
+  // Part i of the next stage into half `buf`.  FULL: the stage has 64 steps; else
+  // steps past the end arrive as zeros.
+  template <bool FULL>
+  __device__ __forceinline__ void load_a(int buf, int i) {
+    i32x4* at = lds + buf * kStage + wave * 64 + i * T;
+    if (FULL) return load_lds16(pa, oa[i], at);
+    const int p = i * T + threadIdx.x, line = p / TA::kPerRow;
+    const int k = AKC ? TA::swizzle(line, p % TA::kPerRow) * 8 : line;
+    load_lds16(k < left ? pa + oa[i] : reinterpret_cast<const char*>(&kZeros), at);
+  }
+  template <bool FULL>
+  __device__ __forceinline__ void load_b(int buf, int i) {
+    i32x4* at = lds + buf * kStage + TA::kChunks + wave * 64 + i * T;
+    if (FULL) return load_lds16(pb, ob[i], at);
+    const int p = i * T + threadIdx.x, line = p / TB::kPerRow;
+    const int k = BKC ? TB::swizzle(line, p % TB::kPerRow) * 8 : line;
+    load_lds16(k < left ? pb + ob[i] : reinterpret_cast<const char*>(&kZeros), at);
+  }
+  __device__ __forceinline__ void loaded() {
+    pa += da;
+    pb += db;
+    left -= BK;
+  }
+  __device__ __forceinline__ void load(int buf) {
+    for (int i = 0; i < NA; i++) left >= BK ? load_a<true>(buf, i) : load_a<false>(buf, i);
+    for (int i = 0; i < NB; i++) left >= BK ? load_b<true>(buf, i) : load_b<false>(buf, i);
+    loaded();
+  }
+  // fragment i of the upper or lower 64 rows (UP), or j of the 64 columns, at half H of a stage
+  template <int H, int UP>
+  __device__ __forceinline__ void read_a(int buf, int slot, int i) {
+    fa[slot][i] = __builtin_bit_cast(V, TA::fragment(lds + buf * kStage, r0 + UP * 64 + i * 16, H * 32));
+  }
+  template <int H>
+  __device__ __forceinline__ void read_b(int buf, int slot, int j) {
+    fb[slot][j] = __builtin_bit_cast(V, TB::fragment(lds + buf * kStage + TA::kChunks, c0 + j * 16, H * 32));
+  }
+  template <int UP>
+  __device__ __forceinline__ void multiply(int sa, int sb, int i) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) acc[UP * 4 + i][j] = mfma(fb[sb][j], fa[sa][i], acc[UP * 4 + i][j]);
+  }
+  // everything asked for has arrived, for every wave
+  static __device__ __forceinline__ void arrive() {
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // The first three quarters of the stage in half `buf`: 16 matrix instructions each
+  // and between them the reads of the next quarter's fragments, in a fixed order.
+  __device__ __forceinline__ void quarters(int buf) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      multiply<0>(0, 0, i);
+      read_a<0, 1>(buf, 1, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      multiply<1>(1, 0, i);
+      read_b<1>(buf, 1, i);
+      read_a<1, 0>(buf, 0, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      multiply<0>(0, 1, i);
+      read_a<1, 1>(buf, 1, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // One stage, the one after the next asked for in its place, up to the first
+  // fragments of the next.
+  template <bool FULL>
+  __device__ __forceinline__ void stage(int buf, bool more) {
+    quarters(buf);
+    arrive();
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (FULL || more) {
+        load_a<FULL>(buf, i);
+        load_b<FULL>(buf, i);
+      }
+      multiply<1>(1, 1, i);
+      read_a<0, 0>(buf ^ 1, 0, i);
+      read_b<0>(buf ^ 1, 0, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (FULL || more) loaded();
+  }
+  // All but the last quarter of the tile whose first stage is on its way into half
+  // `buf`, `klen` contraction steps in all; returns the half where another tile may begin.
+  __device__ __forceinline__ int stages(int klen, int buf) {
+    static_assert(NA == 4 && NB == 4, "a stage's loads are spread over four parts of a quarter");
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+    const int steps = max((klen + BK - 1) / BK, 1), full = klen / BK;
+    arrive();
+    if (steps > 1) load(buf ^ 1);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      read_a<0, 0>(buf, 0, i);
+      read_b<0>(buf, 0, i);
+    }
+    int s = 0;
+    for (; s + 2 < full; s++) {
+      stage<true>(buf, true);
+      buf ^= 1;
+    }
+    for (; s + 1 < steps; s++) {
+      stage<false>(buf, s + 2 < steps);
+      buf ^= 1;
+    }
+    quarters(buf);
+    arrive();
+    return buf ^ 1;
+  }
+  __device__ __forceinline__ void last_quarter() {
+#pragma unroll
+    for (int i = 0; i < 4; i++) multiply<1>(1, 1, i);
+  }
+  __device__ __forceinline__ void store(O* out, uint64_t ldo, int om, int on) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int m = r0 + i * 16 + (lane & 15);
+      if (m >= om) continue;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int n = c0 + j * 16 + (lane >> 4) * 4;
+        if (n < on) store_pack(out + (uint64_t)m * ldo + n, acc[i][j]);  // on is a multiple of 8
+      }
+    }
+  }
+};
+
+constexpr uint32_t kBigLds = 2 * 2 * 256 * 64 * 2;  // bytes: two stages of two operands
+
+template <typename D, bool TRANS, typename O>
+__global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
+  __shared__ i32x4 lds[kBigLds / 16];
+  GroupTiles<256> tiles;
+  tiles.init(a.offsets, a.groups, a.rows);
+  const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds;
+  uint64_t first;
+  uint32_t many;
+  die_run((uint64_t)tiles.total * nt, blockIdx.x % kXcds, &first, &many);
+  uint32_t at = blockIdx.x / kXcds;
+  if (at >= many) return;
+  BigTiles<D, true, TRANS, O> big;
+  big.init(lds);
+  GroupTile t;
+  int n0;
+  auto aim = [&](uint64_t tile) {
+    t = tiles.find((uint32_t)(tile / nt));
+    n0 = (int)(tile % nt) * 256;
+    const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256;
+    big.aim(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, t.count - t.m * 256,
+            static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw,
+            a.n - n0, a.k);
+  };
+  aim(first + at);
+  big.load(0);
+  int buf = 0;
+  for (;;) {
+    O* out = static_cast<O*>(a.out) + ((uint64_t)t.begin + (uint64_t)t.m * 256) * a.ldo + n0;
+    const int om = t.count - t.m * 256, on = a.n - n0;
+    buf = big.stages(a.k, buf);
+    at += stride;
+    const bool more = at < many;
+    if (more) {
+      aim(first + at);
+      big.load(buf);
+    }
+    big.last_quarter();
+    big.store(out, a.ldo, om, on);
+    if (!more) return;
+  }
+}
+
+template <typename D, typename O>
+__global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
+  __shared__ i32x4 lds[kBigLds / 16];
+  const uint32_t mt = (a.k + 255) / 256, nt = (a.n + 255) / 256;
+  uint64_t first;
+  uint32_t many;
+  die_run((uint64_t)mt * nt * a.groups, blockIdx.x % kXcds, &first, &many);
+  if (blockIdx.x / kXcds >= many) return;
+  const uint64_t tile = first + blockIdx.x / kXcds;
+  const int g = tile / ((uint64_t)mt * nt);
+  const int m0 = (tile / nt % mt) * 256, n0 = (tile % nt) * 256;
+  int begin, count;
+  group_range(a.offsets, g, a.rows, &begin, &count);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  count = __builtin_amdgcn_readfirstlane(count);
+  BigTiles<D, false, false, O> big;
+  big.init(lds);
+  big.aim(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
+          static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, a.n - n0, count);
+  big.load(0);
+  big.stages(count, 0);
+  big.last_quarter();
+  big.store(static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo, a.k - m0, a.n - n0);
+}
+
+// Whether a tile's operands can be addressed with 32-bit byte offsets from their
+// first element: 256 rows, or 64 contraction steps, of `ld` values.
+bool short_stride(uint64_t ld) { return ld < (1u << 22); }
+
 // Most row tiles of height bm that ascending offsets can make of `rows` rows.
 uint64_t max_row_tiles(const GroupMmArgs& a, uint64_t bm) {
   const uint64_t one = (a.rows + bm - 1) / bm;
@@ -130,6 +415,13 @@ uint64_t max_row_tiles(const GroupMmArgs& a, uint64_t bm) {
 
 template <typename D, bool TRANS, bool FLAT, typename O>
 hipError_t run_mm(const GroupMmArgs& a, hipStream_t s) {
+  if (FLAT && a.k && a.k % 8 == 0 && a.n % 8 == 0 && a.rows >= 128 * (int64_t)a.groups && short_stride(a.ldx) &&
+      short_stride(a.ldw)) {
+    const uint64_t tiles = max_row_tiles(a, 256) * ((a.n + 255) / 256);
+    const uint64_t grid = tiles < 256 ? (tiles + kXcds - 1) / kXcds * kXcds : 256;  // one to a compute unit
+    group_mm_big<D, TRANS, O><<<dim3((uint32_t)grid), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
   constexpr int BM = 128, BN = 128;
   const uint64_t tiles = max_row_tiles(a, BM) * ((a.n + BN - 1) / BN);
   const uint64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
@@ -140,6 +432,14 @@ hipError_t run_mm(const GroupMmArgs& a, hipStream_t s) {
 
 template <typename D, bool FLAT, typename O>
 hipError_t run_wgrad(const GroupWgradArgs& a, hipStream_t s) {
+  if (FLAT && a.k % 8 == 0 && a.n % 8 == 0 && a.k >= 256 && a.n >= 256 && short_stride(a.ldx) &&
+      short_stride(a.ldy)) {
+    const uint64_t tiles = (uint64_t)a.groups * ((a.k + 255) / 256) * ((a.n + 255) / 256);
+    const uint64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
+    if (grid * 512 >> 32) return hipErrorInvalidConfiguration;
+    group_wgrad_big<D, O><<<dim3((uint32_t)grid), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
   constexpr int BM = 128, BN = 128;
   const uint64_t tiles = (uint64_t)a.groups * ((a.k + BM - 1) / BM) * ((a.n + BN - 1) / BN);
   const uint64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;

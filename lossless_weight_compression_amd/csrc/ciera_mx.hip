@@ -137,9 +137,10 @@ __global__ __launch_bounds__(256) void mx_mm_general(MxMmArgs a) {
   __shared__ i32x4 la[2][BM * CH];
   __shared__ i32x4 lb[2][BN * CH];
   GroupTile t;
-  if (!find_group_tile(a.offsets, a.groups, a.rows, BM, (a.n + BN - 1) / BN, blockIdx.x, &t)) return;
+  int tn;
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
-  const int mleft = t.count - t.m * BM, n0 = t.n * BN, nleft = a.n - n0;
+  const int mleft = t.count - t.m * BM, n0 = tn * BN, nleft = a.n - n0;
   const uint64_t cb = a.kp / 2, sb = a.kp / 32;  // bytes of a row's codes and scales
   const uint8_t* pa = a.a + row * cb;
   const uint8_t* psa = a.sa + row * sb;

@@ -49,63 +49,93 @@ __device__ __forceinline__ void group_range(const int32_t* off, int g, int rows,
   *count = max(b - a, 0);
 }
 
+// Sum of v over the lanes up to and including this one: within rows of 16 lanes,
+// then each row's total added to the rows after it.
 __device__ __forceinline__ int wave_inclusive_sum(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // from 1 lane below
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // 4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of the row below, to rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31, to rows 2 and 3
   return v;
 }
 
-// Where workgroup `bid` of a product grouped by expert works: tile m of group g
-// (rows [begin + m * bm, begin + count)) and column tile n.  The row tiles of all
-// groups are numbered in order; each wave adds them up by itself, 64 groups at a
-// time.  Workgroups are dealt to the dies in turn, so each die gets one
-// contiguous run of the tiles: its L2 then holds few groups' weights at a time.
-// The grid covers the largest possible number of tiles; false: nothing to do.
+// The row tiles (height BM) of all groups, numbered in order.  Each wave adds them
+// up by itself, 64 groups at a time; up to 64 groups stay in registers.
 struct GroupTile {
-  int g, m, n, begin, count;
+  int g, m, begin, count;  // tile m of group g: rows [begin + m * BM, begin + count)
 };
-__device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, int rows, int bm, int ntiles,
-                                                uint32_t bid, GroupTile* t) {
-  const int lane = threadIdx.x & 63;
-  uint32_t total = 0;
-  int begin = 0, count = 0, incl = 0;
-  for (int c = 0; c < groups; c += 64) {
+template <int BM>
+struct GroupTiles {
+  const int32_t* off;
+  int groups, rows;
+  int begin, count, incl;  // of this lane's group in the chunk of 64 last looked at
+  uint32_t total;
+
+  __device__ __forceinline__ void chunk(int c) {
+    const int g = c + (threadIdx.x & 63);
     begin = count = 0;
-    if (c + lane < groups) group_range(off, c + lane, rows, &begin, &count);
-    incl = wave_inclusive_sum((count + bm - 1) / bm);
-    total += __builtin_amdgcn_readlane(incl, 63);
+    if (g < groups) group_range(off, g, rows, &begin, &count);
+    incl = wave_inclusive_sum((count + BM - 1) / BM);
   }
-  const uint64_t all = (uint64_t)total * ntiles;
-  const uint64_t per = all / kXcds, rem = all % kXcds;
-  const uint32_t x = bid % kXcds, idx = bid / kXcds;
-  if (idx >= per + (x < rem ? 1 : 0)) return false;
-  const uint64_t tile = x * per + min((uint64_t)x, rem) + idx;
-  const uint32_t mt = __builtin_amdgcn_readfirstlane((uint32_t)(tile / ntiles));
-  t->n = __builtin_amdgcn_readfirstlane((int)(tile % ntiles));
-  uint32_t before = 0;
-  for (int c = 0; c < groups; c += 64) {
+  __device__ __forceinline__ void init(const int32_t* o, int g, int r) {
+    off = o;
+    groups = g;
+    rows = r;
+    total = 0;
+    for (int c = 0; c < groups; c += 64) {
+      chunk(c);
+      total += (uint32_t)__builtin_amdgcn_readlane(incl, 63);
+    }
+  }
+  // row tile mt < total
+  __device__ __forceinline__ GroupTile find(uint32_t mt) {
+    uint32_t before = 0;
+    int c = 0;
     if (groups > 64) {
-      begin = count = 0;
-      if (c + lane < groups) group_range(off, c + lane, rows, &begin, &count);
-      incl = wave_inclusive_sum((count + bm - 1) / bm);
+      for (;; c += 64) {
+        chunk(c);
+        const uint32_t t = (uint32_t)__builtin_amdgcn_readlane(incl, 63);
+        if (before + t > mt || c + 64 >= groups) break;
+        before += t;
+      }
     }
     const uint64_t hit = __ballot(before + (uint32_t)incl > mt);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      const int tiles = (count + bm - 1) / bm;
-      t->g = c + l;
-      t->begin = __builtin_amdgcn_readlane(begin, l);
-      t->count = __builtin_amdgcn_readlane(count, l);
-      t->m = mt - before - (__builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(tiles, l));
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
+    const int l = hit ? __builtin_ctzll(hit) : 0;
+    GroupTile t;
+    t.g = c + l;
+    t.begin = __builtin_amdgcn_readlane(begin, l);
+    t.count = __builtin_amdgcn_readlane(count, l);
+    t.m = (int)(mt - before) - (__builtin_amdgcn_readlane(incl, l) - (t.count + BM - 1) / BM);
+    return t;
   }
-  return false;
+};
+
+// Share of one of `all` equal tiles' lists: workgroups are dealt to the dies in
+// turn, so each die gets one contiguous run of the tiles and its L2 holds few
+// groups' operands at a time.  [*first, *first + *n) is die x's run.
+__device__ __forceinline__ void die_run(uint64_t all, uint32_t x, uint64_t* first, uint32_t* n) {
+  const uint64_t per = all / kXcds, rem = all % kXcds;
+  *first = x * per + (x < rem ? x : rem);
+  *n = (uint32_t)(per + (x < rem ? 1 : 0));
+}
+
+// Row tile and column tile of workgroup `bid`, one tile each; false: beyond the
+// last tile (the grid covers the largest possible number).
+template <int BM>
+__device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, int rows, int ntiles, uint32_t bid,
+                                                GroupTile* t, int* n) {
+  GroupTiles<BM> tiles;
+  tiles.init(off, groups, rows);
+  uint64_t first;
+  uint32_t count;
+  die_run((uint64_t)tiles.total * ntiles, bid % kXcds, &first, &count);
+  if (bid / kXcds >= count) return false;
+  const uint64_t tile = first + bid / kXcds;
+  *t = tiles.find((uint32_t)(tile / ntiles));
+  *n = (int)(tile % ntiles);
+  return true;
 }
 
 // One operand tile in LDS, in 16-byte chunks (8 two-byte values).  KC: the
@@ -113,14 +143,15 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
 // permuted by the row so that the 8 rows a fragment read touches at once lie in
 // different banks.  Else BK contraction steps of R contiguous values, read back
 // with the transposing LDS load, whose 16 lanes take 32 bytes of 4 steps each:
-// chunks are permuted in pairs by the step.
+// chunks are permuted in pairs by the step, so that the 32 bytes of the 8 steps
+// that 32 lanes read lie in different banks.
 template <bool KC, int R, int BK>
 struct LdsTile {
   static constexpr int kChunks = R * BK / 8;
   static constexpr int kPerRow = KC ? BK / 8 : R / 8;
   static __device__ __forceinline__ int swizzle(int line, int c) {
     if (KC) return BK == 32 ? c ^ ((line >> 2) & 3) : c ^ (line & 7);
-    return c ^ ((line & 7) << 1);
+    return c ^ (((line & 3) | ((line >> 1) & 4)) << 1);
   }
   // position of chunk c of a line (a row, or a contraction step)
   static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
@@ -160,19 +191,21 @@ __device__ __forceinline__ i32x4 load_chunk(const uint16_t* base, uint64_t ld, i
 }
 
 // Four consecutive outputs of one row, those left of `cols`.
-template <typename O>
-struct Out4;
 template <typename E>
 struct __attribute__((packed, aligned(sizeof(E)))) Pack4 {
   E v[4];
 };
 template <typename O>
+__device__ __forceinline__ void store_pack(O* at, f32x4 v) {
+  Pack4<O> p;
+#pragma unroll
+  for (int i = 0; i < 4; i++) p.v[i] = (O)v[i];
+  *reinterpret_cast<Pack4<O>*>(at) = p;
+}
+template <typename O>
 __device__ __forceinline__ void store4(O* row, int col, int cols, f32x4 v) {
   if (col + 4 <= cols) {
-    Pack4<O> p;
-#pragma unroll
-    for (int i = 0; i < 4; i++) p.v[i] = (O)v[i];
-    *reinterpret_cast<Pack4<O>*>(row + col) = p;
+    store_pack(row + col, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i++)
