@@ -69,9 +69,9 @@ __device__ __forceinline__ void general_tile(const uint16_t* a, uint64_t lda, in
     const int cur = s & 1;
     typename D::V fa[WM], fb[WN];
 #pragma unroll
-    for (int i = 0; i < WM; i++) fa[i] = __builtin_bit_cast(typename D::V, TA::fragment(la[cur], r0 + i * 16, 0));
+    for (int i = 0; i < WM; i++) fa[i] = __builtin_bit_cast(typename D::V, TA::fragment(la[cur], r0, i, 0));
 #pragma unroll
-    for (int j = 0; j < WN; j++) fb[j] = __builtin_bit_cast(typename D::V, TB::fragment(lb[cur], c0 + j * 16, 0));
+    for (int j = 0; j < WN; j++) fb[j] = __builtin_bit_cast(typename D::V, TB::fragment(lb[cur], c0, j, 0));
 #pragma unroll
     for (int i = 0; i < WM; i++)
 #pragma unroll
@@ -144,20 +144,23 @@ __device__ __forceinline__ void load_lds16(const char* base, uint32_t offset, i3
 // 128 x 64 of a tile each.  Rows start at multiples of 16 bytes and hold multiples of
 // 8 values along their contiguous side.  64 contraction steps at a time (a stage)
 // go from memory into one half of LDS, not passing registers, while the other half
-// is multiplied; the fragments of half a stage are read while those of the half
-// before are multiplied, across the one barrier of a stage too.  The first stage
-// of the next tile is on its way while this one's results are stored.
+// is multiplied; fragments are read a quarter stage ahead of their use, across the
+// one barrier of a stage too.  The first two stages of the next tile are on their way
+// before this one's results are stored, and do not wait for these stores.
 template <typename D, bool AKC, bool BKC, typename O>
 struct BigTiles {
   static constexpr int BM = 256, BN = 256, BK = 64, T = 512;
   typedef LdsTile<AKC, BM, BK> TA;
-  typedef LdsTile<BKC, BN, BK> TB;
+  typedef LdsTile<BKC, BN, BK, true> TB;
   typedef typename D::V V;
   static constexpr int NA = TA::kChunks / T, NB = TB::kChunks / T;
+  static_assert(NA == 4 && NB == 4, "a stage's loads are spread over the parts of a quarter");
   static constexpr int kStage = TA::kChunks + TB::kChunks;
+  static constexpr int kStores = sizeof(O) == 2 ? 16 : 32;  // a wave's store instructions for a whole tile
 
   i32x4* lds;
   int wave, lane, r0, c0;
+  bool ahead;                  // a whole tile's stores may still be under way
   // the tile being loaded
   const char *pa, *pb;         // its operands at the next stage
   uint64_t da, db;             // bytes from stage to stage
@@ -173,11 +176,13 @@ struct BigTiles {
     lane = threadIdx.x & 63;
     r0 = (wave >> 2) * 128;
     c0 = (wave & 3) * 64;
+    ahead = false;
   }
-  // a lane's chunk has a fixed place in LDS, so it fetches what the permutation puts
-  // there; rows and columns past the tile's end repeat the last one
-  __device__ __forceinline__ void aim(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
-                                      int klen) {
+  // A lane's chunk has a fixed place in LDS, so it fetches what the permutation puts
+  // there; rows and columns past the tile's end repeat the last one.  Asks for the
+  // first stage into half `buf` and the second, if there is one, into the other.
+  __device__ __forceinline__ void start(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
+                                        int klen, int buf) {
     pa = reinterpret_cast<const char*>(a);
     pb = reinterpret_cast<const char*>(b);
     da = AKC ? BK * 2 : BK * 2 * lda;
@@ -193,6 +198,8 @@ struct BigTiles {
       const int p = i * T + threadIdx.x, line = p / TB::kPerRow, c = TB::swizzle(line, p % TB::kPerRow) * 8;
       ob[i] = 2 * (BKC ? (uint32_t)min(line, bn - 1) * (uint32_t)ldb + c : line * (uint32_t)ldb + min(c, bn - 8));
     }
+    load(buf);
+    if (klen > BK) load(buf ^ 1);
   }
   // Part i of the next stage into half `buf`.  FULL: the stage has 64 steps; else
   // steps past the end arrive as zeros.
@@ -218,36 +225,69 @@ struct BigTiles {
     left -= BK;
   }
   __device__ __forceinline__ void load(int buf) {
-    for (int i = 0; i < NA; i++) left >= BK ? load_a<true>(buf, i) : load_a<false>(buf, i);
-    for (int i = 0; i < NB; i++) left >= BK ? load_b<true>(buf, i) : load_b<false>(buf, i);
+    if (left >= BK) {
+#pragma unroll
+      for (int i = 0; i < NA; i++) load_a<true>(buf, i);
+#pragma unroll
+      for (int i = 0; i < NB; i++) load_b<true>(buf, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NA; i++) load_a<false>(buf, i);
+#pragma unroll
+      for (int i = 0; i < NB; i++) load_b<false>(buf, i);
+    }
     loaded();
   }
   // fragment i of the upper or lower 64 rows (UP), or j of the 64 columns, at half H of a stage
   template <int H, int UP>
   __device__ __forceinline__ void read_a(int buf, int slot, int i) {
-    fa[slot][i] = __builtin_bit_cast(V, TA::fragment(lds + buf * kStage, r0 + UP * 64 + i * 16, H * 32));
+    fa[slot][i] = __builtin_bit_cast(V, TA::fragment(lds + buf * kStage, r0, UP * 4 + i, H * 32));
   }
   template <int H>
   __device__ __forceinline__ void read_b(int buf, int slot, int j) {
-    fb[slot][j] = __builtin_bit_cast(V, TB::fragment(lds + buf * kStage + TA::kChunks, c0 + j * 16, H * 32));
+    fb[slot][j] = __builtin_bit_cast(V, TB::fragment(lds + buf * kStage + TA::kChunks, c0, j, H * 32));
   }
   template <int UP>
   __device__ __forceinline__ void multiply(int sa, int sb, int i) {
 #pragma unroll
     for (int j = 0; j < 4; j++) acc[UP * 4 + i][j] = mfma(fb[sb][j], fa[sa][i], acc[UP * 4 + i][j]);
   }
-  // everything asked for has arrived, for every wave
+  // All but the last N of this wave's loads and stores are done (they end in order),
+  // as are its LDS reads; then the same for every wave.
+  template <int N>
   static __device__ __forceinline__ void arrive() {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0070);  // vmcnt N, lgkmcnt 0
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   }
-  // The first three quarters of the stage in half `buf`: 16 matrix instructions each
-  // and between them the reads of the next quarter's fragments, in a fixed order.
-  __device__ __forceinline__ void quarters(int buf) {
+  // One quarter's part of the loads of the stage after the next: 3 of the 4 in the last
+  // quarter, the others in the one after it.
+  template <bool FULL, bool FOURTH>
+  __device__ __forceinline__ void load_part(int buf, int i, bool more) {
+    if ((FULL || more) && (i == 3) == FOURTH) {
+      load_a<FULL>(buf, i);
+      load_b<FULL>(buf, i);
+      if (FOURTH) loaded();
+    }
+  }
+  // The last quarter of the stage in half `buf` ^ 1 (not if FIRST) and the first three
+  // of the one in `buf`: 16 matrix instructions each and between them, in a fixed
+  // order, the reads of the next quarter's fragments and the loads of the stage after
+  // these two, into the half that the first of them leaves.
+  template <bool FIRST, bool FULL>
+  __device__ __forceinline__ void stage(int buf, bool more) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
+      if (!FIRST) load_part<FULL, false>(buf ^ 1, i, more);
+      if (!FIRST) multiply<1>(1, 1, i);
+      read_a<0, 0>(buf, 0, i);
+      read_b<0>(buf, 0, i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      if (!FIRST) load_part<FULL, true>(buf ^ 1, i, more);
       multiply<0>(0, 0, i);
       read_a<0, 1>(buf, 1, i);
       __builtin_amdgcn_sched_barrier(0);
@@ -266,68 +306,72 @@ struct BigTiles {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // One stage, the one after the next asked for in its place, up to the first
-  // fragments of the next.
+  // What a wave without rows of the tile does of a stage.
   template <bool FULL>
-  __device__ __forceinline__ void stage(int buf, bool more) {
-    quarters(buf);
-    arrive();
+  __device__ __forceinline__ void idle(int buf, bool more) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (FULL || more) {
-        load_a<FULL>(buf, i);
-        load_b<FULL>(buf, i);
-      }
-      multiply<1>(1, 1, i);
-      read_a<0, 0>(buf ^ 1, 0, i);
-      read_b<0>(buf ^ 1, 0, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (FULL || more) loaded();
+    for (int i = 0; i < 4; i++) load_part<FULL, false>(buf ^ 1, i, more);
+    load_part<FULL, true>(buf ^ 1, 3, more);
   }
-  // All but the last quarter of the tile whose first stage is on its way into half
-  // `buf`, `klen` contraction steps in all; returns the half where another tile may begin.
-  __device__ __forceinline__ int stages(int klen, int buf) {
-    static_assert(NA == 4 && NB == 4, "a stage's loads are spread over four parts of a quarter");
+  template <bool WORK>
+  __device__ __forceinline__ void run(int klen, int* half) {
+    const int steps = max((klen + BK - 1) / BK, 1), full = klen / BK;
+    int buf = *half;
+    // stage 0 is here; the second stage's 8 loads and the last tile's stores may not be
+    if (!ahead) arrive<0>();
+    else if (steps > 1) arrive<kStores + NA + NB>();
+    else arrive<kStores>();
+    if (WORK) stage<true, true>(buf, false);
+    if (ahead) arrive<kStores>();
+    else arrive<0>();
+    int s = 0;
+    for (; s + 2 < full; s++) {
+      buf ^= 1;
+      if (WORK) stage<false, true>(buf, true);
+      else idle<true>(buf, true);
+      arrive<0>();
+    }
+    for (; s + 1 < steps; s++) {
+      buf ^= 1;
+      if (WORK) stage<false, false>(buf, s + 2 < steps);
+      else idle<false>(buf, s + 2 < steps);
+      arrive<0>();
+    }
+    *half = buf ^ 1;
+  }
+  // All but the last quarter of the tile that was started in half *half, of `om` rows
+  // and `klen` contraction steps; then both halves are free, *half the one for the next.
+  __device__ __forceinline__ void stages(int om, int klen, int* half) {
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
       for (int j = 0; j < 4; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-    const int steps = max((klen + BK - 1) / BK, 1), full = klen / BK;
-    arrive();
-    if (steps > 1) load(buf ^ 1);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      read_a<0, 0>(buf, 0, i);
-      read_b<0>(buf, 0, i);
-    }
-    int s = 0;
-    for (; s + 2 < full; s++) {
-      stage<true>(buf, true);
-      buf ^= 1;
-    }
-    for (; s + 1 < steps; s++) {
-      stage<false>(buf, s + 2 < steps);
-      buf ^= 1;
-    }
-    quarters(buf);
-    arrive();
-    return buf ^ 1;
+    if (r0 < om) run<true>(klen, half);
+    else run<false>(klen, half);
   }
-  __device__ __forceinline__ void last_quarter() {
+  // The last quarter, and the results.
+  __device__ __forceinline__ void finish(O* out, uint64_t ldo, int om, int on) {
+    ahead = om >= BM && on >= BN;
+    if (r0 >= om) return;
 #pragma unroll
     for (int i = 0; i < 4; i++) multiply<1>(1, 1, i);
-  }
-  __device__ __forceinline__ void store(O* out, uint64_t ldo, int om, int on) {
+    O* at = out + (uint64_t)(r0 + (lane & 15)) * ldo + c0 + (lane >> 4) * 8;
+    if (ahead) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        store8(at, acc[i][0], acc[i][1]);
+        store8(at + 32, acc[i][2], acc[i][3]);
+        at += 16 * ldo;
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const int m = r0 + i * 16 + (lane & 15);
-      if (m >= om) continue;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int n = c0 + j * 16 + (lane >> 4) * 4;
-        if (n < on) store_pack(out + (uint64_t)m * ldo + n, acc[i][j]);  // on is a multiple of 8
-      }
+      const bool row = r0 + i * 16 + (lane & 15) < om;
+      const int n = c0 + (lane >> 4) * 8;  // on is a multiple of 8
+      if (row && n < on) store8(at, acc[i][0], acc[i][1]);
+      if (row && n + 32 < on) store8(at + 32, acc[i][2], acc[i][3]);
+      at += 16 * ldo;
     }
   }
 };
@@ -347,58 +391,183 @@ __global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
   if (at >= many) return;
   BigTiles<D, true, TRANS, O> big;
   big.init(lds);
-  GroupTile t;
-  int n0;
-  auto aim = [&](uint64_t tile) {
-    t = tiles.find((uint32_t)(tile / nt));
-    n0 = (int)(tile % nt) * 256;
+  O* out;
+  int om, on, half = 0;
+  auto start = [&](uint64_t tile) {
+    const GroupTile t = tiles.find((uint32_t)(tile / nt));
+    const int n0 = (int)(tile % nt) * 256;
     const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256;
-    big.aim(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, t.count - t.m * 256,
-            static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw,
-            a.n - n0, a.k);
+    om = t.count - t.m * 256;
+    on = a.n - n0;
+    out = static_cast<O*>(a.out) + row * a.ldo + n0;
+    big.start(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, om,
+              static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, on,
+              a.k, half);
   };
-  aim(first + at);
-  big.load(0);
-  int buf = 0;
+  start(first + at);
   for (;;) {
-    O* out = static_cast<O*>(a.out) + ((uint64_t)t.begin + (uint64_t)t.m * 256) * a.ldo + n0;
-    const int om = t.count - t.m * 256, on = a.n - n0;
-    buf = big.stages(a.k, buf);
+    big.stages(om, a.k, &half);
+    O* done = out;
+    const int dm = om, dn = on;
     at += stride;
-    const bool more = at < many;
-    if (more) {
-      aim(first + at);
-      big.load(buf);
-    }
-    big.last_quarter();
-    big.store(out, a.ldo, om, on);
-    if (!more) return;
+    if (at < many) start(first + at);
+    big.finish(done, a.ldo, dm, dn);
+    if (at >= many) return;
   }
 }
+
+// The tiles of the groups' gradients, `per` to a group, shared out to the dies.  A tile
+// takes as long as its group has rows.  Up to 64 groups: each is cut into equal units
+// of consecutive tiles, 64 units at most, which are given out one by one, the most work
+// first, to the die with the least so far; a lane keeps one unit.  (64 groups whose
+// sizes spread by a factor of 10: the busiest die has 2 % more than its share, against
+// 33 % if each took 8 groups in order.)  More groups: each die takes one run of tiles of
+// equal work.
+struct GradTiles {
+  const int32_t* off;
+  int groups, rows;
+  uint32_t per, die;
+  int begin, count;           // of the lane's group
+  uint32_t unit, parts;       // tiles of a unit, units of a group
+  uint32_t own, before;       // the lane's unit: its tiles, if on this die, and those of the die before it
+  uint64_t first;             // more than 64 groups: the die's first tile
+  uint64_t many;              // tiles of the die
+
+  static __device__ __forceinline__ int cost(int c) { return (c + 63) / 64 + 4; }  // in stages; 4: start and stores
+  __device__ __forceinline__ int chunk(int c) {
+    const int g = c + (threadIdx.x & 63);
+    begin = count = 0;
+    if (g < groups) group_range(off, g, rows, &begin, &count);
+    return wave_inclusive_sum(g < groups ? cost(count) : 0);
+  }
+  // more than 64 groups: the first tile that begins at work w or later
+  __device__ __forceinline__ uint64_t tile_at(uint64_t w) {
+    uint64_t sum = 0;
+    for (int c = 0; c < groups; c += 64) {
+      const int incl = chunk(c);
+      const uint64_t hit = __ballot((sum + (uint32_t)incl) * per > w);
+      if (hit && c + __builtin_ctzll(hit) < groups) {
+        const int l = __builtin_ctzll(hit);
+        const uint32_t one = cost(__builtin_amdgcn_readlane(count, l));
+        const uint64_t pre = (sum + (uint32_t)__builtin_amdgcn_readlane(incl, l) - one) * per;
+        return (uint64_t)(c + l) * per + (w - pre + one - 1) / one;
+      }
+      sum += (uint32_t)__builtin_amdgcn_readlane(incl, 63);
+    }
+    return (uint64_t)groups * per;
+  }
+  __device__ __forceinline__ void share_runs() {
+    uint64_t total = 0;
+    for (int c = 0; c < groups; c += 64) total += (uint32_t)__builtin_amdgcn_readlane(chunk(c), 63);
+    const uint64_t part = total * per / kXcds;
+    first = tile_at(part * die);
+    many = (die + 1 == kXcds ? (uint64_t)groups * per : tile_at(part * (die + 1))) - first;
+  }
+  __device__ __forceinline__ void share_units() {
+    const uint32_t lane = threadIdx.x & 63;
+    parts = min(64u / (uint32_t)groups, per);
+    unit = (per + parts - 1) / parts;
+    const uint32_t g = lane / parts, part = lane % parts;
+    const uint32_t tiles = g < (uint32_t)groups && part * unit < per ? min(unit, per - part * unit) : 0;
+    begin = count = 0;
+    if (tiles) group_range(off, g, rows, &begin, &count);
+    const float work = tiles ? (float)cost(count) * (float)tiles : -1.f;
+    int rank = 0;
+    for (int l = 0; l < 64; l++) {
+      const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, work), l));
+      rank += w > work || (w == work && l < (int)lane);
+    }
+    // the first 8 units go to the dies in order
+    own = before = 0;
+    uint32_t dealt = 0;
+    const uint64_t mine = __ballot(rank == (int)die && tiles);
+    if (mine) dealt = __builtin_amdgcn_readlane(tiles, __builtin_ctzll(mine));
+    if (rank == (int)die) own = tiles;
+    float load = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute((rank & 63) * 4, __builtin_bit_cast(int, work)));
+    if (lane >= kXcds) load = 3e38f;  // lane x < 8: work of die x
+    for (int r = kXcds; r < 64; r++) {
+      const int l = __builtin_ctzll(__ballot(rank == r));
+      const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, work), l));
+      if (w < 0.f) break;
+      float m = load;
+      m = fminf(m, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), 0xb1, 0xf, 0xf, false)));   // lane ^ 1
+      m = fminf(m, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), 0x4e, 0xf, 0xf, false)));   // lane ^ 2
+      m = fminf(m, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, m), 0x141, 0xf, 0xf, false)));  // 7 - lane
+      const uint32_t d = __builtin_ctzll(__ballot(load == m));
+      if (lane == d) load += w;
+      if (d == die) {
+        if (lane == (uint32_t)l) {
+          own = tiles;
+          before = dealt;
+        }
+        dealt += __builtin_amdgcn_readlane(tiles, l);
+      }
+    }
+    many = dealt;
+  }
+  __device__ __forceinline__ void share(const GroupWgradArgs& a, uint32_t tiles, uint32_t d) {
+    off = a.offsets;
+    groups = a.groups;
+    rows = a.rows;
+    per = tiles;
+    die = d;
+    if (groups <= 64) share_units();
+    else share_runs();
+  }
+  // tile t < many of the die: its group, the tile in the group, the group's rows
+  __device__ __forceinline__ void find(uint64_t t, int* g, uint32_t* in, int* b, int* n) {
+    if (groups <= 64) {
+      const int l = __builtin_ctzll(__ballot((uint32_t)t - before < own));
+      *g = l / (int)parts;
+      *in = l % parts * unit + (uint32_t)t - (uint32_t)__builtin_amdgcn_readlane(before, l);
+      *b = __builtin_amdgcn_readlane(begin, l);
+      *n = __builtin_amdgcn_readlane(count, l);
+    } else {
+      *g = (int)((first + t) / per);
+      *in = (uint32_t)((first + t) % per);
+      group_range(off, *g, rows, b, n);
+      *b = __builtin_amdgcn_readfirstlane(*b);
+      *n = __builtin_amdgcn_readfirstlane(*n);
+    }
+  }
+};
 
 template <typename D, typename O>
 __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
   __shared__ i32x4 lds[kBigLds / 16];
-  const uint32_t mt = (a.k + 255) / 256, nt = (a.n + 255) / 256;
-  uint64_t first;
-  uint32_t many;
-  die_run((uint64_t)mt * nt * a.groups, blockIdx.x % kXcds, &first, &many);
-  if (blockIdx.x / kXcds >= many) return;
-  const uint64_t tile = first + blockIdx.x / kXcds;
-  const int g = tile / ((uint64_t)mt * nt);
-  const int m0 = (tile / nt % mt) * 256, n0 = (tile % nt) * 256;
-  int begin, count;
-  group_range(a.offsets, g, a.rows, &begin, &count);
-  begin = __builtin_amdgcn_readfirstlane(begin);
-  count = __builtin_amdgcn_readfirstlane(count);
+  const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds, me = blockIdx.x / kXcds;
+  GradTiles tiles;
+  tiles.share(a, (uint32_t)((a.k + 255) / 256) * nt, blockIdx.x % kXcds);
+  // the die's tiles are dealt to its workgroups forth and back: the first have most work
+  uint64_t round = 0, tile = me;
+  if (tile >= tiles.many) return;
   BigTiles<D, false, false, O> big;
   big.init(lds);
-  big.aim(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
-          static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, a.n - n0, count);
-  big.load(0);
-  big.stages(count, 0);
-  big.last_quarter();
-  big.store(static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo, a.k - m0, a.n - n0);
+  O* out;
+  int om, on, count, half = 0;
+  auto start = [&]() {
+    int g, begin;
+    uint32_t in;
+    tiles.find(tile, &g, &in, &begin, &count);
+    const int m0 = (int)(in / nt) * 256, n0 = (int)(in % nt) * 256;
+    om = a.k - m0;
+    on = a.n - n0;
+    out = static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0;
+    big.start(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, om,
+              static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, on, count, half);
+  };
+  start();
+  for (;;) {
+    big.stages(om, count, &half);
+    O* done = out;
+    const int dm = om, dn = on;
+    round++;
+    tile = round * stride + (round & 1 ? stride - 1 - me : me);
+    const bool more = tile < tiles.many;
+    if (more) start();
+    big.finish(done, a.ldo, dm, dn);
+    if (!more) return;
+  }
 }
 
 // Whether a tile's operands can be addressed with 32-bit byte offsets from their
@@ -435,8 +604,7 @@ hipError_t run_wgrad(const GroupWgradArgs& a, hipStream_t s) {
   if (FLAT && a.k % 8 == 0 && a.n % 8 == 0 && a.k >= 256 && a.n >= 256 && short_stride(a.ldx) &&
       short_stride(a.ldy)) {
     const uint64_t tiles = (uint64_t)a.groups * ((a.k + 255) / 256) * ((a.n + 255) / 256);
-    const uint64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-    if (grid * 512 >> 32) return hipErrorInvalidConfiguration;
+    const uint64_t grid = tiles < 256 ? (tiles + kXcds - 1) / kXcds * kXcds : 256;  // one to a compute unit
     group_wgrad_big<D, O><<<dim3((uint32_t)grid), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }

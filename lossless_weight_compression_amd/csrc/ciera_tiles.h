@@ -139,33 +139,42 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
 }
 
 // One operand tile in LDS, in 16-byte chunks (8 two-byte values).  KC: the
-// contraction is contiguous in memory; R rows of BK values, whose chunks are
-// permuted by the row so that the 8 rows a fragment read touches at once lie in
-// different banks.  Else BK contraction steps of R contiguous values, read back
-// with the transposing LDS load, whose 16 lanes take 32 bytes of 4 steps each:
-// chunks are permuted in pairs by the step, so that the 32 bytes of the 8 steps
-// that 32 lanes read lie in different banks.
-template <bool KC, int R, int BK>
+// contraction is contiguous in memory; R rows of BK values.  Else BK contraction
+// steps of R contiguous values, read back with the transposing LDS load, whose 16
+// lanes take 8 bytes each, of 4 steps.
+//
+// A fragment holds 16 rows.  PERM: not 16 consecutive ones; of every 32 rows the
+// even fragment takes the first 4 of every 8, the odd one the others, so that a lane,
+// which gets 4 consecutive rows of each as its results, has 8 consecutive ones (16
+// bytes) of the two.
+//
+// The chunks of a line are permuted by the line, so that what the lanes of one LDS
+// cycle read lies in different banks: 8 rows' chunks of the same steps, or 4 steps'
+// chunks of the same rows.
+template <bool KC, int R, int BK, bool PERM = false>
 struct LdsTile {
   static constexpr int kChunks = R * BK / 8;
   static constexpr int kPerRow = KC ? BK / 8 : R / 8;
   static __device__ __forceinline__ int swizzle(int line, int c) {
-    if (KC) return BK == 32 ? c ^ ((line >> 2) & 3) : c ^ (line & 7);
-    return c ^ (((line & 3) | ((line >> 1) & 4)) << 1);
+    if (KC && BK == 32) return c ^ ((line >> 2) & 3);
+    if (KC) return PERM ? c ^ ((line & 3) | ((line >> 1) & 4)) : c ^ (line & 7);
+    return PERM ? c ^ ((line & 3) << 2) : c ^ (((line & 3) | ((line >> 1) & 4)) << 1);
   }
   // position of chunk c of a line (a row, or a contraction step)
   static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
 
-  // the 8 contraction values k0 + 8 * (lane / 16) ... of row r0 + lane % 16
-  static __device__ __forceinline__ s16x8 fragment(const i32x4* lds, int r0, int k0) {
+  // Fragment f of the rows from r0 on, steps k0 + 8 * (lane / 16) ... of its row lane % 16.
+  static __device__ __forceinline__ s16x8 fragment(const i32x4* lds, int r0, int f, int k0) {
     const int lane = threadIdx.x & 63;
     if (KC) {
-      return __builtin_bit_cast(s16x8, lds[pos(r0 + (lane & 15), (k0 >> 3) + (lane >> 4))]);
+      const int r = PERM ? (f >> 1) * 32 + ((lane & 12) << 1) + (f & 1) * 4 + (lane & 3) : f * 16 + (lane & 15);
+      return __builtin_bit_cast(s16x8, lds[pos(r0 + r, (k0 >> 3) + (lane >> 4))]);
     } else {
       typedef __attribute__((address_space(3))) s16x4* lds_p;
       const int step = k0 + (lane >> 4) * 8 + ((lane & 15) >> 2);
-      const int c = (r0 >> 3) + ((lane & 3) >> 1);
-      const char* base = reinterpret_cast<const char*>(lds) + (lane & 1) * 8;
+      const int r = PERM ? (f >> 1) * 32 + (lane & 3) * 8 + (f & 1) * 4 : f * 16 + (lane & 3) * 4;
+      const char* base = reinterpret_cast<const char*>(lds) + (r & 4) * 2;
+      const int c = (r0 + r) >> 3;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(base + pos(step, c) * 16));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(base + pos(step + 4, c) * 16));
       return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -190,26 +199,44 @@ __device__ __forceinline__ i32x4 load_chunk(const uint16_t* base, uint64_t ld, i
   return v;
 }
 
-// Four consecutive outputs of one row, those left of `cols`.
-template <typename E>
-struct __attribute__((packed, aligned(sizeof(E)))) Pack4 {
-  E v[4];
+// Consecutive outputs of one row, at any element.
+template <typename E, int N>
+struct __attribute__((packed, aligned(sizeof(E)))) Pack {
+  E v[N];
 };
-template <typename O>
-__device__ __forceinline__ void store_pack(O* at, f32x4 v) {
-  Pack4<O> p;
-#pragma unroll
-  for (int i = 0; i < 4; i++) p.v[i] = (O)v[i];
-  *reinterpret_cast<Pack4<O>*>(at) = p;
-}
 template <typename O>
 __device__ __forceinline__ void store4(O* row, int col, int cols, f32x4 v) {
   if (col + 4 <= cols) {
-    store_pack(row + col, v);
+    Pack<O, 4> p;
+#pragma unroll
+    for (int i = 0; i < 4; i++) p.v[i] = (O)v[i];
+    *reinterpret_cast<Pack<O, 4>*>(row + col) = p;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; i++)
       if (col + i < cols) row[col + i] = (O)v[i];
+  }
+}
+// 8 outputs, 4 each of two fragments: one store in two-byte types, two in fp32.
+template <typename O>
+__device__ __forceinline__ void store8(O* at, f32x4 lo, f32x4 hi) {
+  if (sizeof(O) == 2) {
+    Pack<O, 8> p;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      p.v[i] = (O)lo[i];
+      p.v[4 + i] = (O)hi[i];
+    }
+    *reinterpret_cast<Pack<O, 8>*>(at) = p;
+  } else {
+    Pack<O, 4> p, q;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      p.v[i] = (O)lo[i];
+      q.v[i] = (O)hi[i];
+    }
+    *reinterpret_cast<Pack<O, 4>*>(at) = p;
+    *reinterpret_cast<Pack<O, 4>*>(at + 4) = q;
   }
 }
 
