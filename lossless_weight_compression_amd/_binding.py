@@ -148,6 +148,12 @@ def _load() -> ctypes.CDLL:
 
 _lib = _load()
 
+import torch  # noqa: E402  (after _load, which says why it comes first)
+
+# handle of a device's current stream, without the Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_TORCH_CODES = {torch.bfloat16: CIERA_BF16, torch.float32: CIERA_FP32, torch.float16: CIERA_FP16}
+
 
 def _check(code: int, where: str) -> None:
     if code != CIERA_OK:
@@ -192,8 +198,7 @@ def _u8(t, what: str, min_numel: int) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -391,30 +396,31 @@ def ciera_decode_launch_bounded(batch: Batch, max_workgroups: int, stream=None) 
 # ------------------------------------------- expert products and 4-bit weights
 
 def _on_current_device(t, what: str) -> None:
-    import torch
     if t.device.type != "cuda":
         raise ValueError(f"{what}: on {t.device}, not on a GPU")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def matrix_item(t, what: str = "matrix") -> Matrix:
     """A 2-D or 3-D torch tensor of bf16, fp16 or fp32 on the current GPU, with
     any strides but the last, which must be 1 (a Matrix is passed through)."""
-    if isinstance(t, Matrix):
+    if type(t) is Matrix:
         return t
-    import torch
-    codes = {torch.bfloat16: CIERA_BF16, torch.float32: CIERA_FP32, torch.float16: CIERA_FP16}
-    if t.dtype not in codes:
+    code = _TORCH_CODES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what}: dtype {t.dtype}, expected bfloat16, float16 or float32")
-    if t.dim() not in (2, 3):
-        raise ValueError(f"{what}: {t.dim()} dimensions, expected 2 or 3")
-    if t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what}: values of a row are not adjacent (shape {tuple(t.shape)}, stride {t.stride()})")
-    _on_current_device(t, what)
-    groups, rs = (t.shape[0], t.stride(1)) if t.dim() == 3 else (1, t.stride(0))
-    return Matrix(t.data_ptr(), codes[t.dtype], groups, t.shape[-2], t.shape[-1], rs,
-                  t.stride(0) if t.dim() == 3 else 0)
+    shape, stride = t.shape, t.stride()
+    n = len(shape)
+    if n != 2 and n != 3:
+        raise ValueError(f"{what}: {n} dimensions, expected 2 or 3")
+    if stride[-1] != 1 and shape[-1] > 1 and t.numel():
+        raise ValueError(f"{what}: values of a row are not adjacent (shape {tuple(shape)}, stride {stride})")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _on_current_device(t, what)
+    if n == 2:
+        return Matrix(t.data_ptr(), code, 1, shape[0], shape[1], stride[0], 0)
+    return Matrix(t.data_ptr(), code, shape[0], shape[1], shape[2], stride[1], stride[0])
 
 
 def mx_item(codes, scales, groups: int, rows: int, cols: int) -> Mx:
@@ -437,10 +443,11 @@ def _mx(q) -> Mx:
 def _offsets(offsets, groups: int) -> Optional[int]:
     if offsets is None or isinstance(offsets, int):
         return offsets
-    import torch
-    p = _ptr(offsets, "offsets", torch.int32, groups + 1)
-    _on_current_device(offsets, "offsets")
-    return p
+    if not (offsets.is_cuda and offsets.dtype is torch.int32 and offsets.numel() == groups + 1
+            and offsets.is_contiguous() and offsets.get_device() == torch.cuda.current_device()):
+        _ptr(offsets, "offsets", torch.int32, groups + 1)
+        _on_current_device(offsets, "offsets")
+    return offsets.data_ptr()
 
 
 def ciera_mx_sizes(groups: int, rows: int, cols: int) -> Tuple[int, int]:

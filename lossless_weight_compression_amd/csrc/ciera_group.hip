@@ -570,6 +570,209 @@ __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
   }
 }
 
+// ------------------------------------------------------- few rows to a group
+// What counts then is how fast the weights are read, each once.  A workgroup takes 16
+// rows of a group (or 16 * MF) and some columns; its 8 waves take the contraction steps in turn, so
+// that all of them read at once, from memory into registers, the next step's values
+// under way while this one's are multiplied; their sums are joined through LDS in the
+// order of the waves.
+constexpr int kThinWaves = 8;
+
+// The joined sums: cols columns of 16 rows, of which `rows` are stored.  part: each
+// wave's [16][kLd] floats.
+template <typename O, int COLS>
+struct ThinJoin {
+  static constexpr int kLd = COLS + 4;
+  static __device__ __forceinline__ void store(const float* part, O* out, uint64_t ldo, int rows, int cols) {
+    for (int p = threadIdx.x; p < 16 * COLS / 4; p += kThinWaves * 64) {
+      const int m = p / (COLS / 4), c = p % (COLS / 4) * 4;
+      if (m >= rows || c >= cols) continue;
+      f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kThinWaves; w++) v += *reinterpret_cast<const f32x4*>(part + (w * 16 + m) * kLd + c);
+      store4(out + (uint64_t)m * ldo, c, cols, v);
+    }
+  }
+};
+
+// W [K, N]: a lane holds 8 contraction steps of VEC columns (two-byte values, 2 * VEC
+// bytes of 8 rows) and turns them around in registers; 16 lanes cover 16 * VEC columns.
+template <typename D, typename O, int MF, int VEC>
+__global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
+  constexpr int BN = 16 * VEC, W = VEC / 2;  // words of a row's columns in a lane
+  typedef ThinJoin<O, BN> Join;
+  __shared__ __attribute__((aligned(16))) float part[kThinWaves * 16 * Join::kLd];
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16 * MF>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16 * MF;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16 * MF;
+  const int c = (lane & 15) * VEC, q = lane >> 4;
+  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + n0 + c;
+  const uint16_t* x[MF];
+#pragma unroll
+  for (int f = 0; f < MF; f++)
+    x[f] = static_cast<const uint16_t*>(a.x) + (row + min(f * 16 + (lane & 15), rows - 1)) * a.ldx;
+
+  struct Step {
+    uint32_t w[8][W];
+    i32x4 x[MF];
+  };
+  auto load = [&](Step& s, int k0) {
+    const int k = k0 + q * 8;
+    if (k0 + 32 <= a.k && left >= BN) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const uint16_t* p = w + (uint64_t)(k + j) * a.ldw;
+        if constexpr (VEC == 8) {
+          const i32x4 v = load16(p);
+#pragma unroll
+          for (int i = 0; i < 4; i++) s.w[j][i] = v[i];
+        } else {
+          const Pack<uint32_t, 2> v = *reinterpret_cast<const Pack<uint32_t, 2>*>(p);
+          s.w[j][0] = v.v[0];
+          s.w[j][1] = v.v[1];
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < MF; f++) s.x[f] = load16(x[f] + k);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++)
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+          uint32_t v = 0;
+          if (k + j < a.k) {
+            const uint16_t* p = w + (uint64_t)(k + j) * a.ldw + 2 * i;
+            if (c + 2 * i < left) v = p[0];
+            if (c + 2 * i + 1 < left) v |= (uint32_t)p[1] << 16;
+          }
+          s.w[j][i] = v;
+        }
+#pragma unroll
+      for (int f = 0; f < MF; f++) s.x[f] = load_chunk<false>(x[f], 0, 0, 1, k, a.k);
+    }
+  };
+  f32x4 acc[MF][VEC];
+#pragma unroll
+  for (int f = 0; f < MF; f++)
+#pragma unroll
+    for (int j = 0; j < VEC; j++) acc[f][j] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](const Step& s) {
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+      i32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        v[i] = __builtin_amdgcn_perm(s.w[2 * i + 1][j / 2], s.w[2 * i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+      for (int f = 0; f < MF; f++)
+        acc[f][j] = mfma(__builtin_bit_cast(typename D::V, v), __builtin_bit_cast(typename D::V, s.x[f]), acc[f][j]);
+    }
+  };
+  constexpr int STEP = 32 * kThinWaves;
+  int k0 = wave * 32;
+  Step s[2];
+  if (k0 < a.k) load(s[0], k0);
+  while (k0 < a.k) {
+    if (k0 + STEP < a.k) load(s[1], k0 + STEP);
+    multiply(s[0]);
+    k0 += STEP;
+    if (k0 >= a.k) break;
+    if (k0 + STEP < a.k) load(s[0], k0 + STEP);
+    multiply(s[1]);
+    k0 += STEP;
+  }
+  // results of a lane: row lane % 16, columns (lane / 16 * 4 + i) * VEC + j
+  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
+#pragma unroll
+  for (int f = 0; f < MF; f++) {
+    float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4 * VEC;
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4)
+        *reinterpret_cast<f32x4*>(mine + i * VEC + j) =
+            f32x4{acc[f][j][i], acc[f][j + 1][i], acc[f][j + 2][i], acc[f][j + 3][i]};
+    __syncthreads();
+    Join::store(part, out + (uint64_t)f * 16 * a.ldo, a.ldo, rows - f * 16, left);
+    if (f + 1 < MF) __syncthreads();
+  }
+}
+
+// W [N, K]: a lane reads 64 bytes of one row of W (4 loads, so that 4 lanes cover 256
+// bytes of a row), NF rows of 16 to a wave.
+template <typename D, typename O, int NF>
+__global__ __launch_bounds__(512) void group_mm_thin_t(GroupMmArgs a) {
+  constexpr int BN = 16 * NF;
+  typedef ThinJoin<O, BN> Join;
+  __shared__ __attribute__((aligned(16))) float part[kThinWaves * 16 * Join::kLd];
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
+  const int q = lane >> 4;
+  const uint16_t* w[NF];
+#pragma unroll
+  for (int f = 0; f < NF; f++)
+    w[f] = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw +
+           (uint64_t)(n0 + min(f * 16 + (lane & 15), left - 1)) * a.ldw;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx;
+  struct Step {
+    i32x4 w[NF][4], x[4];
+  };
+  auto load = [&](Step& s, int k0) {
+    const int k = k0 + q * 32;
+    if (k0 + 128 <= a.k) {
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+#pragma unroll
+        for (int f = 0; f < NF; f++) s.w[f][u] = load16(w[f] + k + u * 8);
+        s.x[u] = load16(x + k + u * 8);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; u++) {
+#pragma unroll
+        for (int f = 0; f < NF; f++) s.w[f][u] = load_chunk<false>(w[f], 0, 0, 1, k + u * 8, a.k);
+        s.x[u] = load_chunk<false>(x, 0, 0, 1, k + u * 8, a.k);
+      }
+    }
+  };
+  f32x4 acc[NF];
+#pragma unroll
+  for (int j = 0; j < NF; j++) acc[j] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](const Step& s) {
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+#pragma unroll
+      for (int j = 0; j < NF; j++)
+        acc[j] = mfma(__builtin_bit_cast(typename D::V, s.w[j][u]), __builtin_bit_cast(typename D::V, s.x[u]), acc[j]);
+  };
+  constexpr int STEP = 128 * kThinWaves;
+  int k0 = wave * 128;
+  Step s[2];
+  if (k0 < a.k) load(s[0], k0);
+  while (k0 < a.k) {
+    if (k0 + STEP < a.k) load(s[1], k0 + STEP);
+    multiply(s[0]);
+    k0 += STEP;
+    if (k0 >= a.k) break;
+    if (k0 + STEP < a.k) load(s[0], k0 + STEP);
+    multiply(s[1]);
+    k0 += STEP;
+  }
+  // results of a lane: row lane % 16, columns j * 16 + lane / 16 * 4 + i
+  float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4;
+#pragma unroll
+  for (int j = 0; j < NF; j++) *reinterpret_cast<f32x4*>(mine + j * 16) = acc[j];
+  __syncthreads();
+  Join::store(part, static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, rows, left);
+}
+
 // Whether a tile's operands can be addressed with 32-bit byte offsets from their
 // first element: 256 rows, or 64 contraction steps, of `ld` values.
 bool short_stride(uint64_t ld) { return ld < (1u << 22); }
@@ -582,8 +785,42 @@ uint64_t max_row_tiles(const GroupMmArgs& a, uint64_t bm) {
   return full + (groups < (uint64_t)a.rows ? groups : (uint64_t)a.rows);
 }
 
+hipError_t tile_grid(uint64_t tiles, uint32_t threads, dim3* grid) {
+  const uint64_t g = (tiles + kXcds - 1) / kXcds * kXcds;
+  if (g * threads >> 32) return hipErrorInvalidConfiguration;
+  *grid = dim3((uint32_t)g);
+  return hipSuccess;
+}
+
+// Rows of 16 * MF to a workgroup; narrow columns where wide ones would not make enough
+// workgroups for the card.
+template <typename D, bool TRANS, typename O, int MF>
+hipError_t run_thin(const GroupMmArgs& a, hipStream_t s) {
+  constexpr int WIDE = TRANS ? 64 : 128, NARROW = TRANS ? 16 : 64;
+  const uint64_t mt = max_row_tiles(a, 16 * MF);
+  const bool wide = mt * ((a.n + WIDE - 1) / WIDE) >= 1024;
+  const int bn = wide ? WIDE : NARROW;
+  dim3 grid;
+  if (hipError_t e = tile_grid(mt * ((a.n + bn - 1) / bn), 512, &grid)) return e;
+  if constexpr (TRANS) {
+    if (wide) group_mm_thin_t<D, O, 4><<<grid, dim3(512), 0, s>>>(a);
+    else group_mm_thin_t<D, O, 1><<<grid, dim3(512), 0, s>>>(a);
+  } else {
+    if (wide) group_mm_thin<D, O, MF, 8><<<grid, dim3(512), 0, s>>>(a);
+    else group_mm_thin<D, O, MF, 4><<<grid, dim3(512), 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
 template <typename D, bool TRANS, bool FLAT, typename O>
 hipError_t run_mm(const GroupMmArgs& a, hipStream_t s) {
+  // Few rows to a group on average (64 experts of 2048 x 1024, bf16; the 128 x 128 kernel
+  // in brackets): [K, N] 8 rows 43 us (56), 16 rows 51 (61), 32 rows in pairs of 16 56
+  // (72), 64 rows 81 (73); [N, K] 8 rows 53 (62), 16 rows 66 (64), pairs lose throughout.
+  if (a.rows <= (TRANS ? 12 : 16) * (int64_t)a.groups) return run_thin<D, TRANS, O, 1>(a, s);
+  if constexpr (!TRANS) {
+    if (a.rows <= 32 * (int64_t)a.groups) return run_thin<D, TRANS, O, 2>(a, s);
+  }
   if (FLAT && a.k && a.k % 8 == 0 && a.n % 8 == 0 && a.rows >= 128 * (int64_t)a.groups && short_stride(a.ldx) &&
       short_stride(a.ldw)) {
     const uint64_t tiles = max_row_tiles(a, 256) * ((a.n + 255) / 256);
@@ -592,10 +829,9 @@ hipError_t run_mm(const GroupMmArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   constexpr int BM = 128, BN = 128;
-  const uint64_t tiles = max_row_tiles(a, BM) * ((a.n + BN - 1) / BN);
-  const uint64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid * 256 >> 32) return hipErrorInvalidConfiguration;
-  group_mm_general<D, TRANS, FLAT, O, BM, BN><<<dim3((uint32_t)grid), dim3(256), 0, s>>>(a);
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a, BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
+  group_mm_general<D, TRANS, FLAT, O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -609,10 +845,9 @@ hipError_t run_wgrad(const GroupWgradArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   constexpr int BM = 128, BN = 128;
-  const uint64_t tiles = (uint64_t)a.groups * ((a.k + BM - 1) / BM) * ((a.n + BN - 1) / BN);
-  const uint64_t grid = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (grid * 256 >> 32) return hipErrorInvalidConfiguration;
-  group_wgrad_general<D, FLAT, O, BM, BN><<<dim3((uint32_t)grid), dim3(256), 0, s>>>(a);
+  dim3 grid;
+  if (hipError_t e = tile_grid((uint64_t)a.groups * ((a.k + BM - 1) / BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
+  group_wgrad_general<D, FLAT, O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -111,7 +111,7 @@ ciera_status_t ciera_mx_quantize(const ciera_matrix_t* x, uint32_t axis, const c
   if (overlap(rx, rc) || overlap(rx, rs) || overlap(rc, rs)) return CIERA_ERR_INVALID_ARG;
   const MxQuantArgs a = {x->data, q->codes, q->scales, x->row_stride, x->group_stride,
                          (int32_t)x->groups, (int32_t)x->rows, (int32_t)x->cols};
-  return launched("4-bit quantisation launch", launch_mx_quantize(x->dtype, axis, flat(x), a, hip_stream(stream)));
+  return launched("4-bit quantisation launch", launch_mx_quantize(x->dtype, axis, a, hip_stream(stream)));
 }
 
 ciera_status_t ciera_mx_dequantize(const ciera_mx_t* q, const ciera_matrix_t* out, void* stream) {
@@ -124,7 +124,7 @@ ciera_status_t ciera_mx_dequantize(const ciera_mx_t* q, const ciera_matrix_t* ou
   if (overlap(ro, rc) || overlap(ro, rs)) return CIERA_ERR_INVALID_ARG;
   const MxDequantArgs a = {q->codes, q->scales, out->data, out->row_stride, out->group_stride,
                            (int32_t)out->groups, (int32_t)out->rows, (int32_t)out->cols};
-  return launched("4-bit dequantisation launch", launch_mx_dequantize(out->dtype, flat(out), a, hip_stream(stream)));
+  return launched("4-bit dequantisation launch", launch_mx_dequantize(out->dtype, a, hip_stream(stream)));
 }
 
 ciera_status_t ciera_mx_mm(const ciera_mx_t* a, const ciera_mx_t* b, const int32_t* offsets,

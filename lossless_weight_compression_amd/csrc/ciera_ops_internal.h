@@ -67,7 +67,7 @@ struct MxDequantArgs {
 hipError_t launch_group_mm(int dtype, bool out_f32, bool transpose_w, bool flat, const GroupMmArgs& a, hipStream_t s);
 hipError_t launch_group_wgrad(int dtype, bool out_f32, bool flat, const GroupWgradArgs& a, hipStream_t s);
 hipError_t launch_mx_mm(int out_dtype, const MxMmArgs& a, hipStream_t s);
-hipError_t launch_mx_quantize(int dtype, int axis, bool flat, const MxQuantArgs& a, hipStream_t s);
-hipError_t launch_mx_dequantize(int dtype, bool flat, const MxDequantArgs& a, hipStream_t s);
+hipError_t launch_mx_quantize(int dtype, int axis, const MxQuantArgs& a, hipStream_t s);
+hipError_t launch_mx_dequantize(int dtype, const MxDequantArgs& a, hipStream_t s);
 
 }  // namespace ciera

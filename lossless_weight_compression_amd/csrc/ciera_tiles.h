@@ -201,7 +201,7 @@ __device__ __forceinline__ i32x4 load_chunk(const uint16_t* base, uint64_t ld, i
 
 // Consecutive outputs of one row, at any element.
 template <typename E, int N>
-struct __attribute__((packed, aligned(sizeof(E)))) Pack {
+struct __attribute__((packed, aligned(2))) Pack {
   E v[N];
 };
 template <typename O>
