@@ -1,6 +1,7 @@
 // Products grouped by expert: y = x W_g on the rows of every group, and the
 // gradient of the weights, x_g^T dy_g.
 #include "ciera.h"
+#include "ciera_big.h"
 #include "ciera_ops_internal.h"
 #include "ciera_tiles.h"
 
@@ -69,9 +70,9 @@ __device__ __forceinline__ void general_tile(const uint16_t* a, uint64_t lda, in
     const int cur = s & 1;
     typename D::V fa[WM], fb[WN];
 #pragma unroll
-    for (int i = 0; i < WM; i++) fa[i] = __builtin_bit_cast(typename D::V, TA::fragment(la[cur], r0, i, 0));
+    for (int i = 0; i < WM; i++) fa[i] = __builtin_bit_cast(typename D::V, TA::fragment(la[cur], r0 + i * 16));
 #pragma unroll
-    for (int j = 0; j < WN; j++) fb[j] = __builtin_bit_cast(typename D::V, TB::fragment(lb[cur], c0, j, 0));
+    for (int j = 0; j < WN; j++) fb[j] = __builtin_bit_cast(typename D::V, TB::fragment(lb[cur], c0 + j * 16));
 #pragma unroll
     for (int i = 0; i < WM; i++)
 #pragma unroll
@@ -122,265 +123,9 @@ __global__ __launch_bounds__(256) void group_wgrad_general(GroupWgradArgs a) {
                                                  a.n - n0);
 }
 
-// 16 zero bytes: what is loaded in place of contraction steps past the end.
-__device__ const i32x4 kZeros = {0, 0, 0, 0};
-
-// 16 bytes per lane from memory straight into LDS, lane l's at `lds` + l.  Written in
-// assembly because the compiler, where it sees such a load, waits for it before the
-// next LDS read of any address; the kernels here wait themselves (arrive).  It has no
-// result register; the clobber keeps LDS reads from moving across it.  m0, which holds
-// the address in LDS, is the compiler's scratch register too, set anew at each use.
-__device__ __forceinline__ void load_lds16(const void* p, i32x4* lds) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(p) : "memory");
-}
-__device__ __forceinline__ void load_lds16(const char* base, uint32_t offset, i32x4* lds) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(offset), "s"(base)
-               : "memory");
-}
-
-// 256 x 256 tiles of C = A B, one after another by the same workgroup: 8 waves of
-// 128 x 64 of a tile each.  Rows start at multiples of 16 bytes and hold multiples of
-// 8 values along their contiguous side.  64 contraction steps at a time (a stage)
-// go from memory into one half of LDS, not passing registers, while the other half
-// is multiplied; fragments are read a quarter stage ahead of their use, across the
-// one barrier of a stage too.  The first two stages of the next tile are on their way
-// before this one's results are stored, and do not wait for these stores.
-template <typename D, bool AKC, bool BKC, typename O>
-struct BigTiles {
-  static constexpr int BM = 256, BN = 256, BK = 64, T = 512;
-  typedef LdsTile<AKC, BM, BK> TA;
-  typedef LdsTile<BKC, BN, BK, true> TB;
-  typedef typename D::V V;
-  static constexpr int NA = TA::kChunks / T, NB = TB::kChunks / T;
-  static_assert(NA == 4 && NB == 4, "a stage's loads are spread over the parts of a quarter");
-  static constexpr int kStage = TA::kChunks + TB::kChunks;
-  static constexpr int kStores = sizeof(O) == 2 ? 16 : 32;  // a wave's store instructions for a whole tile
-
-  i32x4* lds;
-  int wave, lane, r0, c0;
-  bool ahead;                  // a whole tile's stores may still be under way
-  // the tile being loaded
-  const char *pa, *pb;         // its operands at the next stage
-  uint64_t da, db;             // bytes from stage to stage
-  uint32_t oa[NA], ob[NB];     // this lane's chunks of a stage, bytes from there
-  int left;                    // contraction steps not loaded yet
-  // the tile being multiplied
-  f32x4 acc[8][4];
-  V fa[2][4], fb[2][4];
-
-  __device__ __forceinline__ void init(i32x4* l) {
-    lds = l;
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    lane = threadIdx.x & 63;
-    r0 = (wave >> 2) * 128;
-    c0 = (wave & 3) * 64;
-    ahead = false;
-  }
-  // A lane's chunk has a fixed place in LDS, so it fetches what the permutation puts
-  // there; rows and columns past the tile's end repeat the last one.  Asks for the
-  // first stage into half `buf` and the second, if there is one, into the other.
-  __device__ __forceinline__ void start(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
-                                        int klen, int buf) {
-    pa = reinterpret_cast<const char*>(a);
-    pb = reinterpret_cast<const char*>(b);
-    da = AKC ? BK * 2 : BK * 2 * lda;
-    db = BKC ? BK * 2 : BK * 2 * ldb;
-    left = klen;
-#pragma unroll
-    for (int i = 0; i < NA; i++) {
-      const int p = i * T + threadIdx.x, line = p / TA::kPerRow, c = TA::swizzle(line, p % TA::kPerRow) * 8;
-      oa[i] = 2 * (AKC ? (uint32_t)min(line, am - 1) * (uint32_t)lda + c : line * (uint32_t)lda + min(c, am - 8));
-    }
-#pragma unroll
-    for (int i = 0; i < NB; i++) {
-      const int p = i * T + threadIdx.x, line = p / TB::kPerRow, c = TB::swizzle(line, p % TB::kPerRow) * 8;
-      ob[i] = 2 * (BKC ? (uint32_t)min(line, bn - 1) * (uint32_t)ldb + c : line * (uint32_t)ldb + min(c, bn - 8));
-    }
-    load(buf);
-    if (klen > BK) load(buf ^ 1);
-  }
-  // Part i of the next stage into half `buf`.  FULL: the stage has 64 steps; else
-  // steps past the end arrive as zeros.
-  template <bool FULL>
-  __device__ __forceinline__ void load_a(int buf, int i) {
-    i32x4* at = lds + buf * kStage + wave * 64 + i * T;
-    if (FULL) return load_lds16(pa, oa[i], at);
-    const int p = i * T + threadIdx.x, line = p / TA::kPerRow;
-    const int k = AKC ? TA::swizzle(line, p % TA::kPerRow) * 8 : line;
-    load_lds16(k < left ? pa + oa[i] : reinterpret_cast<const char*>(&kZeros), at);
-  }
-  template <bool FULL>
-  __device__ __forceinline__ void load_b(int buf, int i) {
-    i32x4* at = lds + buf * kStage + TA::kChunks + wave * 64 + i * T;
-    if (FULL) return load_lds16(pb, ob[i], at);
-    const int p = i * T + threadIdx.x, line = p / TB::kPerRow;
-    const int k = BKC ? TB::swizzle(line, p % TB::kPerRow) * 8 : line;
-    load_lds16(k < left ? pb + ob[i] : reinterpret_cast<const char*>(&kZeros), at);
-  }
-  __device__ __forceinline__ void loaded() {
-    pa += da;
-    pb += db;
-    left -= BK;
-  }
-  __device__ __forceinline__ void load(int buf) {
-    if (left >= BK) {
-#pragma unroll
-      for (int i = 0; i < NA; i++) load_a<true>(buf, i);
-#pragma unroll
-      for (int i = 0; i < NB; i++) load_b<true>(buf, i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NA; i++) load_a<false>(buf, i);
-#pragma unroll
-      for (int i = 0; i < NB; i++) load_b<false>(buf, i);
-    }
-    loaded();
-  }
-  // fragment i of the upper or lower 64 rows (UP), or j of the 64 columns, at half H of a stage
-  template <int H, int UP>
-  __device__ __forceinline__ void read_a(int buf, int slot, int i) {
-    fa[slot][i] = __builtin_bit_cast(V, TA::fragment(lds + buf * kStage, r0, UP * 4 + i, H * 32));
-  }
-  template <int H>
-  __device__ __forceinline__ void read_b(int buf, int slot, int j) {
-    fb[slot][j] = __builtin_bit_cast(V, TB::fragment(lds + buf * kStage + TA::kChunks, c0, j, H * 32));
-  }
-  template <int UP>
-  __device__ __forceinline__ void multiply(int sa, int sb, int i) {
-#pragma unroll
-    for (int j = 0; j < 4; j++) acc[UP * 4 + i][j] = mfma(fb[sb][j], fa[sa][i], acc[UP * 4 + i][j]);
-  }
-  // All but the last N of this wave's loads and stores are done (they end in order),
-  // as are its LDS reads; then the same for every wave.
-  template <int N>
-  static __device__ __forceinline__ void arrive() {
-    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0070);  // vmcnt N, lgkmcnt 0
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  // One quarter's part of the loads of the stage after the next: 3 of the 4 in the last
-  // quarter, the others in the one after it.
-  template <bool FULL, bool FOURTH>
-  __device__ __forceinline__ void load_part(int buf, int i, bool more) {
-    if ((FULL || more) && (i == 3) == FOURTH) {
-      load_a<FULL>(buf, i);
-      load_b<FULL>(buf, i);
-      if (FOURTH) loaded();
-    }
-  }
-  // The last quarter of the stage in half `buf` ^ 1 (not if FIRST) and the first three
-  // of the one in `buf`: 16 matrix instructions each and between them, in a fixed
-  // order, the reads of the next quarter's fragments and the loads of the stage after
-  // these two, into the half that the first of them leaves.
-  template <bool FIRST, bool FULL>
-  __device__ __forceinline__ void stage(int buf, bool more) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (!FIRST) load_part<FULL, false>(buf ^ 1, i, more);
-      if (!FIRST) multiply<1>(1, 1, i);
-      read_a<0, 0>(buf, 0, i);
-      read_b<0>(buf, 0, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      if (!FIRST) load_part<FULL, true>(buf ^ 1, i, more);
-      multiply<0>(0, 0, i);
-      read_a<0, 1>(buf, 1, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      multiply<1>(1, 0, i);
-      read_b<1>(buf, 1, i);
-      read_a<1, 0>(buf, 0, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      multiply<0>(0, 1, i);
-      read_a<1, 1>(buf, 1, i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-  // What a wave without rows of the tile does of a stage.
-  template <bool FULL>
-  __device__ __forceinline__ void idle(int buf, bool more) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) load_part<FULL, false>(buf ^ 1, i, more);
-    load_part<FULL, true>(buf ^ 1, 3, more);
-  }
-  template <bool WORK>
-  __device__ __forceinline__ void run(int klen, int* half) {
-    const int steps = max((klen + BK - 1) / BK, 1), full = klen / BK;
-    int buf = *half;
-    // stage 0 is here; the second stage's 8 loads and the last tile's stores may not be
-    if (!ahead) arrive<0>();
-    else if (steps > 1) arrive<kStores + NA + NB>();
-    else arrive<kStores>();
-    if (WORK) stage<true, true>(buf, false);
-    if (ahead) arrive<kStores>();
-    else arrive<0>();
-    int s = 0;
-    for (; s + 2 < full; s++) {
-      buf ^= 1;
-      if (WORK) stage<false, true>(buf, true);
-      else idle<true>(buf, true);
-      arrive<0>();
-    }
-    for (; s + 1 < steps; s++) {
-      buf ^= 1;
-      if (WORK) stage<false, false>(buf, s + 2 < steps);
-      else idle<false>(buf, s + 2 < steps);
-      arrive<0>();
-    }
-    *half = buf ^ 1;
-  }
-  // All but the last quarter of the tile that was started in half *half, of `om` rows
-  // and `klen` contraction steps; then both halves are free, *half the one for the next.
-  __device__ __forceinline__ void stages(int om, int klen, int* half) {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-    if (r0 < om) run<true>(klen, half);
-    else run<false>(klen, half);
-  }
-  // The last quarter, and the results.
-  __device__ __forceinline__ void finish(O* out, uint64_t ldo, int om, int on) {
-    ahead = om >= BM && on >= BN;
-    if (r0 >= om) return;
-#pragma unroll
-    for (int i = 0; i < 4; i++) multiply<1>(1, 1, i);
-    O* at = out + (uint64_t)(r0 + (lane & 15)) * ldo + c0 + (lane >> 4) * 8;
-    if (ahead) {
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        store8(at, acc[i][0], acc[i][1]);
-        store8(at + 32, acc[i][2], acc[i][3]);
-        at += 16 * ldo;
-      }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const bool row = r0 + i * 16 + (lane & 15) < om;
-      const int n = c0 + (lane >> 4) * 8;  // on is a multiple of 8
-      if (row && n < on) store8(at, acc[i][0], acc[i][1]);
-      if (row && n + 32 < on) store8(at + 32, acc[i][2], acc[i][3]);
-      at += 16 * ldo;
-    }
-  }
-};
-
-constexpr uint32_t kBigLds = 2 * 2 * 256 * 64 * 2;  // bytes: two stages of two operands
-
 template <typename D, bool TRANS, typename O>
 __global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
-  __shared__ i32x4 lds[kBigLds / 16];
+  __shared__ i32x4 lds[BigTiles<D, true, TRANS, O>::kLds];
   GroupTiles<256> tiles;
   tiles.init(a.offsets, a.groups, a.rows);
   const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds;
@@ -534,7 +279,7 @@ struct GradTiles {
 
 template <typename D, typename O>
 __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
-  __shared__ i32x4 lds[kBigLds / 16];
+  __shared__ i32x4 lds[BigTiles<D, false, false, O>::kLds];
   const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds, me = blockIdx.x / kXcds;
   GradTiles tiles;
   tiles.share(a, (uint32_t)((a.k + 255) / 256) * nt, blockIdx.x % kXcds);
@@ -773,31 +518,12 @@ __global__ __launch_bounds__(512) void group_mm_thin_t(GroupMmArgs a) {
   Join::store(part, static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, rows, left);
 }
 
-// Whether a tile's operands can be addressed with 32-bit byte offsets from their
-// first element: 256 rows, or 64 contraction steps, of `ld` values.
-bool short_stride(uint64_t ld) { return ld < (1u << 22); }
-
-// Most row tiles of height bm that ascending offsets can make of `rows` rows.
-uint64_t max_row_tiles(const GroupMmArgs& a, uint64_t bm) {
-  const uint64_t one = (a.rows + bm - 1) / bm;
-  if (a.groups == 1) return one;
-  const uint64_t full = a.rows / bm, groups = (uint64_t)a.groups;
-  return full + (groups < (uint64_t)a.rows ? groups : (uint64_t)a.rows);
-}
-
-hipError_t tile_grid(uint64_t tiles, uint32_t threads, dim3* grid) {
-  const uint64_t g = (tiles + kXcds - 1) / kXcds * kXcds;
-  if (g * threads >> 32) return hipErrorInvalidConfiguration;
-  *grid = dim3((uint32_t)g);
-  return hipSuccess;
-}
-
 // Rows of 16 * MF to a workgroup; narrow columns where wide ones would not make enough
 // workgroups for the card.
 template <typename D, bool TRANS, typename O, int MF>
 hipError_t run_thin(const GroupMmArgs& a, hipStream_t s) {
   constexpr int WIDE = TRANS ? 64 : 128, NARROW = TRANS ? 16 : 64;
-  const uint64_t mt = max_row_tiles(a, 16 * MF);
+  const uint64_t mt = max_row_tiles(a.rows, a.groups, 16 * MF);
   const bool wide = mt * ((a.n + WIDE - 1) / WIDE) >= 1024;
   const int bn = wide ? WIDE : NARROW;
   dim3 grid;
@@ -821,16 +547,15 @@ hipError_t run_mm(const GroupMmArgs& a, hipStream_t s) {
   if constexpr (!TRANS) {
     if (a.rows <= 32 * (int64_t)a.groups) return run_thin<D, TRANS, O, 2>(a, s);
   }
-  if (FLAT && a.k && a.k % 8 == 0 && a.n % 8 == 0 && a.rows >= 128 * (int64_t)a.groups && short_stride(a.ldx) &&
+  if (FLAT && a.k && a.k % 8 == 0 && (TRANS || a.n % 8 == 0) && a.rows >= 128 * (int64_t)a.groups && short_stride(a.ldx) &&
       short_stride(a.ldw)) {
-    const uint64_t tiles = max_row_tiles(a, 256) * ((a.n + 255) / 256);
-    const uint64_t grid = tiles < 256 ? (tiles + kXcds - 1) / kXcds * kXcds : 256;  // one to a compute unit
-    group_mm_big<D, TRANS, O><<<dim3((uint32_t)grid), dim3(512), 0, s>>>(a);
+    const uint64_t tiles = max_row_tiles(a.rows, a.groups, 256) * ((a.n + 255) / 256);
+    group_mm_big<D, TRANS, O><<<unit_grid(tiles), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
   constexpr int BM = 128, BN = 128;
   dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a, BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
   group_mm_general<D, TRANS, FLAT, O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -840,8 +565,7 @@ hipError_t run_wgrad(const GroupWgradArgs& a, hipStream_t s) {
   if (FLAT && a.k % 8 == 0 && a.n % 8 == 0 && a.k >= 256 && a.n >= 256 && short_stride(a.ldx) &&
       short_stride(a.ldy)) {
     const uint64_t tiles = (uint64_t)a.groups * ((a.k + 255) / 256) * ((a.n + 255) / 256);
-    const uint64_t grid = tiles < 256 ? (tiles + kXcds - 1) / kXcds * kXcds : 256;  // one to a compute unit
-    group_wgrad_big<D, O><<<dim3((uint32_t)grid), dim3(512), 0, s>>>(a);
+    group_wgrad_big<D, O><<<unit_grid(tiles), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
   constexpr int BM = 128, BN = 128;

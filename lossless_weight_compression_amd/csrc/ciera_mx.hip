@@ -6,6 +6,7 @@
 // byte e + 127 and never below 0; each value is the nearest magnitude to
 // |v| 2^-e, ties to the even code, above 6 the 6 itself, with v's sign in bit 3.
 #include "ciera.h"
+#include "ciera_big.h"
 #include "ciera_ops_internal.h"
 #include "ciera_tiles.h"
 
@@ -408,27 +409,25 @@ __global__ __launch_bounds__(256) void mx_mm_general(MxMmArgs a) {
     const bool more = s + 1 < steps;
     if (more) load(s + 1);
     const int cur = s & 1;
-    i32x8 fa[WM], fb[WN];
+    i32x4 fa[WM], fb[WN];
     int xa[WM], xb[WN];
 #pragma unroll
     for (int i = 0; i < WM; i++) {
       const int r = r0 + i * 16 + (lane & 15);
-      const i32x4 v = la[cur][pos(r, lane >> 4)];
-      fa[i] = i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+      fa[i] = la[cur][pos(r, lane >> 4)];
       xa[i] = r < mleft ? psa[r * sb + s * 4 + (lane >> 4)] : 0;
     }
 #pragma unroll
     for (int j = 0; j < WN; j++) {
       const int r = c0 + j * 16 + (lane & 15);
-      const i32x4 v = lb[cur][pos(r, lane >> 4)];
-      fb[j] = i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0};
+      fb[j] = lb[cur][pos(r, lane >> 4)];
       xb[j] = r < nleft ? psb[r * sb + s * 4 + (lane >> 4)] : 0;
     }
 #pragma unroll
     for (int i = 0; i < WM; i++)
 #pragma unroll
       for (int j = 0; j < WN; j++)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i], acc[i][j], 4, 4, 0, xb[j], 0, xa[i]);
+        acc[i][j] = mfma(fb[j], xb[j], fa[i], xa[i], acc[i][j]);
     if (more) put(cur ^ 1);
     __syncthreads();
   }
@@ -442,18 +441,147 @@ __global__ __launch_bounds__(256) void mx_mm_general(MxMmArgs a) {
   }
 }
 
+// Large products: 256 x 256 tiles, 256 codes of every row at a time.  In units of two
+// bytes (4 codes) the operands look like two-byte ones.
+template <typename O>
+__global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
+  typedef BigTiles<Mx4, true, true, O> Big;
+  __shared__ i32x4 lds[Big::kLds];
+  GroupTiles<256> tiles;
+  tiles.init(a.offsets, a.groups, a.rows);
+  const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds;
+  uint64_t first;
+  uint32_t many;
+  die_run((uint64_t)tiles.total * nt, blockIdx.x % kXcds, &first, &many);
+  uint32_t at = blockIdx.x / kXcds;
+  if (at >= many) return;
+  Big big;
+  big.init(lds);
+  const int units = a.kp / 4;
+  const uint32_t srow = a.kp / 32;
+  O* out;
+  int om, on, half = 0;
+  auto start = [&](uint64_t tile) {
+    const GroupTile t = tiles.find((uint32_t)(tile / nt));
+    const int n0 = (int)(tile % nt) * 256;
+    const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256, brow = (uint64_t)t.g * a.n + n0;
+    om = t.count - t.m * 256;
+    on = a.n - n0;
+    out = static_cast<O*>(a.out) + row * a.ldo + n0;
+    big.scales(a.sa + row * srow, om, a.sb + brow * srow, on, srow);
+    big.start(reinterpret_cast<const uint16_t*>(a.a) + row * units, units, om,
+              reinterpret_cast<const uint16_t*>(a.b) + brow * units, units, on, units, half);
+  };
+  start(first + at);
+  for (;;) {
+    big.stages(om, units, &half);
+    O* done = out;
+    const int dm = om, dn = on;
+    at += stride;
+    if (at < many) start(first + at);
+    big.finish(done, a.ldo, dm, dn);
+    if (at >= many) return;
+  }
+}
+
+// Few rows to a group: 16 rows and 16 * NF columns to a workgroup.  Its 4 waves take
+// runs of 512 codes of every row in turn, from memory into registers: a lane 4 blocks
+// and the word of their scales; their sums are joined through LDS in order.
+constexpr int kMxThinWaves = 4;
+
+template <typename O, int NF>
+__global__ __launch_bounds__(256) void mx_mm_thin(MxMmArgs a) {
+  constexpr int BN = 16 * NF, LD = BN + 4;
+  __shared__ __attribute__((aligned(16))) float part[kMxThinWaves * 16 * LD];
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
+  const int blocks = a.kp / 32;
+  const i32x4* pw[NF];
+  const uint8_t* psw[NF];
+#pragma unroll
+  for (int f = 0; f < NF; f++) {
+    const uint64_t r = (uint64_t)t.g * a.n + n0 + min(f * 16 + (lane & 15), left - 1);
+    pw[f] = reinterpret_cast<const i32x4*>(a.b) + r * blocks;
+    psw[f] = a.sb + r * blocks;
+  }
+  const uint64_t xr = row + min(lane & 15, rows - 1);
+  const i32x4* px = reinterpret_cast<const i32x4*>(a.a) + xr * blocks;
+  const uint8_t* psx = a.sa + xr * blocks;
+  f32x4 acc[NF];
+#pragma unroll
+  for (int f = 0; f < NF; f++) acc[f] = f32x4{0, 0, 0, 0};
+  for (int b0 = wave * 16; b0 < blocks; b0 += kMxThinWaves * 16) {
+    const int b = b0 + q * 4;  // rows hold multiples of 4 blocks: a lane's run is in or out
+    i32x4 w[NF][4], x[4];
+    uint32_t sw[NF], sx = 0;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      x[u] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int f = 0; f < NF; f++) w[f][u] = i32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int f = 0; f < NF; f++) sw[f] = 0;
+    if (b < blocks) {
+#pragma unroll
+      for (int f = 0; f < NF; f++) {
+#pragma unroll
+        for (int u = 0; u < 4; u++) w[f][u] = pw[f][b + u];
+        sw[f] = *reinterpret_cast<const uint32_t*>(psw[f] + b);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; u++) x[u] = px[b + u];
+      sx = *reinterpret_cast<const uint32_t*>(psx + b);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++)
+#pragma unroll
+      for (int f = 0; f < NF; f++)
+        acc[f] = mfma(w[f][u], (int)(sw[f] >> (8 * u)), x[u], (int)(sx >> (8 * u)), acc[f]);
+  }
+  float* mine = part + (wave * 16 + (lane & 15)) * LD + (lane >> 4) * 4;
+#pragma unroll
+  for (int f = 0; f < NF; f++) *reinterpret_cast<f32x4*>(mine + f * 16) = acc[f];
+  __syncthreads();
+  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
+  for (int p = threadIdx.x; p < 16 * BN / 4; p += kMxThinWaves * 64) {
+    const int m = p / (BN / 4), c = p % (BN / 4) * 4;
+    if (m >= rows || c >= left) continue;
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kMxThinWaves; w++) v += *reinterpret_cast<const f32x4*>(part + (w * 16 + m) * LD + c);
+    store4(out + (uint64_t)m * a.ldo, c, left, v);
+  }
+}
+
 // Workgroups of a pass; beyond the limit each takes several parts in turn.
 uint32_t pass_grid(uint64_t parts, uint64_t limit) { return (uint32_t)(parts < limit ? parts : limit); }
 uint32_t row_grid(const RowPass& p) { return pass_grid((p.total + 4 * kRun - 1) / (4 * kRun), 1 << 20); }
 
 template <typename O>
 hipError_t run_mx_mm(const MxMmArgs& a, hipStream_t s) {
-  constexpr int BM = 128, BN = 128;
-  const uint64_t rows = a.rows, groups = a.groups;
-  const uint64_t mt = groups == 1 ? (rows + BM - 1) / BM : rows / BM + (groups < rows ? groups : rows);
-  const uint64_t grid = (mt * ((a.n + BN - 1) / BN) + kXcds - 1) / kXcds * kXcds;
-  if (grid * 256 >> 32) return hipErrorInvalidConfiguration;
-  mx_mm_general<O, BM, BN><<<dim3((uint32_t)grid), dim3(256), 0, s>>>(a);
+#ifndef M1
+#define M1 16
+#define M2 128
+#endif
+  dim3 grid;
+  if (a.rows <= M1 * (int64_t)a.groups) {
+    const uint64_t mt = max_row_tiles(a.rows, a.groups, 16);
+    const bool wide = mt * ((a.n + 63) / 64) >= 2048;
+    if (hipError_t e = tile_grid(mt * ((a.n + (wide ? 63 : 15)) / (wide ? 64 : 16)), 256, &grid)) return e;
+    if (wide) mx_mm_thin<O, 4><<<grid, dim3(256), 0, s>>>(a);
+    else mx_mm_thin<O, 1><<<grid, dim3(256), 0, s>>>(a);
+  } else if (a.kp && a.rows >= M2 * (int64_t)a.groups && short_stride(a.kp / 4)) {
+    mx_mm_big<O><<<unit_grid(max_row_tiles(a.rows, a.groups, 256) * ((a.n + 255) / 256)), dim3(512), 0, s>>>(a);
+  } else {
+    constexpr int BM = 128, BN = 128;
+    if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
+    mx_mm_general<O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

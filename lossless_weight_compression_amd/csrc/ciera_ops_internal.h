@@ -62,6 +62,24 @@ struct MxDequantArgs {
   int32_t groups, rows, cols;
 };
 
+// Most row tiles of height bm that ascending offsets can make of `rows` rows.
+inline uint64_t max_row_tiles(uint64_t rows, uint64_t groups, uint64_t bm) {
+  if (groups == 1) return (rows + bm - 1) / bm;
+  return rows / bm + (groups < rows ? groups : rows);
+}
+// The grid of one workgroup to a tile: as many on each die.
+inline hipError_t tile_grid(uint64_t tiles, uint32_t threads, dim3* grid) {
+  const uint64_t g = (tiles + kXcds - 1) / kXcds * kXcds;
+  if (g * threads >> 32) return hipErrorInvalidConfiguration;
+  *grid = dim3((uint32_t)g);
+  return hipSuccess;
+}
+// One workgroup to a compute unit, fewer if there are fewer tiles.
+constexpr uint32_t kUnits = 256;
+inline dim3 unit_grid(uint64_t tiles) {
+  return dim3((uint32_t)(tiles < kUnits ? (tiles + kXcds - 1) / kXcds * kXcds : kUnits));
+}
+
 // dtype: ciera_dtype_t of x; out_f32: the output is fp32 instead of x's type.
 // flat: every operand row is 16-byte aligned (base, strides).
 hipError_t launch_group_mm(int dtype, bool out_f32, bool transpose_w, bool flat, const GroupMmArgs& a, hipStream_t s);

@@ -11,16 +11,21 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 struct Bf16 {
-  typedef __bf16 T;
   typedef bf16x8 V;
+  static constexpr bool kScaled = false;
 };
 struct Fp16 {
-  typedef _Float16 T;
   typedef f16x8 V;
+  static constexpr bool kScaled = false;
+};
+struct Mx4 {  // 32 codes
+  typedef i32x4 V;
+  static constexpr bool kScaled = true;
 };
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -30,11 +35,49 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// 32 x 32 results over 16 steps
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+// 16 x 16 results over 128 steps: a lane's 32 codes and their scale, in the lowest byte.
+__device__ __forceinline__ f32x4 mfma(i32x4 a, int scale_a, i32x4 b, int scale_b, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
+                                                          i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, c, 4, 4, 0, scale_a, 0,
+                                                          scale_b);
+}
+// 32 x 32 results over 64 steps, the scales in byte U.
+template <int U>
+__device__ __forceinline__ f32x16 mfma(i32x4 a, int scale_a, i32x4 b, int scale_b, f32x16 c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
+                                                         i32x8{b[0], b[1], b[2], b[3], 0, 0, 0, 0}, c, 4, 4, U, scale_a, U,
+                                                         scale_b);
+}
+
 // 16 bytes at any 2-byte aligned address (the hardware splits what crosses a line).
 struct __attribute__((packed, aligned(2))) Bytes16 {
   i32x4 v;
 };
 __device__ __forceinline__ i32x4 load16(const void* p) { return reinterpret_cast<const Bytes16*>(p)->v; }
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+template <typename T>
+__device__ __forceinline__ T read_lds(uint32_t at) {
+  return *(__attribute__((address_space(3))) const T*)(uintptr_t)at;
+}
+// The transposing LDS load, twice: of every 16 lanes, lane i gets column i of the rows
+// of 16 two-byte values that they address (4 lanes, 8 bytes each, to a row): 4 rows,
+// and 4 more `next` bytes on.
+__device__ __forceinline__ s16x8 read_transposed(uint32_t at, uint32_t next) {
+  typedef __attribute__((address_space(3))) s16x4* lds_p;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(uintptr_t)at);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(uintptr_t)(at + next));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 // The rows of one group as the kernel sees them: offsets out of order or out of
 // range are clamped, so that no access leaves the operands.
@@ -141,46 +184,43 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
 // One operand tile in LDS, in 16-byte chunks (8 two-byte values).  KC: the
 // contraction is contiguous in memory; R rows of BK values.  Else BK contraction
 // steps of R contiguous values, read back with the transposing LDS load, whose 16
-// lanes take 8 bytes each, of 4 steps.
-//
-// A fragment holds 16 rows.  PERM: not 16 consecutive ones; of every 32 rows the
-// even fragment takes the first 4 of every 8, the odd one the others, so that a lane,
-// which gets 4 consecutive rows of each as its results, has 8 consecutive ones (16
-// bytes) of the two.
-//
-// The chunks of a line are permuted by the line, so that what the lanes of one LDS
-// cycle read lies in different banks: 8 rows' chunks of the same steps, or 4 steps'
-// chunks of the same rows.
-template <bool KC, int R, int BK, bool PERM = false>
+// lanes take 8 bytes each, of 4 steps.  The chunks of a line are permuted by the line,
+// so that what the lanes of one LDS cycle read lies in different banks.
+template <bool KC, int R, int BK>
 struct LdsTile {
   static constexpr int kChunks = R * BK / 8;
   static constexpr int kPerRow = KC ? BK / 8 : R / 8;
+  static_assert(!KC || BK == 32, "the permutation of rows is made for rows of 4 chunks");
   static __device__ __forceinline__ int swizzle(int line, int c) {
-    if (KC && BK == 32) return c ^ ((line >> 2) & 3);
-    if (KC) return PERM ? c ^ ((line & 3) | ((line >> 1) & 4)) : c ^ (line & 7);
-    return PERM ? c ^ ((line & 3) << 2) : c ^ (((line & 3) | ((line >> 1) & 4)) << 1);
+    return KC ? c ^ ((line >> 2) & 3) : c ^ (((line & 3) | ((line >> 1) & 4)) << 1);
   }
   // position of chunk c of a line (a row, or a contraction step)
   static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
 
-  // Fragment f of the rows from r0 on, steps k0 + 8 * (lane / 16) ... of its row lane % 16.
-  static __device__ __forceinline__ s16x8 fragment(const i32x4* lds, int r0, int f, int k0) {
+  // of row r0 + lane % 16 the contraction steps 8 * (lane / 16) ...
+  static __device__ __forceinline__ s16x8 fragment(const i32x4* lds, int r0) {
     const int lane = threadIdx.x & 63;
     if (KC) {
-      const int r = PERM ? (f >> 1) * 32 + ((lane & 12) << 1) + (f & 1) * 4 + (lane & 3) : f * 16 + (lane & 15);
-      return __builtin_bit_cast(s16x8, lds[pos(r0 + r, (k0 >> 3) + (lane >> 4))]);
+      return __builtin_bit_cast(s16x8, lds[pos(r0 + (lane & 15), lane >> 4)]);
     } else {
-      typedef __attribute__((address_space(3))) s16x4* lds_p;
-      const int step = k0 + (lane >> 4) * 8 + ((lane & 15) >> 2);
-      const int r = PERM ? (f >> 1) * 32 + (lane & 3) * 8 + (f & 1) * 4 : f * 16 + (lane & 3) * 4;
-      const char* base = reinterpret_cast<const char*>(lds) + (r & 4) * 2;
-      const int c = (r0 + r) >> 3;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(base + pos(step, c) * 16));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(base + pos(step + 4, c) * 16));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const int step = (lane >> 4) * 8 + ((lane & 15) >> 2), c = (r0 >> 3) + ((lane & 3) >> 1);
+      return read_transposed(lds_address(lds) + pos(step, c) * 16 + (lane & 1) * 8, 4 * kPerRow * 16);
     }
   }
 };
+
+// f(0), f(1), ... with the number as a constant.
+template <int I>
+struct Int {
+  static constexpr int v = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(Int<I>());
+    each<N, I + 1>(f);
+  }
+}
 
 // 8 values of a two-byte matrix from (line, c * 8) on, zeros where the line or
 // the column lies outside: lines of `ld` values at any 2-byte aligned address.
@@ -217,27 +257,15 @@ __device__ __forceinline__ void store4(O* row, int col, int cols, f32x4 v) {
       if (col + i < cols) row[col + i] = (O)v[i];
   }
 }
-// 8 outputs, 4 each of two fragments: one store in two-byte types, two in fp32.
+// 8 outputs: one store in two-byte types, two in fp32.
 template <typename O>
 __device__ __forceinline__ void store8(O* at, f32x4 lo, f32x4 hi) {
-  if (sizeof(O) == 2) {
-    Pack<O, 8> p;
+  constexpr int N = sizeof(O) == 2 ? 8 : 4;
+  Pack<O, N> p[8 / N];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      p.v[i] = (O)lo[i];
-      p.v[4 + i] = (O)hi[i];
-    }
-    *reinterpret_cast<Pack<O, 8>*>(at) = p;
-  } else {
-    Pack<O, 4> p, q;
+  for (int i = 0; i < 8; i++) p[i / N].v[i % N] = (O)(i < 4 ? lo[i & 3] : hi[i & 3]);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      p.v[i] = (O)lo[i];
-      q.v[i] = (O)hi[i];
-    }
-    *reinterpret_cast<Pack<O, 4>*>(at) = p;
-    *reinterpret_cast<Pack<O, 4>*>(at + 4) = q;
-  }
+  for (int i = 0; i < 8 / N; i++) reinterpret_cast<Pack<O, N>*>(at)[i] = p[i];
 }
 
 }  // namespace
