@@ -35,74 +35,6 @@ __device__ __forceinline__ void load_lds4(const char* base, uint32_t offset, voi
                : "memory");
 }
 
-// v, as if computed anew here: what depends on it is not kept in registers across the
-// main loop.
-__device__ __forceinline__ int afresh(int v) {
-  asm volatile("" : "+v"(v));
-  return v;
-}
-// LDS writes of this wave's lanes before, reads by others after (and the other way
-// round): the LDS unit takes a wave's accesses in order, the compiler has to.
-__device__ __forceinline__ void wave_order() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_wave_barrier();
-  asm volatile("" ::: "memory");
-}
-
-// One operand of a stage in LDS: 256 rows, 64 contraction steps of two bytes, in
-// 16-byte chunks.  KC: the contraction is contiguous in memory, 8 chunks to a row; else
-// 32 chunks to a contraction step, read back with the transposing load.
-//
-// A fragment is S rows, 16 or 32.  COLS (the operand whose rows are the result's columns):
-// they are taken in an order that gives a lane, which gets 4 of them together as results,
-// 8 consecutive columns.
-//
-// The chunks of a line (a row, or a contraction step) are permuted by the line, so that
-// what the lanes of one LDS cycle read lies in different banks: the same chunk of 8 rows,
-// or pieces of 4 contraction steps.
-template <bool KC, bool COLS, int S>
-struct StageTile {
-  static constexpr int kChunks = 2048, kPerRow = KC ? 8 : 32;
-  static __device__ __forceinline__ int swizzle(int line, int c) {
-    const int k = (line & 3) | ((line >> 1) & 4);
-    if (KC) return c ^ (COLS ? k : line & 7);
-    return c ^ (S == 16 && !COLS ? k << 1 : (line & 3) << 2);
-  }
-  static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
-  // the row of fragment 0 that this lane reads
-  static __device__ __forceinline__ int first_row() {
-    const int v = threadIdx.x & (S - 1);
-    if (!COLS) return v;
-    return S == 16 ? ((v & 12) << 1) + (v & 3) : (v & 16) + ((v >> 2) & 1) * 8 + ((v >> 3) & 1) * 4 + (v & 3);
-  }
-  // Where this lane reads fragment 0 of the rows from r0 on in the first part of the
-  // stage (an address in LDS).  Other fragments and parts lie at that place with bits
-  // flipped and a constant added, which costs no register each.  S = 16: a part is half
-  // a stage, 8 steps of it to each 16 lanes.  S = 32: a part is 8 steps of each half of
-  // the stage, one for each half of the wave.
-  static __device__ __forceinline__ uint32_t place(const i32x4* lds, int r0) {
-    const int lane = threadIdx.x & 63, p = lane & 3;
-    if (KC) return lds_address(lds) + pos(r0 + first_row(), S == 16 ? lane >> 4 : (lane >> 5) * 4) * 16;
-    const int step = (S == 16 ? (lane >> 4) * 8 : (lane >> 5) * 32) + ((lane >> 2) & 3);
-    int c, half;
-    if (S == 16) {
-      c = COLS ? p : p >> 1;
-      half = COLS ? 0 : p & 1;
-    } else {
-      c = ((lane >> 4) & 1) * 2 + (COLS ? p & 1 : p >> 1);
-      half = COLS ? p >> 1 : p & 1;
-    }
-    return lds_address(lds) + pos(step, r0 / 8 + c) * 16 + half * 8;
-  }
-  template <int F, int PART>
-  static __device__ __forceinline__ s16x8 fragment(uint32_t place) {
-    constexpr int ROW = S == 32 ? F * 32 : COLS ? (F >> 1) * 32 + (F & 1) * 4 : F * 16;
-    if constexpr (KC) return read_lds<s16x8>((place ^ (PART * (S == 16 ? 64 : 16))) + ROW * kPerRow * 16);
-    constexpr int FLIP = ROW / 8 * 16, HALF = (ROW & 7) * 2;
-    return read_transposed((place ^ FLIP) + PART * (S == 16 ? 32 : 8) * kPerRow * 16 + HALF, 4 * kPerRow * 16);
-  }
-};
-
 // What a wave does with a stage in LDS: 128 x 64 results, by quarters of 4 parts.
 // read<U, I> fetches what part I of quarter U needs new, multiply<U, I> multiplies it; the
 // parts of a quarter may be read while the quarter before is multiplied.

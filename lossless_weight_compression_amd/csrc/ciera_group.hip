@@ -2,125 +2,44 @@
 // gradient of the weights, x_g^T dy_g.
 #include "ciera.h"
 #include "ciera_big.h"
+#include "ciera_mid.h"
 #include "ciera_ops_internal.h"
 #include "ciera_tiles.h"
 
 namespace ciera {
 namespace {
 
-// One BM x BN tile of C = A B over `klen` contraction steps, 4 waves of
-// (BM / 2) x (BN / 2).  A has `am` rows left, B `bn` columns; loads go through
-// registers, so that rows may start at any element and end anywhere.
-template <typename D, bool AKC, bool BKC, bool FLAT, typename O, int BM, int BN>
-__device__ __forceinline__ void general_tile(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb,
-                                             int bn, int klen, O* out, uint64_t ldo, int om, int on) {
-  constexpr int BK = 32;
-  typedef LdsTile<AKC, BM, BK> TA;
-  typedef LdsTile<BKC, BN, BK> TB;
-  constexpr int NA = TA::kChunks / 256, NB = TB::kChunks / 256;
-  constexpr int WM = BM / 2 / 16, WN = BN / 2 / 16;
-  __shared__ i32x4 la[2][TA::kChunks];
-  __shared__ i32x4 lb[2][TB::kChunks];
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * (BN / 2);
-
-  i32x4 ra[NA], rb[NB];
-  auto load = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < NA; i++) {
-      const int p = i * 256 + tid, line = p / TA::kPerRow, c = p % TA::kPerRow;
-      ra[i] = AKC ? load_chunk<FLAT>(a, lda, line, am, k0 + c * 8, klen)
-                  : load_chunk<FLAT>(a, lda, k0 + line, klen, c * 8, am);
-    }
-#pragma unroll
-    for (int i = 0; i < NB; i++) {
-      const int p = i * 256 + tid, line = p / TB::kPerRow, c = p % TB::kPerRow;
-      rb[i] = BKC ? load_chunk<FLAT>(b, ldb, line, bn, k0 + c * 8, klen)
-                  : load_chunk<FLAT>(b, ldb, k0 + line, klen, c * 8, bn);
-    }
-  };
-  auto put = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < NA; i++) {
-      const int p = i * 256 + tid;
-      la[s][TA::pos(p / TA::kPerRow, p % TA::kPerRow)] = ra[i];
-    }
-#pragma unroll
-    for (int i = 0; i < NB; i++) {
-      const int p = i * 256 + tid;
-      lb[s][TB::pos(p / TB::kPerRow, p % TB::kPerRow)] = rb[i];
-    }
-  };
-
-  f32x4 acc[WM][WN];
-#pragma unroll
-  for (int i = 0; i < WM; i++)
-#pragma unroll
-    for (int j = 0; j < WN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-
-  const int steps = (klen + BK - 1) / BK;
-  if (steps) {
-    load(0);
-    put(0);
-  }
-  __syncthreads();
-  for (int s = 0; s < steps; s++) {
-    const bool more = s + 1 < steps;
-    if (more) load((s + 1) * BK);
-    const int cur = s & 1;
-    typename D::V fa[WM], fb[WN];
-#pragma unroll
-    for (int i = 0; i < WM; i++) fa[i] = __builtin_bit_cast(typename D::V, TA::fragment(la[cur], r0 + i * 16));
-#pragma unroll
-    for (int j = 0; j < WN; j++) fb[j] = __builtin_bit_cast(typename D::V, TB::fragment(lb[cur], c0 + j * 16));
-#pragma unroll
-    for (int i = 0; i < WM; i++)
-#pragma unroll
-      for (int j = 0; j < WN; j++) acc[i][j] = mfma(fb[j], fa[i], acc[i][j]);
-    if (more) put(cur ^ 1);
-    __syncthreads();
-  }
-  // the operands are given in swapped order: a lane holds 4 consecutive columns of a row
-  const int lane = tid & 63;
-#pragma unroll
-  for (int i = 0; i < WM; i++) {
-    const int m = r0 + i * 16 + (lane & 15);
-    if (m >= om) continue;
-#pragma unroll
-    for (int j = 0; j < WN; j++) store4(out + (uint64_t)m * ldo, c0 + j * 16 + (lane >> 4) * 4, on, acc[i][j]);
-  }
-}
-
-template <typename D, bool TRANS, bool FLAT, typename O, int BM, int BN>
-__global__ __launch_bounds__(256) void group_mm_general(GroupMmArgs a) {
+template <typename D, bool TRANS, typename O, int BM>
+__global__ __launch_bounds__(256, 2) void group_mm_mid(GroupMmArgs a) {
   GroupTile t;
   int tn;
-  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + 127) / 128, blockIdx.x, &t, &tn)) return;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
-  const int mleft = t.count - t.m * BM, n0 = tn * BN, nleft = a.n - n0;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.ldx;
-  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0);
-  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
-  general_tile<D, true, TRANS, FLAT, O, BM, BN>(x, a.ldx, mleft, w, a.ldw, nleft, a.k, out, a.ldo, mleft, nleft);
+  // the last tile ends with the matrix: it gives some columns a second time, the same values
+  const int n0 = TRANS ? tn * 128 : max(min(tn * 128, a.n - 128), 0);
+  mid_tile<D, true, TRANS, O, BM>(
+      static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, t.count - t.m * BM,
+      static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, a.n - n0, a.k,
+      static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo);
 }
 
-template <typename D, bool FLAT, typename O, int BM, int BN>
-__global__ __launch_bounds__(256) void group_wgrad_general(GroupWgradArgs a) {
-  const uint32_t mt = (a.k + BM - 1) / BM, nt = (a.n + BN - 1) / BN;
+template <typename D, typename O, int BM>
+__global__ __launch_bounds__(256, 2) void group_wgrad_mid(GroupWgradArgs a) {
+  const uint32_t mt = (a.k + BM - 1) / BM, nt = (a.n + 127) / 128;
   uint64_t first;
   uint32_t many;
   die_run((uint64_t)mt * nt * a.groups, blockIdx.x % kXcds, &first, &many);
   if (blockIdx.x / kXcds >= many) return;
   const uint64_t tile = first + blockIdx.x / kXcds;
   const int g = tile / ((uint64_t)mt * nt);
-  const int m0 = (tile / nt % mt) * BM, n0 = (tile % nt) * BN;
+  const int m0 = max(min((int)(tile / nt % mt) * BM, a.k - BM), 0), n0 = max(min((int)(tile % nt) * 128, a.n - 128), 0);
   int begin, count;
   group_range(a.offsets, g, a.rows, &begin, &count);
-  const uint16_t* px = static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0;
-  const uint16_t* pd = static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0;
-  O* out = static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0;
-  general_tile<D, false, false, FLAT, O, BM, BN>(px, a.ldx, a.k - m0, pd, a.ldy, a.n - n0, count, out, a.ldo, a.k - m0,
-                                                 a.n - n0);
+  begin = __builtin_amdgcn_readfirstlane(begin);
+  count = __builtin_amdgcn_readfirstlane(count);
+  mid_tile<D, false, false, O, BM>(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
+                                   static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, a.n - n0, count,
+                                   static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo);
 }
 
 template <typename D, bool TRANS, typename O>
@@ -317,7 +236,7 @@ __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
 
 // ------------------------------------------------------- few rows to a group
 // What counts then is how fast the weights are read, each once.  A workgroup takes 16
-// rows of a group (or 16 * MF) and some columns; its 8 waves take the contraction steps in turn, so
+// rows of a group and some columns; its 8 waves take the contraction steps in turn, so
 // that all of them read at once, from memory into registers, the next step's values
 // under way while this one's are multiplied; their sums are joined through LDS in the
 // order of the waves.
@@ -342,27 +261,24 @@ struct ThinJoin {
 
 // W [K, N]: a lane holds 8 contraction steps of VEC columns (two-byte values, 2 * VEC
 // bytes of 8 rows) and turns them around in registers; 16 lanes cover 16 * VEC columns.
-template <typename D, typename O, int MF, int VEC>
+template <typename D, typename O, int VEC>
 __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
   constexpr int BN = 16 * VEC, W = VEC / 2;  // words of a row's columns in a lane
   typedef ThinJoin<O, BN> Join;
   __shared__ __attribute__((aligned(16))) float part[kThinWaves * 16 * Join::kLd];
   GroupTile t;
   int tn;
-  if (!find_group_tile<16 * MF>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16 * MF;
-  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16 * MF;
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
   const int c = (lane & 15) * VEC, q = lane >> 4;
   const uint16_t* w = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + n0 + c;
-  const uint16_t* x[MF];
-#pragma unroll
-  for (int f = 0; f < MF; f++)
-    x[f] = static_cast<const uint16_t*>(a.x) + (row + min(f * 16 + (lane & 15), rows - 1)) * a.ldx;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx;
 
   struct Step {
     uint32_t w[8][W];
-    i32x4 x[MF];
+    i32x4 x;
   };
   auto load = [&](Step& s, int k0) {
     const int k = k0 + q * 8;
@@ -380,8 +296,7 @@ __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
           s.w[j][1] = v.v[1];
         }
       }
-#pragma unroll
-      for (int f = 0; f < MF; f++) s.x[f] = load16(x[f] + k);
+      s.x = load16(x + k);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; j++)
@@ -395,15 +310,12 @@ __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
           }
           s.w[j][i] = v;
         }
-#pragma unroll
-      for (int f = 0; f < MF; f++) s.x[f] = load_chunk<false>(x[f], 0, 0, 1, k, a.k);
+      s.x = load_some(x + k, a.k - k);
     }
   };
-  f32x4 acc[MF][VEC];
+  f32x4 acc[VEC];
 #pragma unroll
-  for (int f = 0; f < MF; f++)
-#pragma unroll
-    for (int j = 0; j < VEC; j++) acc[f][j] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < VEC; j++) acc[j] = f32x4{0, 0, 0, 0};
   auto multiply = [&](const Step& s) {
 #pragma unroll
     for (int j = 0; j < VEC; j++) {
@@ -411,9 +323,7 @@ __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; i++)
         v[i] = __builtin_amdgcn_perm(s.w[2 * i + 1][j / 2], s.w[2 * i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
-#pragma unroll
-      for (int f = 0; f < MF; f++)
-        acc[f][j] = mfma(__builtin_bit_cast(typename D::V, v), __builtin_bit_cast(typename D::V, s.x[f]), acc[f][j]);
+      acc[j] = mfma(__builtin_bit_cast(typename D::V, v), __builtin_bit_cast(typename D::V, s.x), acc[j]);
     }
   };
   constexpr int STEP = 32 * kThinWaves;
@@ -430,27 +340,21 @@ __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
     k0 += STEP;
   }
   // results of a lane: row lane % 16, columns (lane / 16 * 4 + i) * VEC + j
-  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
+  float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4 * VEC;
 #pragma unroll
-  for (int f = 0; f < MF; f++) {
-    float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4 * VEC;
+  for (int i = 0; i < 4; i++)
 #pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int j = 0; j < VEC; j += 4)
-        *reinterpret_cast<f32x4*>(mine + i * VEC + j) =
-            f32x4{acc[f][j][i], acc[f][j + 1][i], acc[f][j + 2][i], acc[f][j + 3][i]};
-    __syncthreads();
-    Join::store(part, out + (uint64_t)f * 16 * a.ldo, a.ldo, rows - f * 16, left);
-    if (f + 1 < MF) __syncthreads();
-  }
+    for (int j = 0; j < VEC; j += 4)
+      *reinterpret_cast<f32x4*>(mine + i * VEC + j) = f32x4{acc[j][i], acc[j + 1][i], acc[j + 2][i], acc[j + 3][i]};
+  __syncthreads();
+  Join::store(part, static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, rows, left);
 }
 
-// W [N, K]: a lane reads 64 bytes of one row of W (4 loads, so that 4 lanes cover 256
-// bytes of a row), NF rows of 16 to a wave.
-template <typename D, typename O, int NF>
+// W [N, K]: a lane reads 64 bytes of one of 16 rows of W (4 loads, so that 4 lanes cover 256
+// bytes of a row).
+template <typename D, typename O>
 __global__ __launch_bounds__(512) void group_mm_thin_t(GroupMmArgs a) {
-  constexpr int BN = 16 * NF;
+  constexpr int BN = 16;
   typedef ThinJoin<O, BN> Join;
   __shared__ __attribute__((aligned(16))) float part[kThinWaves * 16 * Join::kLd];
   GroupTile t;
@@ -460,42 +364,33 @@ __global__ __launch_bounds__(512) void group_mm_thin_t(GroupMmArgs a) {
   const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
   const int q = lane >> 4;
-  const uint16_t* w[NF];
-#pragma unroll
-  for (int f = 0; f < NF; f++)
-    w[f] = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw +
-           (uint64_t)(n0 + min(f * 16 + (lane & 15), left - 1)) * a.ldw;
+  const uint16_t* w =
+      static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (uint64_t)(n0 + min(lane & 15, left - 1)) * a.ldw;
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx;
   struct Step {
-    i32x4 w[NF][4], x[4];
+    i32x4 w[4], x[4];
   };
   auto load = [&](Step& s, int k0) {
     const int k = k0 + q * 32;
     if (k0 + 128 <= a.k) {
 #pragma unroll
       for (int u = 0; u < 4; u++) {
-#pragma unroll
-        for (int f = 0; f < NF; f++) s.w[f][u] = load16(w[f] + k + u * 8);
+        s.w[u] = load16(w + k + u * 8);
         s.x[u] = load16(x + k + u * 8);
       }
     } else {
 #pragma unroll
       for (int u = 0; u < 4; u++) {
-#pragma unroll
-        for (int f = 0; f < NF; f++) s.w[f][u] = load_chunk<false>(w[f], 0, 0, 1, k + u * 8, a.k);
-        s.x[u] = load_chunk<false>(x, 0, 0, 1, k + u * 8, a.k);
+        s.w[u] = load_some(w + k + u * 8, a.k - k - u * 8);
+        s.x[u] = load_some(x + k + u * 8, a.k - k - u * 8);
       }
     }
   };
-  f32x4 acc[NF];
-#pragma unroll
-  for (int j = 0; j < NF; j++) acc[j] = f32x4{0, 0, 0, 0};
+  f32x4 acc = {0, 0, 0, 0};
   auto multiply = [&](const Step& s) {
 #pragma unroll
     for (int u = 0; u < 4; u++)
-#pragma unroll
-      for (int j = 0; j < NF; j++)
-        acc[j] = mfma(__builtin_bit_cast(typename D::V, s.w[j][u]), __builtin_bit_cast(typename D::V, s.x[u]), acc[j]);
+      acc = mfma(__builtin_bit_cast(typename D::V, s.w[u]), __builtin_bit_cast(typename D::V, s.x[u]), acc);
   };
   constexpr int STEP = 128 * kThinWaves;
   int k0 = wave * 128;
@@ -510,82 +405,89 @@ __global__ __launch_bounds__(512) void group_mm_thin_t(GroupMmArgs a) {
     multiply(s[1]);
     k0 += STEP;
   }
-  // results of a lane: row lane % 16, columns j * 16 + lane / 16 * 4 + i
+  // results of a lane: row lane % 16, columns lane / 16 * 4 + i
   float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4;
-#pragma unroll
-  for (int j = 0; j < NF; j++) *reinterpret_cast<f32x4*>(mine + j * 16) = acc[j];
+  *reinterpret_cast<f32x4*>(mine) = acc;
   __syncthreads();
   Join::store(part, static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, rows, left);
 }
 
-// Rows of 16 * MF to a workgroup; narrow columns where wide ones would not make enough
-// workgroups for the card.
-template <typename D, bool TRANS, typename O, int MF>
+// Narrow columns to a workgroup where wide ones would not make enough workgroups for the
+// card.
+template <typename D, bool TRANS, typename O>
 hipError_t run_thin(const GroupMmArgs& a, hipStream_t s) {
-  constexpr int WIDE = TRANS ? 64 : 128, NARROW = TRANS ? 16 : 64;
-  const uint64_t mt = max_row_tiles(a.rows, a.groups, 16 * MF);
-  const bool wide = mt * ((a.n + WIDE - 1) / WIDE) >= 1024;
+  constexpr int WIDE = 128, NARROW = TRANS ? 16 : 64;
+  const uint64_t mt = max_row_tiles(a.rows, a.groups, 16);
+  const bool wide = !TRANS && mt * ((a.n + WIDE - 1) / WIDE) >= 4 * kUnits;
   const int bn = wide ? WIDE : NARROW;
   dim3 grid;
   if (hipError_t e = tile_grid(mt * ((a.n + bn - 1) / bn), 512, &grid)) return e;
   if constexpr (TRANS) {
-    if (wide) group_mm_thin_t<D, O, 4><<<grid, dim3(512), 0, s>>>(a);
-    else group_mm_thin_t<D, O, 1><<<grid, dim3(512), 0, s>>>(a);
+    group_mm_thin_t<D, O><<<grid, dim3(512), 0, s>>>(a);
   } else {
-    if (wide) group_mm_thin<D, O, MF, 8><<<grid, dim3(512), 0, s>>>(a);
-    else group_mm_thin<D, O, MF, 4><<<grid, dim3(512), 0, s>>>(a);
+    if (wide) group_mm_thin<D, O, 8><<<grid, dim3(512), 0, s>>>(a);
+    else group_mm_thin<D, O, 4><<<grid, dim3(512), 0, s>>>(a);
   }
   return hipGetLastError();
 }
 
-template <typename D, bool TRANS, bool FLAT, typename O>
-hipError_t run_mm(const GroupMmArgs& a, hipStream_t s) {
-  // Few rows to a group on average (64 experts of 2048 x 1024, bf16; the 128 x 128 kernel
-  // in brackets): [K, N] 8 rows 43 us (56), 16 rows 51 (61), 32 rows in pairs of 16 56
-  // (72), 64 rows 81 (73); [N, K] 8 rows 53 (62), 16 rows 66 (64), pairs lose throughout.
-  if (a.rows <= (TRANS ? 12 : 16) * (int64_t)a.groups) return run_thin<D, TRANS, O, 1>(a, s);
-  if constexpr (!TRANS) {
-    if (a.rows <= 32 * (int64_t)a.groups) return run_thin<D, TRANS, O, 2>(a, s);
-  }
-  if (FLAT && a.k && a.k % 8 == 0 && (TRANS || a.n % 8 == 0) && a.rows >= 128 * (int64_t)a.groups && short_stride(a.ldx) &&
-      short_stride(a.ldw)) {
-    const uint64_t tiles = max_row_tiles(a.rows, a.groups, 256) * ((a.n + 255) / 256);
-    group_mm_big<D, TRANS, O><<<unit_grid(tiles), dim3(512), 0, s>>>(a);
-    return hipGetLastError();
-  }
-  constexpr int BM = 128, BN = 128;
+template <typename D, bool TRANS, typename O, int BM>
+hipError_t run_mid(const GroupMmArgs& a, hipStream_t s) {
   dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
-  group_mm_general<D, TRANS, FLAT, O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
-  return hipGetLastError();
-}
-
-template <typename D, bool FLAT, typename O>
-hipError_t run_wgrad(const GroupWgradArgs& a, hipStream_t s) {
-  if (FLAT && a.k % 8 == 0 && a.n % 8 == 0 && a.k >= 256 && a.n >= 256 && short_stride(a.ldx) &&
-      short_stride(a.ldy)) {
-    const uint64_t tiles = (uint64_t)a.groups * ((a.k + 255) / 256) * ((a.n + 255) / 256);
-    group_wgrad_big<D, O><<<unit_grid(tiles), dim3(512), 0, s>>>(a);
-    return hipGetLastError();
-  }
-  constexpr int BM = 128, BN = 128;
-  dim3 grid;
-  if (hipError_t e = tile_grid((uint64_t)a.groups * ((a.k + BM - 1) / BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
-  group_wgrad_general<D, FLAT, O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + 127) / 128), 256, &grid)) return e;
+  group_mm_mid<D, TRANS, O, BM><<<grid, dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename D, bool TRANS, typename O>
-hipError_t pick_mm(bool flat, const GroupMmArgs& a, hipStream_t s) {
-  return flat ? run_mm<D, TRANS, true, O>(a, s) : run_mm<D, TRANS, false, O>(a, s);
+hipError_t run_mm(bool flat, const GroupMmArgs& a, hipStream_t s) {
+  // By rows to a group on average; 64 experts of 2048 x 1024, bf16, us:
+  //   rows             2    8   16   24   32   64  100  128  160  200  256
+  //   [K, N] thin     29   44   50
+  //          64 rows  32   44   55   55   55   56   70   83   89  107  115
+  //          256 x 256                                 110  107  112  116
+  //   [N, K] thin     32   53   66
+  //          64 rows  29   41   52   50   51   53   71   83   89  106  113
+  // The thin kernel takes [N, K] only where tiles of 64 x 128 are too few for the card (1
+  // token over 8 of the experts: 10.9 us, 15.3), the 256 x 256 one all that gives it half
+  // the card, the 128 x 128 one what is large but cannot be read straight into LDS (13
+  // groups, 40000 rows, 1447 x 777, fp16: 184 us, in 64 x 128 tiles 219).
+  const int64_t rows = a.rows, groups = a.groups;
+  const uint64_t nt = (a.n + 127) / 128;
+  if (rows <= 16 * groups && (!TRANS || max_row_tiles(rows, groups, 64) * nt < kUnits)) return run_thin<D, TRANS, O>(a, s);
+  const uint64_t big = max_row_tiles(rows, groups, 256) * ((a.n + 255) / 256);
+  if (flat && a.k && a.k % 8 == 0 && (TRANS || a.n % 8 == 0) && rows >= 256 * groups && big >= kUnits / 2 &&
+      short_stride(a.ldx) && short_stride(a.ldw)) {
+    group_mm_big<D, TRANS, O><<<unit_grid(big), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  if (rows <= 96 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits) return run_mid<D, TRANS, O, 64>(a, s);
+  return run_mid<D, TRANS, O, 128>(a, s);
 }
+
+template <typename D, typename O>
+hipError_t run_wgrad(bool flat, const GroupWgradArgs& a, hipStream_t s) {
+  const uint64_t big = (uint64_t)a.groups * ((a.k + 255) / 256) * ((a.n + 255) / 256);
+  if (flat && a.k % 8 == 0 && a.n % 8 == 0 && a.k >= 256 && a.n >= 256 && big >= kUnits / 2 && short_stride(a.ldx) &&
+      short_stride(a.ldy)) {
+    group_wgrad_big<D, O><<<unit_grid(big), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  dim3 grid;
+  const uint64_t wide = (uint64_t)a.groups * ((a.k + 127) / 128) * ((a.n + 127) / 128);
+  if (wide < 2 * kUnits) {
+    if (hipError_t e = tile_grid((uint64_t)a.groups * ((a.k + 63) / 64) * ((a.n + 127) / 128), 256, &grid)) return e;
+    group_wgrad_mid<D, O, 64><<<grid, dim3(256), 0, s>>>(a);
+  } else {
+    if (hipError_t e = tile_grid(wide, 256, &grid)) return e;
+    group_wgrad_mid<D, O, 128><<<grid, dim3(256), 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
 template <typename D, typename O>
 hipError_t pick_mm(bool transpose_w, bool flat, const GroupMmArgs& a, hipStream_t s) {
-  return transpose_w ? pick_mm<D, true, O>(flat, a, s) : pick_mm<D, false, O>(flat, a, s);
-}
-template <typename D, typename O>
-hipError_t pick_wgrad(bool flat, const GroupWgradArgs& a, hipStream_t s) {
-  return flat ? run_wgrad<D, true, O>(a, s) : run_wgrad<D, false, O>(a, s);
+  return transpose_w ? run_mm<D, true, O>(flat, a, s) : run_mm<D, false, O>(flat, a, s);
 }
 
 }  // namespace
@@ -600,8 +502,8 @@ hipError_t launch_group_mm(int dtype, bool out_f32, bool transpose_w, bool flat,
 hipError_t launch_group_wgrad(int dtype, bool out_f32, bool flat, const GroupWgradArgs& a, hipStream_t s) {
   (void)hipGetLastError();
   if (dtype == CIERA_BF16)
-    return out_f32 ? pick_wgrad<Bf16, float>(flat, a, s) : pick_wgrad<Bf16, __bf16>(flat, a, s);
-  return out_f32 ? pick_wgrad<Fp16, float>(flat, a, s) : pick_wgrad<Fp16, _Float16>(flat, a, s);
+    return out_f32 ? run_wgrad<Bf16, float>(flat, a, s) : run_wgrad<Bf16, __bf16>(flat, a, s);
+  return out_f32 ? run_wgrad<Fp16, float>(flat, a, s) : run_wgrad<Fp16, _Float16>(flat, a, s);
 }
 
 }  // namespace ciera

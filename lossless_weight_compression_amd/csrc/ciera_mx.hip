@@ -7,6 +7,7 @@
 // |v| 2^-e, ties to the even code, above 6 the 6 itself, with v's sign in bit 3.
 #include "ciera.h"
 #include "ciera_big.h"
+#include "ciera_mid.h"
 #include "ciera_ops_internal.h"
 #include "ciera_tiles.h"
 
@@ -352,97 +353,23 @@ __global__ __launch_bounds__(256) void mx_dequantize(MxDequantArgs a, RowPass pa
   }
 }
 
-// out = a b^T on the rows of every group: the 4-bit matrix instruction takes 128
-// contraction steps, a lane's 32 codes and their one scale.
-template <typename O, int BM, int BN>
-__global__ __launch_bounds__(256) void mx_mm_general(MxMmArgs a) {
-  constexpr int CH = 4;  // 16-byte chunks (32 codes) of a row per step of 128
-  constexpr int NA = BM * CH / 256, NB = BN * CH / 256, WM = BM / 2 / 16, WN = BN / 2 / 16;
-  __shared__ i32x4 la[2][BM * CH];
-  __shared__ i32x4 lb[2][BN * CH];
+// out = a b^T on the rows of every group.  In units of two bytes (4 codes) the operands
+// look like two-byte ones.
+template <typename O, int BM>
+__global__ __launch_bounds__(256, 2) void mx_mm_mid(MxMmArgs a) {
   GroupTile t;
   int tn;
-  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
-  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
-  const int mleft = t.count - t.m * BM, n0 = tn * BN, nleft = a.n - n0;
-  const uint64_t cb = a.kp / 2, sb = a.kp / 32;  // bytes of a row's codes and scales
-  const uint8_t* pa = a.a + row * cb;
-  const uint8_t* psa = a.sa + row * sb;
-  const uint64_t brow = (uint64_t)t.g * a.n + n0;
-  const uint8_t* pb = a.b + brow * cb;
-  const uint8_t* psb = a.sb + brow * sb;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * (BN / 2);
-  auto pos = [](int r, int c) { return r * CH + (c ^ ((r >> 2) & 3)); };
-
-  i32x4 ra[NA], rb[NB];
-  auto load = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < NA; i++) {
-      const int p = i * 256 + tid, r = p / CH, c = p % CH;
-      ra[i] = r < mleft ? *reinterpret_cast<const i32x4*>(pa + r * cb + s * 64 + c * 16) : i32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int i = 0; i < NB; i++) {
-      const int p = i * 256 + tid, r = p / CH, c = p % CH;
-      rb[i] = r < nleft ? *reinterpret_cast<const i32x4*>(pb + r * cb + s * 64 + c * 16) : i32x4{0, 0, 0, 0};
-    }
-  };
-  auto put = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < NA; i++) la[s][pos((i * 256 + tid) / CH, (i * 256 + tid) % CH)] = ra[i];
-#pragma unroll
-    for (int i = 0; i < NB; i++) lb[s][pos((i * 256 + tid) / CH, (i * 256 + tid) % CH)] = rb[i];
-  };
-  f32x4 acc[WM][WN];
-#pragma unroll
-  for (int i = 0; i < WM; i++)
-#pragma unroll
-    for (int j = 0; j < WN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-  const int steps = a.kp / 128;
-  if (steps) {
-    load(0);
-    put(0);
-  }
-  __syncthreads();
-  for (int s = 0; s < steps; s++) {
-    const bool more = s + 1 < steps;
-    if (more) load(s + 1);
-    const int cur = s & 1;
-    i32x4 fa[WM], fb[WN];
-    int xa[WM], xb[WN];
-#pragma unroll
-    for (int i = 0; i < WM; i++) {
-      const int r = r0 + i * 16 + (lane & 15);
-      fa[i] = la[cur][pos(r, lane >> 4)];
-      xa[i] = r < mleft ? psa[r * sb + s * 4 + (lane >> 4)] : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < WN; j++) {
-      const int r = c0 + j * 16 + (lane & 15);
-      fb[j] = lb[cur][pos(r, lane >> 4)];
-      xb[j] = r < nleft ? psb[r * sb + s * 4 + (lane >> 4)] : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < WM; i++)
-#pragma unroll
-      for (int j = 0; j < WN; j++)
-        acc[i][j] = mfma(fb[j], xb[j], fa[i], xa[i], acc[i][j]);
-    if (more) put(cur ^ 1);
-    __syncthreads();
-  }
-  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
-#pragma unroll
-  for (int i = 0; i < WM; i++) {
-    const int m = r0 + i * 16 + (lane & 15);
-    if (m >= mleft) continue;
-#pragma unroll
-    for (int j = 0; j < WN; j++) store4(out + (uint64_t)m * a.ldo, c0 + j * 16 + (lane >> 4) * 4, nleft, acc[i][j]);
-  }
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + 127) / 128, blockIdx.x, &t, &tn)) return;
+  const int n0 = tn * 128, units = a.kp / 4;
+  const uint32_t srow = a.kp / 32;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM, brow = (uint64_t)t.g * a.n + n0;
+  mid_tile<Mx4, true, true, O, BM>(reinterpret_cast<const uint16_t*>(a.a) + row * units, units, t.count - t.m * BM,
+                                   reinterpret_cast<const uint16_t*>(a.b) + brow * units, units, a.n - n0, units,
+                                   static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, a.sa + row * srow, a.sb + brow * srow,
+                                   srow);
 }
 
-// Large products: 256 x 256 tiles, 256 codes of every row at a time.  In units of two
-// bytes (4 codes) the operands look like two-byte ones.
+// Large products: 256 x 256 tiles, 256 codes of every row at a time.
 template <typename O>
 __global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
   typedef BigTiles<Mx4, true, true, O> Big;
@@ -484,14 +411,14 @@ __global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
   }
 }
 
-// Few rows to a group: 16 rows and 16 * NF columns to a workgroup.  Its 4 waves take
+// Few rows to a group: 16 rows and 16 columns to a workgroup.  Its 4 waves take
 // runs of 512 codes of every row in turn, from memory into registers: a lane 4 blocks
 // and the word of their scales; their sums are joined through LDS in order.
 constexpr int kMxThinWaves = 4;
 
-template <typename O, int NF>
+template <typename O>
 __global__ __launch_bounds__(256) void mx_mm_thin(MxMmArgs a) {
-  constexpr int BN = 16 * NF, LD = BN + 4;
+  constexpr int BN = 16, LD = BN + 4;
   __shared__ __attribute__((aligned(16))) float part[kMxThinWaves * 16 * LD];
   GroupTile t;
   int tn;
@@ -500,52 +427,33 @@ __global__ __launch_bounds__(256) void mx_mm_thin(MxMmArgs a) {
   const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
   const int blocks = a.kp / 32;
-  const i32x4* pw[NF];
-  const uint8_t* psw[NF];
-#pragma unroll
-  for (int f = 0; f < NF; f++) {
-    const uint64_t r = (uint64_t)t.g * a.n + n0 + min(f * 16 + (lane & 15), left - 1);
-    pw[f] = reinterpret_cast<const i32x4*>(a.b) + r * blocks;
-    psw[f] = a.sb + r * blocks;
-  }
+  const uint64_t wr = (uint64_t)t.g * a.n + n0 + min(lane & 15, left - 1);
+  const i32x4* pw = reinterpret_cast<const i32x4*>(a.b) + wr * blocks;
+  const uint8_t* psw = a.sb + wr * blocks;
   const uint64_t xr = row + min(lane & 15, rows - 1);
   const i32x4* px = reinterpret_cast<const i32x4*>(a.a) + xr * blocks;
   const uint8_t* psx = a.sa + xr * blocks;
-  f32x4 acc[NF];
-#pragma unroll
-  for (int f = 0; f < NF; f++) acc[f] = f32x4{0, 0, 0, 0};
+  f32x4 acc = {0, 0, 0, 0};
   for (int b0 = wave * 16; b0 < blocks; b0 += kMxThinWaves * 16) {
     const int b = b0 + q * 4;  // rows hold multiples of 4 blocks: a lane's run is in or out
-    i32x4 w[NF][4], x[4];
-    uint32_t sw[NF], sx = 0;
+    i32x4 w[4], x[4];
+    uint32_t sw = 0, sx = 0;
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-      x[u] = i32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int f = 0; f < NF; f++) w[f][u] = i32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int f = 0; f < NF; f++) sw[f] = 0;
+    for (int u = 0; u < 4; u++) w[u] = x[u] = i32x4{0, 0, 0, 0};
     if (b < blocks) {
 #pragma unroll
-      for (int f = 0; f < NF; f++) {
-#pragma unroll
-        for (int u = 0; u < 4; u++) w[f][u] = pw[f][b + u];
-        sw[f] = *reinterpret_cast<const uint32_t*>(psw[f] + b);
+      for (int u = 0; u < 4; u++) {
+        w[u] = pw[b + u];
+        x[u] = px[b + u];
       }
-#pragma unroll
-      for (int u = 0; u < 4; u++) x[u] = px[b + u];
+      sw = *reinterpret_cast<const uint32_t*>(psw + b);
       sx = *reinterpret_cast<const uint32_t*>(psx + b);
     }
 #pragma unroll
-    for (int u = 0; u < 4; u++)
-#pragma unroll
-      for (int f = 0; f < NF; f++)
-        acc[f] = mfma(w[f][u], (int)(sw[f] >> (8 * u)), x[u], (int)(sx >> (8 * u)), acc[f]);
+    for (int u = 0; u < 4; u++) acc = mfma(w[u], (int)(sw >> (8 * u)), x[u], (int)(sx >> (8 * u)), acc);
   }
   float* mine = part + (wave * 16 + (lane & 15)) * LD + (lane >> 4) * 4;
-#pragma unroll
-  for (int f = 0; f < NF; f++) *reinterpret_cast<f32x4*>(mine + f * 16) = acc[f];
+  *reinterpret_cast<f32x4*>(mine) = acc;
   __syncthreads();
   O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
   for (int p = threadIdx.x; p < 16 * BN / 4; p += kMxThinWaves * 64) {
@@ -564,23 +472,24 @@ uint32_t row_grid(const RowPass& p) { return pass_grid((p.total + 4 * kRun - 1) 
 
 template <typename O>
 hipError_t run_mx_mm(const MxMmArgs& a, hipStream_t s) {
-#ifndef M1
-#define M1 16
-#define M2 128
-#endif
+  // By rows to a group on average; 64 experts of 2048 x 1024, us (1 token over 8 of them:
+  // thin 8, tiles of 64 rows 18):
+  //   rows        4    8   16   24   64  100  128  160  200  256
+  //   thin       18   21   21
+  //   64 rows    14   15   19   19   20   29   32   36   44   52
+  //   256 x 256                                39   38   38   39
+  const int64_t rows = a.rows, groups = a.groups;
+  const uint64_t mid = max_row_tiles(rows, groups, 64) * ((a.n + 127) / 128);
+  const uint64_t big = max_row_tiles(rows, groups, 256) * ((a.n + 255) / 256);
   dim3 grid;
-  if (a.rows <= M1 * (int64_t)a.groups) {
-    const uint64_t mt = max_row_tiles(a.rows, a.groups, 16);
-    const bool wide = mt * ((a.n + 63) / 64) >= 2048;
-    if (hipError_t e = tile_grid(mt * ((a.n + (wide ? 63 : 15)) / (wide ? 64 : 16)), 256, &grid)) return e;
-    if (wide) mx_mm_thin<O, 4><<<grid, dim3(256), 0, s>>>(a);
-    else mx_mm_thin<O, 1><<<grid, dim3(256), 0, s>>>(a);
-  } else if (a.kp && a.rows >= M2 * (int64_t)a.groups && short_stride(a.kp / 4)) {
-    mx_mm_big<O><<<unit_grid(max_row_tiles(a.rows, a.groups, 256) * ((a.n + 255) / 256)), dim3(512), 0, s>>>(a);
+  if (rows <= 16 * groups && mid < kUnits) {
+    if (hipError_t e = tile_grid(max_row_tiles(rows, groups, 16) * ((a.n + 15) / 16), 256, &grid)) return e;
+    mx_mm_thin<O><<<grid, dim3(256), 0, s>>>(a);
+  } else if (a.kp && rows >= 192 * groups && big >= kUnits / 2 && short_stride(a.kp / 4)) {
+    mx_mm_big<O><<<unit_grid(big), dim3(512), 0, s>>>(a);
   } else {
-    constexpr int BM = 128, BN = 128;
-    if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + BN - 1) / BN), 256, &grid)) return e;
-    mx_mm_general<O, BM, BN><<<grid, dim3(256), 0, s>>>(a);
+    if (hipError_t e = tile_grid(mid, 256, &grid)) return e;
+    mx_mm_mid<O, 64><<<grid, dim3(256), 0, s>>>(a);
   }
   return hipGetLastError();
 }

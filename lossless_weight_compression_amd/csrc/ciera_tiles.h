@@ -181,31 +181,72 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
   return true;
 }
 
-// One operand tile in LDS, in 16-byte chunks (8 two-byte values).  KC: the
-// contraction is contiguous in memory; R rows of BK values.  Else BK contraction
-// steps of R contiguous values, read back with the transposing LDS load, whose 16
-// lanes take 8 bytes each, of 4 steps.  The chunks of a line are permuted by the line,
-// so that what the lanes of one LDS cycle read lies in different banks.
-template <bool KC, int R, int BK>
-struct LdsTile {
-  static constexpr int kChunks = R * BK / 8;
-  static constexpr int kPerRow = KC ? BK / 8 : R / 8;
-  static_assert(!KC || BK == 32, "the permutation of rows is made for rows of 4 chunks");
-  static __device__ __forceinline__ int swizzle(int line, int c) {
-    return KC ? c ^ ((line >> 2) & 3) : c ^ (((line & 3) | ((line >> 1) & 4)) << 1);
-  }
-  // position of chunk c of a line (a row, or a contraction step)
-  static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
+// v, as if computed anew here: what depends on it is not kept in registers across the
+// main loop.
+__device__ __forceinline__ int afresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+// LDS writes of this wave's lanes before, reads by others after (and the other way
+// round): the LDS unit takes a wave's accesses in order, the compiler has to.
+__device__ __forceinline__ void wave_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
 
-  // of row r0 + lane % 16 the contraction steps 8 * (lane / 16) ...
-  static __device__ __forceinline__ s16x8 fragment(const i32x4* lds, int r0) {
-    const int lane = threadIdx.x & 63;
-    if (KC) {
-      return __builtin_bit_cast(s16x8, lds[pos(r0 + (lane & 15), lane >> 4)]);
+// One operand of a stage in LDS: R rows, 64 contraction steps of two bytes, in
+// 16-byte chunks.  KC: the contraction is contiguous in memory, 8 chunks to a row; else
+// R / 8 chunks to a contraction step, read back with the transposing load.
+//
+// A fragment is S rows, 16 or 32.  COLS (the operand whose rows are the result's columns):
+// they are taken in an order that gives a lane, which gets 4 of them together as results,
+// 8 consecutive columns.
+//
+// The chunks of a line (a row, or a contraction step) are permuted by the line, so that
+// what the lanes of one LDS cycle read lies in different banks: the same chunk of 8 rows,
+// or pieces of 4 contraction steps.
+template <bool KC, bool COLS, int S, int R = 256>
+struct StageTile {
+  static constexpr int kChunks = R * 8, kPerRow = KC ? 8 : R / 8;
+  static __device__ __forceinline__ int swizzle(int line, int c) {
+    const int k = (line & 3) | ((line >> 1) & 4);
+    if (KC) return c ^ (COLS ? k : line & 7);
+    if (S == 16 && !COLS) return c ^ ((R == 64 ? line & 3 : k) << 1);
+    return c ^ ((line & 3) << 2);
+  }
+  static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
+  // the row of fragment 0 that this lane reads
+  static __device__ __forceinline__ int first_row() {
+    const int v = threadIdx.x & (S - 1);
+    if (!COLS) return v;
+    return S == 16 ? ((v & 12) << 1) + (v & 3) : (v & 16) + ((v >> 2) & 1) * 8 + ((v >> 3) & 1) * 4 + (v & 3);
+  }
+  // Where this lane reads fragment 0 of the rows from r0 on in the first part of the
+  // stage (an address in LDS).  Other fragments and parts lie at that place with bits
+  // flipped and a constant added, which costs no register each.  S = 16: a part is half
+  // a stage, 8 steps of it to each 16 lanes.  S = 32: a part is 8 steps of each half of
+  // the stage, one for each half of the wave.
+  static __device__ __forceinline__ uint32_t place(const i32x4* lds, int r0) {
+    const int lane = threadIdx.x & 63, p = lane & 3;
+    if (KC) return lds_address(lds) + pos(r0 + first_row(), S == 16 ? lane >> 4 : (lane >> 5) * 4) * 16;
+    const int step = (S == 16 ? (lane >> 4) * 8 : (lane >> 5) * 32) + ((lane >> 2) & 3);
+    int c, half;
+    if (S == 16) {
+      c = COLS ? p : p >> 1;
+      half = COLS ? 0 : p & 1;
     } else {
-      const int step = (lane >> 4) * 8 + ((lane & 15) >> 2), c = (r0 >> 3) + ((lane & 3) >> 1);
-      return read_transposed(lds_address(lds) + pos(step, c) * 16 + (lane & 1) * 8, 4 * kPerRow * 16);
+      c = ((lane >> 4) & 1) * 2 + (COLS ? p & 1 : p >> 1);
+      half = COLS ? p >> 1 : p & 1;
     }
+    return lds_address(lds) + pos(step, r0 / 8 + c) * 16 + half * 8;
+  }
+  template <int F, int PART>
+  static __device__ __forceinline__ s16x8 fragment(uint32_t place) {
+    constexpr int ROW = S == 32 ? F * 32 : COLS ? (F >> 1) * 32 + (F & 1) * 4 : F * 16;
+    if constexpr (KC) return read_lds<s16x8>((place ^ (PART * (S == 16 ? 64 : 16))) + ROW * kPerRow * 16);
+    constexpr int FLIP = ROW / 8 * 16, HALF = (ROW & 7) * 2;
+    return read_transposed((place ^ FLIP) + PART * (S == 16 ? 32 : 8) * kPerRow * 16 + HALF, 4 * kPerRow * 16);
   }
 };
 
@@ -222,21 +263,14 @@ __device__ __forceinline__ void each(F f) {
   }
 }
 
-// 8 values of a two-byte matrix from (line, c * 8) on, zeros where the line or
-// the column lies outside: lines of `ld` values at any 2-byte aligned address.
-template <bool FLAT>
-__device__ __forceinline__ i32x4 load_chunk(const uint16_t* base, uint64_t ld, int line, int lines, int col, int cols) {
-  i32x4 v = {0, 0, 0, 0};
-  if (line >= lines || col >= cols) return v;
-  const uint16_t* p = base + (uint64_t)line * ld + col;
-  const int left = cols - col;
-  if (left >= 8) return FLAT ? *reinterpret_cast<const i32x4*>(p) : load16(p);
+// The first `left` of 8 two-byte values, zeros behind.
+__device__ __forceinline__ i32x4 load_some(const uint16_t* p, int left) {
+  if (left >= 8) return load16(p);
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < 8; j++)
     if (j < left) w[j / 2] |= (uint32_t)p[j] << (16 * (j & 1));
-  v[0] = w[0]; v[1] = w[1]; v[2] = w[2]; v[3] = w[3];
-  return v;
+  return i32x4{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
 }
 
 // Consecutive outputs of one row, at any element.

@@ -95,6 +95,96 @@ def test_group_wgrad(shape, dtype, out):
     assert torch.equal(g, again)
 
 
+# Sizes that fill the card: many rows to a group (256 x 256 tiles read straight into LDS)
+# and what only nearly qualifies.  rows, K, N, groups, rows behind the last group
+LARGE = [(4300, 200, 2056, 14, 3), (4200, 8, 2048, 16, 0), (8500, 64, 1032, 33, 7), (4096, 72, 2304, 1, 0),
+         (9001, 128, 1000, 5, 0), (8200, 136, 1024, 32, 100), (6000, 328, 1544, 3, 1), (18000, 40, 520, 70, 11),
+         (4300, 201, 2056, 14, 3), (4300, 200, 2051, 14, 3), (6000, 100, 777, 40, 2)]
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F32)])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("shape", LARGE)
+def test_group_mm_large(shape, transpose, dtype, out):
+    test_group_mm(shape, transpose, dtype, out)
+
+
+# rows, K, N, groups, rows behind the last group: gradients of K x N
+LARGE_GRADS = [(700, 1032, 1288, 8, 3), (3, 2056, 2048, 3, 0), (900, 264, 256, 70, 0), (5000, 1024, 520, 12, 9),
+               (64, 4104, 2048, 1, 0), (1300, 776, 1000, 11, 1), (130, 520, 264, 300, 2), (1300, 777, 1001, 11, 1)]
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F32)])
+@pytest.mark.parametrize("shape", LARGE_GRADS)
+def test_group_wgrad_large(shape, dtype, out):
+    test_group_wgrad(shape, dtype, out)
+
+
+@pytest.mark.parametrize("one", [0, 5, 63, 64, 199])
+def test_group_wgrad_all_rows_in_one_group(one):
+    """All the work in one of many groups, the others' gradients zeros."""
+    say(f"[gpu] wgrad, all rows in group {one}")
+    groups = 64 if one < 64 else 200
+    x, dy = rand((3000, 264), BF, 3), rand((3000, 512), BF, 4, 0.1)
+    offsets = [0] * (one + 1) + [3000] * (groups - one)
+    g = torch.full((groups, 264, 512), 7.0, dtype=F32, device="cuda")
+    L.ciera_group_wgrad(x, dy, g, offsets=off_dev(offsets))
+    want, mag = P.group_wgrad(np64(x), np64(dy), offsets)
+    close(g, want, mag, 3000, F32, "dw")
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("shape", LARGE)
+def test_mx_mm_large(shape, out):
+    test_mx_mm(shape, out)
+
+
+@pytest.mark.parametrize("rows,k,n,groups", [(4300, 200, 2056, 14), (9001, 72, 1032, 5)])
+def test_large_strides_and_neighbours(rows, k, n, groups):
+    """Large tiles out of and into parts of larger buffers: nothing around the output
+    changes, NaN around the operands and in rows of no group reach no result, infinities stay
+    in their rows."""
+    say(f"[gpu] large tiles, strides rows={rows} k={k} n={n}")
+    nan = float("nan")
+    offsets = split(rows, groups, 9, tail=30)
+    off = off_dev(offsets)
+    big_x = torch.full((rows + 2, k + 24), nan, dtype=BF, device="cuda")
+    x = big_x[1:-1, 8:8 + k]
+    x[:rows - 30] = rand((rows - 30, k), BF, 8)
+    big_w = torch.full((groups, k + 3, n + 16), nan, dtype=BF, device="cuda")
+    w = big_w[:, 1:k + 1, 8:8 + n]
+    w.copy_(rand((groups, k, n), BF, 9))
+    big_y = torch.full((rows + 2, n + 19), 7.0, dtype=BF, device="cuda")
+    y = big_y[1:-1, 5:5 + n]
+    ok = slice(0, rows - 30)
+    want, mag = P.group_mm(np64(x), np64(w), offsets, np.full((rows, n), 7.0))
+    L.ciera_group_mm(x, w, y, offsets=off)
+    close(y[ok], want[ok], mag[ok], k, BF, "y")
+    y[ok] = 7.0
+    assert (big_y == 7.0).all()
+    wt = torch.full((groups, n + 1, k + 16), nan, dtype=BF, device="cuda")[:, 1:, 8:8 + k]
+    wt.copy_(w.transpose(1, 2))
+    L.ciera_group_mm(x, wt, y, offsets=off, transpose_w=True)
+    close(y[ok], want[ok], mag[ok], k, BF, "y, [N, K]")
+    y[ok] = 7.0
+    assert (big_y == 7.0).all()
+    x[100, 3], x[700, 0] = float("inf"), nan
+    L.ciera_group_mm(x, w, y, offsets=off)
+    assert (~torch.isfinite(y)).any(1).nonzero().flatten().tolist() == [100, 700]
+    x[100, 3], x[700, 0] = 1.0, 1.0
+    # gradients of [n, k] matrices, in larger ones
+    big_dy = torch.full((rows, n + 8), nan, dtype=BF, device="cuda")
+    dy = big_dy[:, 8:]
+    dy[ok] = rand((rows - 30, n), BF, 10)
+    big_g = torch.full((groups, n + 2, k + 5), 7.0, dtype=F32, device="cuda")
+    g = big_g[:, 1:-1, 3:3 + k]
+    L.ciera_group_wgrad(dy, x, g, offsets=off)
+    want, mag = P.group_wgrad(np64(dy), np64(x), offsets)
+    close(g, want, mag, rows, F32, "dw")
+    g.fill_(7.0)
+    assert (big_g == 7.0).all()
+
+
 @pytest.mark.parametrize("rows", [3, 24, 700])
 def test_sizes_of_nothing(rows):
     say(f"[gpu] K = 0, empty groups, rows={rows}")
@@ -181,11 +271,11 @@ def test_infinities_stay_in_their_rows(rows, k, n):
     assert bad[0].nonzero().tolist() == [[5]] and bad[1].nonzero().tolist() == [[0]]
 
 
+@pytest.mark.parametrize("rows,k,n", [(90, 64, 72), (3000, 520, 3080)])
 @pytest.mark.parametrize("offsets", [[0, 50, 20, 90], [-5, 10, 2000, 60], [90, 60, 30, 0], [2 ** 31 - 1, -2 ** 31, 5, 2 ** 31 - 1]])
-def test_offsets_out_of_order_stay_inside(offsets):
+def test_offsets_out_of_order_stay_inside(offsets, rows, k, n):
     """Unspecified rows, but nothing outside the operands is touched."""
-    say(f"[gpu] offsets {offsets}")
-    rows, k, n = 90, 64, 72
+    say(f"[gpu] offsets {offsets} rows={rows}")
     x, w = rand((rows, k), BF, 14), rand((3, k, n), BF, 15)
     buf = torch.full((rows + 200, n), 7.0, dtype=BF, device="cuda")
     L.ciera_group_mm(x, w, buf[100:100 + rows], offsets=off_dev(offsets))
@@ -333,19 +423,21 @@ def test_mx_mm_nan_scale(rows):
 
 # ---------------------------------------------------------- streams and graphs
 
-def test_on_a_side_stream():
+@pytest.mark.parametrize("rows,k,n", [(300, 512, 256), (6000, 512, 2048)])
+def test_on_a_side_stream(rows, k, n):
     """Every call on a stream other than the current one, beside a call of the same
     kind on the current one: each sees its own operands only."""
-    say("[gpu] side stream")
-    off = off_dev([0, 100, 100, 290])
+    say(f"[gpu] side stream rows={rows}")
+    offsets = [0, rows // 3, rows // 3, rows - 10]
+    off = off_dev(offsets)
     side = torch.cuda.Stream()
     res = {}
     for name in ("main", "side", "again"):
         seed = 50 if name != "side" else 60
-        x, w, dy = rand((300, 512), BF, seed), rand((3, 512, 256), BF, seed + 1), rand((300, 256), BF, seed + 2)
-        res[name] = dict(x=x, w=w, dy=dy, y=torch.zeros(300, 256, dtype=BF, device="cuda"),
-                         g=torch.zeros(3, 512, 256, dtype=F32, device="cuda"), y4=torch.zeros(300, 256, dtype=BF, device="cuda"),
-                         qx=MxMatrix(300, 512), qw=MxMatrix(256, 512, groups=3))
+        x, w, dy = rand((rows, k), BF, seed), rand((3, k, n), BF, seed + 1), rand((rows, n), BF, seed + 2)
+        res[name] = dict(x=x, w=w, dy=dy, y=torch.zeros(rows, n, dtype=BF, device="cuda"),
+                         g=torch.zeros(3, k, n, dtype=F32, device="cuda"), y4=torch.zeros(rows, n, dtype=BF, device="cuda"),
+                         qx=MxMatrix(rows, k), qw=MxMatrix(n, k, groups=3))
     torch.cuda.synchronize()
 
     def go(r, stream):
@@ -362,16 +454,16 @@ def test_on_a_side_stream():
     torch.cuda.synchronize()
     for key in ("y", "g", "y4"):
         assert torch.equal(res["main"][key], res["again"][key]) and not torch.equal(res["main"][key], res["side"][key])
-    want, mag = P.group_mm(np64(res["side"]["x"]), np64(res["side"]["w"]), [0, 100, 100, 290], np.zeros((300, 256)))
-    close(res["side"]["y"], want, mag, 512, BF, "y on the side stream")
+    want, mag = P.group_mm(np64(res["side"]["x"]), np64(res["side"]["w"]), offsets, np.zeros((rows, n)))
+    close(res["side"]["y"], want, mag, k, BF, "y on the side stream")
 
 
-@pytest.mark.parametrize("rows", [8, 700])
-def test_captured_and_replayed(rows):
+@pytest.mark.parametrize("rows,k,n", [(8, 256, 384), (700, 256, 384), (2600, 1024, 3080)])
+def test_captured_and_replayed(rows, k, n):
     """A step of a layer (products, gradients, quantisation, 4-bit product) captured
     once; each replay sees the inputs and offsets of its time and equals the eager calls."""
     say(f"[gpu] graph rows={rows}")
-    k, n, groups = 256, 384, 5
+    groups = 5
     x, w, dy = rand((rows, k), BF, 70), rand((groups, k, n), BF, 71, 0.1), rand((rows, n), BF, 72)
     off = off_dev(split(rows, groups, 1))
     outs = [torch.zeros(rows, n, dtype=BF, device="cuda"), torch.zeros(rows, k, dtype=BF, device="cuda"),
