@@ -9,22 +9,22 @@
 namespace ciera {
 namespace {
 
-template <typename D, bool TRANS, typename O, int BM>
-__global__ __launch_bounds__(256, 2) void group_mm_mid(GroupMmArgs a) {
+template <typename D, bool TRANS, typename O, int BM, int TEAMS>
+__global__ __launch_bounds__(256 * TEAMS, 2) void group_mm_mid(GroupMmArgs a) {
   GroupTile t;
   int tn;
   if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + 127) / 128, blockIdx.x, &t, &tn)) return;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
   // the last tile ends with the matrix: it gives some columns a second time, the same values
   const int n0 = TRANS ? tn * 128 : max(min(tn * 128, a.n - 128), 0);
-  mid_tile<D, true, TRANS, O, BM>(
+  mid_tile<D, true, TRANS, O, BM, TEAMS>(
       static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, t.count - t.m * BM,
       static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, a.n - n0, a.k,
       static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo);
 }
 
-template <typename D, typename O, int BM>
-__global__ __launch_bounds__(256, 2) void group_wgrad_mid(GroupWgradArgs a) {
+template <typename D, typename O, int BM, int TEAMS>
+__global__ __launch_bounds__(256 * TEAMS, 2) void group_wgrad_mid(GroupWgradArgs a) {
   const uint32_t mt = (a.k + BM - 1) / BM, nt = (a.n + 127) / 128;
   uint64_t first;
   uint32_t many;
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256, 2) void group_wgrad_mid(GroupWgradArgs a) {
   group_range(a.offsets, g, a.rows, &begin, &count);
   begin = __builtin_amdgcn_readfirstlane(begin);
   count = __builtin_amdgcn_readfirstlane(count);
-  mid_tile<D, false, false, O, BM>(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
+  mid_tile<D, false, false, O, BM, TEAMS>(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
                                    static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, a.n - n0, count,
                                    static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo);
 }
@@ -47,36 +47,38 @@ __global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
   __shared__ i32x4 lds[BigTiles<D, true, TRANS, O>::kLds];
   GroupTiles<256> tiles;
   tiles.init(a.offsets, a.groups, a.rows);
-  const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds;
-  uint64_t first;
-  uint32_t many;
-  die_run((uint64_t)tiles.total * nt, blockIdx.x % kXcds, &first, &many);
-  uint32_t at = blockIdx.x / kXcds;
-  if (at >= many) return;
+  const uint32_t nt = (a.n + 255) / 256;
+  TileList list;
+  list.init((uint64_t)tiles.total * nt);
   BigTiles<D, true, TRANS, O> big;
   big.init(lds);
   O* out;
   int om, on, half = 0;
-  auto start = [&](uint64_t tile) {
+  // false: no more tiles, or a half without rows
+  auto start = [&](uint32_t i) {
+    uint64_t tile;
+    int r0, rows;
+    if (!list.get(i, &tile, &r0, &rows)) return false;
     const GroupTile t = tiles.find((uint32_t)(tile / nt));
     const int n0 = (int)(tile % nt) * 256;
-    const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256;
-    om = t.count - t.m * 256;
+    const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256 + r0;
+    om = min(t.count - t.m * 256 - r0, rows);
     on = a.n - n0;
+    if (om <= 0) return false;
     out = static_cast<O*>(a.out) + row * a.ldo + n0;
     big.start(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, om,
               static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, on,
               a.k, half);
+    return true;
   };
-  start(first + at);
-  for (;;) {
+  if (!start(0)) return;
+  for (uint32_t i = 1;; i++) {
     big.stages(om, a.k, &half);
     O* done = out;
     const int dm = om, dn = on;
-    at += stride;
-    if (at < many) start(first + at);
+    const bool more = start(i);
     big.finish(done, a.ldo, dm, dn);
-    if (at >= many) return;
+    if (!more) return;
   }
 }
 
@@ -431,11 +433,11 @@ hipError_t run_thin(const GroupMmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename D, bool TRANS, typename O, int BM>
+template <typename D, bool TRANS, typename O, int BM, int TEAMS>
 hipError_t run_mid(const GroupMmArgs& a, hipStream_t s) {
   dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + 127) / 128), 256, &grid)) return e;
-  group_mm_mid<D, TRANS, O, BM><<<grid, dim3(256), 0, s>>>(a);
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + 127) / 128), 256 * TEAMS, &grid)) return e;
+  group_mm_mid<D, TRANS, O, BM, TEAMS><<<grid, dim3(256 * TEAMS), 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -448,21 +450,26 @@ hipError_t run_mm(bool flat, const GroupMmArgs& a, hipStream_t s) {
   //          256 x 256                                 110  107  112  116
   //   [N, K] thin     32   53   66
   //          64 rows  29   41   52   50   51   53   71   83   89  106  113
-  // The thin kernel takes [N, K] only where tiles of 64 x 128 are too few for the card (1
-  // token over 8 of the experts: 10.9 us, 15.3), the 256 x 256 one all that gives it half
-  // the card, the 128 x 128 one what is large but cannot be read straight into LDS (13
-  // groups, 40000 rows, 1447 x 777, fp16: 184 us, in 64 x 128 tiles 219).
+  // The thin kernel takes [N, K], and more rows, only where tiles of 64 x 128 are too few
+  // for the card (1 token over 8 of the experts 10.9 us for 15.3; one matrix 2048 x 7168,
+  // 24 rows 15.6 for 36.7, 64 rows 27.9 for 39.6).  Two teams to a tile where there is one
+  // tile to a unit at most (512 rows, 4096 x 1024: 27.4 us for 30.7).  The 256 x 256 kernel
+  // takes what gives it half the card, the 128 x 128 one what is large but cannot be read
+  // straight into LDS (13 groups, 40000 rows, 1447 x 777, fp16: 184 us for 219).
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t nt = (a.n + 127) / 128;
-  if (rows <= 16 * groups && (!TRANS || max_row_tiles(rows, groups, 64) * nt < kUnits)) return run_thin<D, TRANS, O>(a, s);
+  const uint64_t mid = max_row_tiles(rows, groups, 64) * nt;
+  if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 64 * groups && mid < kUnits / 4))
+    return run_thin<D, TRANS, O>(a, s);
   const uint64_t big = max_row_tiles(rows, groups, 256) * ((a.n + 255) / 256);
   if (flat && a.k && a.k % 8 == 0 && (TRANS || a.n % 8 == 0) && rows >= 256 * groups && big >= kUnits / 2 &&
       short_stride(a.ldx) && short_stride(a.ldw)) {
-    group_mm_big<D, TRANS, O><<<unit_grid(big), dim3(512), 0, s>>>(a);
+    group_mm_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
-  if (rows <= 96 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits) return run_mid<D, TRANS, O, 64>(a, s);
-  return run_mid<D, TRANS, O, 128>(a, s);
+  if (mid < kUnits && a.k >= 512) return run_mid<D, TRANS, O, 64, 2>(a, s);
+  if (rows <= 96 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits) return run_mid<D, TRANS, O, 64, 1>(a, s);
+  return run_mid<D, TRANS, O, 128, 1>(a, s);
 }
 
 template <typename D, typename O>
@@ -470,17 +477,20 @@ hipError_t run_wgrad(bool flat, const GroupWgradArgs& a, hipStream_t s) {
   const uint64_t big = (uint64_t)a.groups * ((a.k + 255) / 256) * ((a.n + 255) / 256);
   if (flat && a.k % 8 == 0 && a.n % 8 == 0 && a.k >= 256 && a.n >= 256 && big >= kUnits / 2 && short_stride(a.ldx) &&
       short_stride(a.ldy)) {
-    group_wgrad_big<D, O><<<unit_grid(big), dim3(512), 0, s>>>(a);
+    group_wgrad_big<D, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
   dim3 grid;
   const uint64_t wide = (uint64_t)a.groups * ((a.k + 127) / 128) * ((a.n + 127) / 128);
   if (wide < 2 * kUnits) {
-    if (hipError_t e = tile_grid((uint64_t)a.groups * ((a.k + 63) / 64) * ((a.n + 127) / 128), 256, &grid)) return e;
-    group_wgrad_mid<D, O, 64><<<grid, dim3(256), 0, s>>>(a);
+    const uint64_t tiles = (uint64_t)a.groups * ((a.k + 63) / 64) * ((a.n + 127) / 128);
+    const bool teams = tiles < kUnits && a.rows >= 256 * (int64_t)a.groups;
+    if (hipError_t e = tile_grid(tiles, teams ? 512 : 256, &grid)) return e;
+    if (teams) group_wgrad_mid<D, O, 64, 2><<<grid, dim3(512), 0, s>>>(a);
+    else group_wgrad_mid<D, O, 64, 1><<<grid, dim3(256), 0, s>>>(a);
   } else {
     if (hipError_t e = tile_grid(wide, 256, &grid)) return e;
-    group_wgrad_mid<D, O, 128><<<grid, dim3(256), 0, s>>>(a);
+    group_wgrad_mid<D, O, 128, 1><<<grid, dim3(256), 0, s>>>(a);
   }
   return hipGetLastError();
 }

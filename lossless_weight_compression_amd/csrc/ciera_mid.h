@@ -18,9 +18,10 @@ struct StageLoad {
   int line, col, left;  // of the first chunk; columns left from there (not KC)
 
   __device__ __forceinline__ void init(const uint16_t* base, uint64_t l, int lines) {
+    const int tid = threadIdx.x & 255;
     ld = l;
-    line = threadIdx.x / Any::kPerRow;
-    col = threadIdx.x % Any::kPerRow * 8;
+    line = tid / Any::kPerRow;
+    col = tid % Any::kPerRow * 8;
     left = lines - col;
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -45,26 +46,49 @@ struct StageLoad {
 };
 
 // One BM x 128 tile of C = A B, 4 waves of BM / 2 x 64.  Stages of 64 contraction steps
-// (256 codes) go from memory into registers, two of them under way, from there into one
-// half of LDS while the other is multiplied.  A has `am` rows left, B `bn` columns.  The
+// (256 codes) go from memory into registers, DEPTH of them under way (4 are no faster than
+// 2), from there into one half of LDS while the other is multiplied.  A has `am` rows left, B `bn` columns.  The
 // loop over whole stages has no branches, so that the compiler can wait for the older
 // stage alone: operands whose contiguous side is not the contraction have to fill the
 // tile for that (the callers move the last tile back to end with the matrix).
 // Scaled operands: sa, sb, `srow` bytes of scales a row.
-template <typename D, bool AKC, bool BKC, typename O, int BM>
+//
+// TEAMS 2: two teams of 4 waves, each with half of the stages; the second one's sums are
+// added to the first's through LDS.  For tiles that are too few to fill the card otherwise.
+template <typename D, bool AKC, bool BKC, typename O, int BM, int TEAMS>
 __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
                                          int klen, O* out, uint64_t ldo, const uint8_t* sa = nullptr,
                                          const uint8_t* sb = nullptr, uint32_t srow = 0) {
-  constexpr int BN = 128, BK = 64, WM = BM / 32, WN = 4, ROWS = BM + BN;
+  constexpr int BN = 128, BK = 64, WM = BM / 32, WN = 4, ROWS = BM + BN, DEPTH = 2;
   typedef StageTile<AKC, false, 16, BM> TA;
   typedef StageTile<BKC, true, 16, BN> TB;
   typedef StageLoad<AKC, BM> LA;
   typedef StageLoad<BKC, BN> LB;
   typedef typename D::V V;
-  __shared__ i32x4 la[2][TA::kChunks];
-  __shared__ i32x4 lb[2][TB::kChunks];
-  __shared__ uint32_t ls[2][D::kScaled ? 2 * ROWS : 1];  // scale words: [half of the stage][row]
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int HALF = TA::kChunks + TB::kChunks;
+  static_assert(2 * HALF >= BM * BN / 4, "the joined sums take the place of a team's stages");
+  __shared__ i32x4 lds[TEAMS * 2 * HALF];
+  __shared__ uint32_t scales[TEAMS * 2][D::kScaled ? 2 * ROWS : 1];  // scale words: [half of the stage][row]
+  const int tid = threadIdx.x & 255, lane = tid & 63, team = TEAMS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  i32x4* const la[2] = {lds + team * 2 * HALF, lds + team * 2 * HALF + HALF};
+  i32x4* const lb[2] = {la[0] + TA::kChunks, la[1] + TA::kChunks};
+  uint32_t* const ls[2] = {scales[team * 2], scales[team * 2 + 1]};
+  // the team's stages; the second one's may be one less, and then end with zeros
+  const int steps = ((klen + BK - 1) / BK + TEAMS - 1) / TEAMS;
+  const int whole = TEAMS == 1 ? klen / BK : max(klen / BK - steps, 0);  // that every team has
+  if (TEAMS > 1 && team) {
+    const uint64_t k = (uint64_t)steps * BK;
+    a += AKC ? k : k * lda;
+    b += BKC ? k : k * ldb;
+    if constexpr (D::kScaled) {
+      sa += steps * 8;
+      sb += steps * 8;
+    }
+    klen = max(klen - steps * BK, 0);
+  } else if (TEAMS > 1) {
+    klen = min(klen, steps * BK);
+  }
   const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * 64;
   LA ga;
   LB gb;
@@ -89,7 +113,7 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
     ga.load(r.a, s * BK, klen);
     gb.load(r.b, s * BK, klen);
     if constexpr (D::kScaled) {
-      r.s[0] = *reinterpret_cast<const uint32_t*>(ps + s * 8);
+      r.s[0] = s * BK < klen ? *reinterpret_cast<const uint32_t*>(ps + s * 8) : 0;
       r.s[1] = s * BK + 32 < klen ? *reinterpret_cast<const uint32_t*>(ps + s * 8 + 4) : 0;
     }
   };
@@ -135,34 +159,41 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
         }
     });
   };
-  const int steps = (klen + BK - 1) / BK;
-  Regs r0s, r1s;
-  if (steps > 0) load(r0s, 0);
-  if (steps > 1) load(r1s, 1);
-  if (steps > 0) put(r0s, 0);
-  __syncthreads();
+  Regs r[DEPTH];  // stage s in r[s % DEPTH], then in half s % 2 of LDS
   int s = 0;
-  const int full = (AKC || am >= BM) && (BKC || bn >= BN) ? klen / BK : 0;
-  for (; s + 3 < full; s += 2) {
-    load_whole(r0s, s + 2);
-    multiply(0);
-    put(r1s, 1);
-    __syncthreads();
-    load_whole(r1s, s + 3);
-    multiply(1);
-    put(r0s, 0);
-    __syncthreads();
+  const int full = (AKC || am >= BM) && (BKC || bn >= BN) ? whole : 0;
+  each<DEPTH>([&](auto i) {
+    if (full >= DEPTH) load_whole(r[i.v], i.v);
+    else if (i.v < steps) load(r[i.v], i.v);
+  });
+  if (steps > 0) put(r[0], 0);
+  __syncthreads();
+  for (; s + 2 * DEPTH - 1 < full; s += DEPTH) {
+    each<DEPTH>([&](auto i) {
+      load_whole(r[i.v], s + i.v + DEPTH);
+      multiply(i.v & 1);
+      put(r[(i.v + 1) % DEPTH], (i.v + 1) & 1);
+      __syncthreads();
+    });
   }
-  for (; s < steps; s += 2) {
-    if (s + 2 < steps) load(r0s, s + 2);
-    multiply(0);
-    if (s + 1 < steps) put(r1s, 1);
+  for (; s < steps; s += DEPTH) {
+    each<DEPTH>([&](auto i) {
+      if (s + i.v >= steps) return;
+      if (s + i.v + DEPTH < steps) load(r[i.v], s + i.v + DEPTH);
+      multiply(i.v & 1);
+      if (s + i.v + 1 < steps) put(r[(i.v + 1) % DEPTH], (i.v + 1) & 1);
+      __syncthreads();
+    });
+  }
+  if constexpr (TEAMS > 1) {
+    // every wave is past its last read of the stages
+    i32x4* sums = lds + wave * (WM * WN * 64) + lane;
+    if (team) {
+      each<WM * WN>([&](auto i) { sums[i.v * 64] = __builtin_bit_cast(i32x4, acc[i.v / WN][i.v % WN]); });
+    }
     __syncthreads();
-    if (s + 1 >= steps) break;
-    if (s + 3 < steps) load(r1s, s + 3);
-    multiply(1);
-    if (s + 2 < steps) put(r0s, 0);
-    __syncthreads();
+    if (team) return;
+    each<WM * WN>([&](auto i) { acc[i.v / WN][i.v % WN] += __builtin_bit_cast(f32x4, sums[i.v * 64]); });
   }
   // a lane: row lane % 16 of each fragment, of its columns 8 * (lane / 16) ... in each 32
   const int n = bn - c0 - (lane >> 4) * 8;

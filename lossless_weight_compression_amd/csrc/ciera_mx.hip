@@ -355,15 +355,16 @@ __global__ __launch_bounds__(256) void mx_dequantize(MxDequantArgs a, RowPass pa
 
 // out = a b^T on the rows of every group.  In units of two bytes (4 codes) the operands
 // look like two-byte ones.
-template <typename O, int BM>
+template <typename O>
 __global__ __launch_bounds__(256, 2) void mx_mm_mid(MxMmArgs a) {
+  constexpr int BM = 64;
   GroupTile t;
   int tn;
   if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + 127) / 128, blockIdx.x, &t, &tn)) return;
   const int n0 = tn * 128, units = a.kp / 4;
   const uint32_t srow = a.kp / 32;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM, brow = (uint64_t)t.g * a.n + n0;
-  mid_tile<Mx4, true, true, O, BM>(reinterpret_cast<const uint16_t*>(a.a) + row * units, units, t.count - t.m * BM,
+  mid_tile<Mx4, true, true, O, BM, 1>(reinterpret_cast<const uint16_t*>(a.a) + row * units, units, t.count - t.m * BM,
                                    reinterpret_cast<const uint16_t*>(a.b) + brow * units, units, a.n - n0, units,
                                    static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, a.sa + row * srow, a.sb + brow * srow,
                                    srow);
@@ -376,38 +377,39 @@ __global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
   __shared__ i32x4 lds[Big::kLds];
   GroupTiles<256> tiles;
   tiles.init(a.offsets, a.groups, a.rows);
-  const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds;
-  uint64_t first;
-  uint32_t many;
-  die_run((uint64_t)tiles.total * nt, blockIdx.x % kXcds, &first, &many);
-  uint32_t at = blockIdx.x / kXcds;
-  if (at >= many) return;
+  const uint32_t nt = (a.n + 255) / 256;
+  TileList list;
+  list.init((uint64_t)tiles.total * nt);
   Big big;
   big.init(lds);
   const int units = a.kp / 4;
   const uint32_t srow = a.kp / 32;
   O* out;
   int om, on, half = 0;
-  auto start = [&](uint64_t tile) {
+  auto start = [&](uint32_t i) {
+    uint64_t tile;
+    int r0, rows;
+    if (!list.get(i, &tile, &r0, &rows)) return false;
     const GroupTile t = tiles.find((uint32_t)(tile / nt));
     const int n0 = (int)(tile % nt) * 256;
-    const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256, brow = (uint64_t)t.g * a.n + n0;
-    om = t.count - t.m * 256;
+    const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 256 + r0, brow = (uint64_t)t.g * a.n + n0;
+    om = min(t.count - t.m * 256 - r0, rows);
     on = a.n - n0;
+    if (om <= 0) return false;
     out = static_cast<O*>(a.out) + row * a.ldo + n0;
     big.scales(a.sa + row * srow, om, a.sb + brow * srow, on, srow);
     big.start(reinterpret_cast<const uint16_t*>(a.a) + row * units, units, om,
               reinterpret_cast<const uint16_t*>(a.b) + brow * units, units, on, units, half);
+    return true;
   };
-  start(first + at);
-  for (;;) {
+  if (!start(0)) return;
+  for (uint32_t i = 1;; i++) {
     big.stages(om, units, &half);
     O* done = out;
     const int dm = om, dn = on;
-    at += stride;
-    if (at < many) start(first + at);
+    const bool more = start(i);
     big.finish(done, a.ldo, dm, dn);
-    if (at >= many) return;
+    if (!more) return;
   }
 }
 
@@ -472,8 +474,9 @@ uint32_t row_grid(const RowPass& p) { return pass_grid((p.total + 4 * kRun - 1) 
 
 template <typename O>
 hipError_t run_mx_mm(const MxMmArgs& a, hipStream_t s) {
-  // By rows to a group on average; 64 experts of 2048 x 1024, us (1 token over 8 of them:
-  // thin 8, tiles of 64 rows 18):
+  // By rows to a group on average; 64 experts of 2048 x 1024, us (where 64 x 128 tiles
+  // leave most of the card idle the thin kernel wins up to 64 rows: one matrix 7168 x 2048,
+  // 24 rows 8.1 for 16.7, 64 rows 11.1 for 17.7; 1 token over 8 experts 8 for 18):
   //   rows        4    8   16   24   64  100  128  160  200  256
   //   thin       18   21   21
   //   64 rows    14   15   19   19   20   29   32   36   44   52
@@ -482,14 +485,14 @@ hipError_t run_mx_mm(const MxMmArgs& a, hipStream_t s) {
   const uint64_t mid = max_row_tiles(rows, groups, 64) * ((a.n + 127) / 128);
   const uint64_t big = max_row_tiles(rows, groups, 256) * ((a.n + 255) / 256);
   dim3 grid;
-  if (rows <= 16 * groups && mid < kUnits) {
+    if ((rows <= 16 * groups && mid < kUnits) || (rows <= 64 * groups && mid < kUnits / 4)) {
     if (hipError_t e = tile_grid(max_row_tiles(rows, groups, 16) * ((a.n + 15) / 16), 256, &grid)) return e;
     mx_mm_thin<O><<<grid, dim3(256), 0, s>>>(a);
   } else if (a.kp && rows >= 192 * groups && big >= kUnits / 2 && short_stride(a.kp / 4)) {
-    mx_mm_big<O><<<unit_grid(big), dim3(512), 0, s>>>(a);
+    mx_mm_big<O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
   } else {
     if (hipError_t e = tile_grid(mid, 256, &grid)) return e;
-    mx_mm_mid<O, 64><<<grid, dim3(256), 0, s>>>(a);
+    mx_mm_mid<O><<<grid, dim3(256), 0, s>>>(a);
   }
   return hipGetLastError();
 }

@@ -74,11 +74,8 @@ inline hipError_t tile_grid(uint64_t tiles, uint32_t threads, dim3* grid) {
   *grid = dim3((uint32_t)g);
   return hipSuccess;
 }
-// One workgroup to a compute unit, fewer if there are fewer tiles.
+// Workgroups of the kernels that take one compute unit each.
 constexpr uint32_t kUnits = 256;
-inline dim3 unit_grid(uint64_t tiles) {
-  return dim3((uint32_t)(tiles < kUnits ? (tiles + kXcds - 1) / kXcds * kXcds : kUnits));
-}
 
 // dtype: ciera_dtype_t of x; out_f32: the output is fp32 instead of x's type.
 // flat: every operand row is 16-byte aligned (base, strides).

@@ -99,7 +99,8 @@ def test_group_wgrad(shape, dtype, out):
 # and what only nearly qualifies.  rows, K, N, groups, rows behind the last group
 LARGE = [(4300, 200, 2056, 14, 3), (4200, 8, 2048, 16, 0), (8500, 64, 1032, 33, 7), (4096, 72, 2304, 1, 0),
          (9001, 128, 1000, 5, 0), (8200, 136, 1024, 32, 100), (6000, 328, 1544, 3, 1), (18000, 40, 520, 70, 11),
-         (4300, 201, 2056, 14, 3), (4300, 200, 2051, 14, 3), (6000, 100, 777, 40, 2)]
+         (4300, 201, 2056, 14, 3), (4300, 200, 2051, 14, 3), (6000, 100, 777, 40, 2), (700, 1100, 136, 4, 2),
+         (520, 576, 300, 2, 0), (2200, 1447, 777, 13, 5)]
 
 
 @pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F32)])
@@ -111,7 +112,8 @@ def test_group_mm_large(shape, transpose, dtype, out):
 
 # rows, K, N, groups, rows behind the last group: gradients of K x N
 LARGE_GRADS = [(700, 1032, 1288, 8, 3), (3, 2056, 2048, 3, 0), (900, 264, 256, 70, 0), (5000, 1024, 520, 12, 9),
-               (64, 4104, 2048, 1, 0), (1300, 776, 1000, 11, 1), (130, 520, 264, 300, 2), (1300, 777, 1001, 11, 1)]
+               (64, 4104, 2048, 1, 0), (1300, 776, 1000, 11, 1), (130, 520, 264, 300, 2), (1300, 777, 1001, 11, 1),
+               (2006, 515, 777, 7, 9), (1500, 130, 64, 5, 0), (300, 100, 130, 1, 0)]
 
 
 @pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F32)])
