@@ -397,7 +397,7 @@ typedef struct {
  *     0 .5 1 1.5 2 3 4 6; 16-byte aligned
  *   scales [groups][rows][kp / 32]: byte s of a block stands for 2^(s - 127),
  *     255 for NaN; 4-byte aligned
- * both dense.  Codes past cols are zero. */
+ * both dense.  Codes past cols are zero, and no scale of a block past cols is 255. */
 typedef struct {
   uint8_t* codes;
   uint8_t* scales;
@@ -430,7 +430,7 @@ ciera_status_t ciera_mx_dequantize(const ciera_mx_t* q, const ciera_matrix_t* ou
  * offsets[groups] on are left as they were.  NULL, allowed for one group,
  * gives it every row.  The array is read on the device: offsets out of order
  * or range leave out unspecified, but nothing outside the operands is read or
- * written.
+ * written.  At most 65536 groups (UNSUPPORTED beyond).
  *
  * ciera_mx_mm -- out[i, n] = sum_k a[i, k] b_g[n, k] for the group g of row i:
  * a has one group, rows x K; b groups x N x K; out rows x N, of any type. */

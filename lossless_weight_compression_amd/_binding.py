@@ -437,7 +437,12 @@ def mx_item(codes, scales, groups: int, rows: int, cols: int) -> Mx:
 
 
 def _mx(q) -> Mx:
-    return q if isinstance(q, Mx) else q.item
+    """The Mx of an MxMatrix on the current device (an Mx is passed through)."""
+    if type(q) is Mx:
+        return q
+    if q.codes.get_device() != torch.cuda.current_device():
+        _on_current_device(q.codes, "4-bit matrix")
+    return q.item
 
 
 def _offsets(offsets, groups: int) -> Optional[int]:

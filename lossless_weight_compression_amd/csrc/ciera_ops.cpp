@@ -13,6 +13,7 @@ namespace {
 typedef unsigned __int128 u128;
 
 constexpr uint64_t kMaxSide = (uint64_t)1 << 30;  // sides and their rounding up to a tile are 32-bit counts
+constexpr uint32_t kMaxGroups = 65536;          // of a product: every workgroup adds up their tiles
 constexpr uint64_t kMaxExtent = (uint64_t)1 << 60;
 
 uint32_t elem_bytes(uint32_t dt) { return dt == CIERA_FP32 ? 4u : 2u; }
@@ -135,6 +136,7 @@ ciera_status_t ciera_mx_mm(const ciera_mx_t* a, const ciera_mx_t* b, const int32
   if (ciera_status_t e = check_matrix(out, true, &ro)) return e;
   if (a->groups != 1 || out->groups != 1 || a->cols != b->cols || out->rows != a->rows || out->cols != b->rows)
     return CIERA_ERR_INVALID_ARG;
+  if (b->groups > kMaxGroups) return CIERA_ERR_UNSUPPORTED;
   if (b->groups == 0 || empty(out)) return CIERA_OK;
   if (bad_offsets(offsets, b->groups)) return CIERA_ERR_INVALID_ARG;
   if (bad_data(out) || bad_data(a, ac) || bad_data(b, bc)) return CIERA_ERR_INVALID_ARG;
@@ -156,6 +158,7 @@ ciera_status_t ciera_group_mm(const ciera_matrix_t* x, const ciera_matrix_t* w, 
   const uint64_t wk = transpose_w ? w->cols : w->rows, wn = transpose_w ? w->rows : w->cols;
   if (x->groups != 1 || out->groups != 1 || wk != x->cols || out->rows != x->rows || out->cols != wn)
     return CIERA_ERR_INVALID_ARG;
+  if (w->groups > kMaxGroups) return CIERA_ERR_UNSUPPORTED;
   if (w->groups == 0 || empty(out)) return CIERA_OK;
   if (bad_offsets(offsets, w->groups)) return CIERA_ERR_INVALID_ARG;
   if (bad_data(x) || bad_data(w) || bad_data(out)) return CIERA_ERR_INVALID_ARG;
@@ -176,6 +179,7 @@ ciera_status_t ciera_group_wgrad(const ciera_matrix_t* x, const ciera_matrix_t* 
     return CIERA_ERR_INVALID_ARG;
   if (x->groups != 1 || dy->groups != 1 || dy->rows != x->rows || out->rows != x->cols || out->cols != dy->cols)
     return CIERA_ERR_INVALID_ARG;
+  if (out->groups > kMaxGroups) return CIERA_ERR_UNSUPPORTED;
   if (empty(out)) return CIERA_OK;
   if (bad_offsets(offsets, out->groups)) return CIERA_ERR_INVALID_ARG;
   if (bad_data(x) || bad_data(dy) || bad_data(out)) return CIERA_ERR_INVALID_ARG;

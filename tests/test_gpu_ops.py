@@ -255,6 +255,50 @@ def test_strides_and_neighbours(rows, k, n):
             assert (big_g == 7.0).all()
 
 
+@pytest.mark.parametrize("groups", [65, 3000])
+def test_many_groups(groups):
+    """More groups than a wave adds up at once, most of them empty or of one row."""
+    say(f"[gpu] {groups} groups")
+    rows, k, n = groups + 900, 40, 24
+    offsets = split(rows, groups, 3, tail=2)
+    off = off_dev(offsets)
+    x, w, dy = rand((rows, k), BF, 24), rand((groups, k, n), BF, 25), rand((rows, n), BF, 26)
+    y = torch.full((rows, n), 7.0, dtype=BF, device="cuda")
+    L.ciera_group_mm(x, w, y, offsets=off)
+    want, mag = P.group_mm(np64(x), np64(w), offsets, np.full((rows, n), 7.0))
+    close(y, want, mag, k, BF, "y")
+    g = torch.full((groups, k, n), 7.0, dtype=BF, device="cuda")
+    L.ciera_group_wgrad(x, dy, g, offsets=off)
+    want, mag = P.group_wgrad(np64(x), np64(dy), offsets)
+    close(g, want, mag, rows, BF, "dw")
+    qx, qw = MxMatrix(rows, k).quantize(x), MxMatrix(n, k, groups=groups).quantize(w, axis=0)
+    y.fill_(7.0)
+    L.ciera_mx_mm(qx, qw, y, offsets=off)
+    want, mag = P.group_mm(mx64(qx)[0], mx64(qw).transpose(0, 2, 1), offsets, np.full((rows, n), 7.0))
+    close(y, want, mag, k, BF, "4-bit y")
+
+
+def test_one_row_for_all():
+    """x and dy as one row repeated (stride 0), and every operand the same memory."""
+    say("[gpu] broadcast rows")
+    for rows in (40, 700, 5000):
+        x, dy = rand((1, 256), BF, 27).expand(rows, 256), rand((1, 264), BF, 28).expand(rows, 264)
+        w, offsets = rand((2, 256, 2056), BF, 29), [0, rows // 3, rows]
+        y = torch.zeros(rows, 2056, dtype=BF, device="cuda")
+        L.ciera_group_mm(x, w, y, offsets=off_dev(offsets))
+        want, mag = P.group_mm(np64(x), np64(w), offsets, np.zeros((rows, 2056)))
+        close(y, want, mag, 256, BF, "y")
+        g = torch.zeros(2, 256, 264, dtype=F32, device="cuda")
+        L.ciera_group_wgrad(x, dy, g, offsets=off_dev(offsets))
+        want, mag = P.group_wgrad(np64(x), np64(dy), offsets)
+        close(g, want, mag, rows, F32, "dw")
+    s = rand((256, 256), BF, 30)
+    y = torch.zeros(256, 256, dtype=F32, device="cuda")
+    L.ciera_group_mm(s, s, y, transpose_w=True)
+    want, mag = P.group_mm(np64(s), np64(s).T[None], [0, 256], np.zeros((256, 256)))
+    close(y, want, mag, 256, F32, "s s^T")
+
+
 @pytest.mark.parametrize("rows,k,n", [(9, 64, 64), (300, 128, 264), (300, 129, 70)])
 def test_infinities_stay_in_their_rows(rows, k, n):
     say(f"[gpu] infinities rows={rows} k={k} n={n}")
@@ -551,6 +595,12 @@ def test_layer_from_streams_to_products():
     # the 4-bit copy of the same weights and its product
     qg = codec.quantize(range(0, 3 * groups, 3), axis=0)
     check_quantised(gate, 0, qg, "gate")
+    check_quantised(down, 1, codec.quantize(range(2, 3 * groups, 3), axis=1), "down, along the rows")
+    again = MxMatrix(dff, dm, groups=groups)
+    assert codec.quantize(range(0, 3 * groups, 3), into=again) is again and torch.equal(again.codes, qg.codes)
+    gap = torch.zeros(groups, dm + 1, dff, dtype=BF, device="cuda")[:, 1:]  # matrices with gaps between them
+    MxMatrix(dm, dff, groups=groups).quantize(gate).dequantize(gap)
+    assert torch.equal(gap, MxMatrix(dm, dff, groups=groups).quantize(gate.contiguous()).dequantize())
     qx = MxMatrix(rows, dm).quantize(x)
     y4 = new(dff)
     L.ciera_mx_mm(qx, qg, y4, offsets=off)

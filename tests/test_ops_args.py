@@ -46,6 +46,7 @@ def test_group_mm_refusals():
     call(out=mat(W - 2 * 8 * 24 + 2, 8, 24))               # ends in w's first element
     call(x=mat(X, 1 << 30, 16), out=mat(OUT, 1 << 30, 24), code=3)
     call(x=mat(X, 8, 16, ld=1 << 62), code=3)
+    call(w=mat(W, 16, 24, groups=65537), code=3)           # more groups than a product takes
 
 
 def test_group_wgrad_refusals():
@@ -64,6 +65,7 @@ def test_group_wgrad_refusals():
     call(dy=mat(0, 8, 24))
     call(out=mat(X, 16, 24, groups=3))
     call(x=mat(X, 8, 1 << 30), out=mat(OUT, 1 << 30, 24, groups=3), code=3)
+    call(out=mat(OUT, 16, 24, groups=65537), code=3)
 
 
 def test_mx_refusals():
@@ -101,6 +103,7 @@ def test_mx_refusals():
     mm(out=mat(0x300000, 8, 24))
     mm(out=mat(0x200000 + 8 * 4 - 2, 8, 24))
     mm(a=L.Mx(0x100000, 0x200000, 1, 0, 1 << 30, 100), out=mat(OUT, 1 << 30, 24), code=3)
+    mm(b=L.Mx(0x300000, 0x4000000, 65537, 0, 24, 100), code=3)
     for args in ((1 << 30, 1, 1), (1, 1 << 30, 1), (1, 1, 1 << 30), ((1 << 30) - 1, (1 << 30) - 1, 128)):
         with pytest.raises(L.CieraError) as e:
             L.ciera_mx_sizes(*args)
@@ -149,3 +152,33 @@ def test_binding_refuses_tensors_it_would_misread():
     assert L.matrix_item(m) is m
     with pytest.raises(ValueError, match="dtype"):
         L.ciera_group_mm(m, mat(W, 16, 24), mat(OUT, 8, 24), offsets=torch.zeros(2, dtype=torch.int64), stream=0)
+
+
+def test_binding_refuses_another_device(monkeypatch):
+    """Operands that lie on a device other than the current one."""
+    class Elsewhere:
+        dtype, shape, is_cuda, device = torch.bfloat16, (8, 16), True, torch.device("cuda", 1)
+        stride = staticmethod(lambda *a: (16, 1)[a[0]] if a else (16, 1))
+        numel = staticmethod(lambda: 128)
+        data_ptr = staticmethod(lambda: X)
+        get_device = staticmethod(lambda: 1)
+        is_contiguous = staticmethod(lambda: True)
+        element_size = staticmethod(lambda: 1)
+
+    class Quantised:
+        codes, item = Elsewhere(), L.Mx(0x100000, 0x200000, 1, 0, 8, 16)
+
+    class Offsets(Elsewhere):
+        dtype = torch.int32
+        numel = staticmethod(lambda: 2)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    m = mat(X, 8, 16)
+    for call in (lambda: L.matrix_item(Elsewhere(), "x"),
+                 lambda: L.ciera_mx_quantize(m, Quantised(), stream=0),
+                 lambda: L.ciera_mx_dequantize(Quantised(), m, stream=0),
+                 lambda: L.ciera_group_mm(m, mat(W, 16, 24), mat(OUT, 8, 24), offsets=Offsets(), stream=0)):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert L.matrix_item(Elsewhere(), "x").rows == 8
