@@ -53,7 +53,7 @@ __device__ __forceinline__ void store_past(O* at, const P& p) {
 template <typename D, bool AKC, bool BKC>
 struct WaveTile16 {
   typedef StageTile<AKC, false, 16> TA;
-  typedef StageTile<BKC, true, 16> TB;
+  typedef StageTile<BKC, false, 16> TB;
   typedef typename D::V V;
   static constexpr bool kScaled = false;
   f32x4 acc[8][4];
@@ -87,10 +87,10 @@ struct WaveTile16 {
 
   // Results to `out`, where the wave's first one belongs: `om` rows and `on` columns
   // (WHOLE: all).  A lane has row lane % 16 of each fragment and of its columns
-  // 8 * (lane / 16) ... in each 32.  Through LDS (kTurn chunks of the wave's own) rows of 128
+  // 4 * (lane / 16) ... in each 16.  Through LDS (kTurn chunks of the wave's own) rows of 128
   // bytes, 64 columns or 32 in fp32, are made of them, 16 at a time, so that 8 lanes
-  // store a whole line; stored as they lie, 64 bytes of a row to an instruction, 64 experts
-  // of 2048 x 1024 took 294 us for 285 (input gradient 310 for 291).
+  // store a whole line (stored directly, 64 bytes of a row to an instruction, 64 experts
+  // of 2048 x 1024 took 294 us for 285, the input gradient 310 for 291).
   static constexpr int kTurn = 128;
   template <bool WHOLE, typename O>
   __device__ __forceinline__ void store(O* out, uint64_t ldo, int om, int on, i32x4* turn) {
@@ -99,19 +99,19 @@ struct WaveTile16 {
     each<8 * SPLIT>([&](auto step) {
       constexpr int I = step.v / SPLIT, J = step.v % SPLIT * 2;
 #pragma unroll
-      for (int c = 0; c < 2; c++) {  // two-byte types: of the two 32 columns; fp32: of 8 columns
-        Pack<O, PER> p;
+      for (int j = 0; j < 4 / SPLIT; j++) {
+        const int at = SPLIT == 1 ? j * 2 + (q >> 1) : j * 4 + q;
+        Pack<O, 4> p;
 #pragma unroll
-        for (int e = 0; e < PER; e++)
-          p.v[e] = (O)(SPLIT == 1 ? acc[I][c * 2 + e / 4][e & 3] : acc[I][J + c][e & 3]);
-        const int at = SPLIT == 1 ? c * 4 + q : q * 2 + c;
-        turn[row * 8 + (at ^ (row & 7))] = __builtin_bit_cast(i32x4, p);
+        for (int e = 0; e < 4; e++) p.v[e] = (O)acc[I][J + j][e];
+        char* to = reinterpret_cast<char*>(turn + row * 8 + (at ^ (row >> 1)));
+        __builtin_memcpy(__builtin_assume_aligned(to + (SPLIT == 1 ? (q & 1) * 8 : 0), 8 * SPLIT), &p, sizeof(p));
       }
       wave_order();
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         const int r = t * 8 + (l >> 3), m = I * 16 + r, n = J * 16 + chunk * PER;
-        const Pack<O, PER> p = __builtin_bit_cast(Pack<O, PER>, turn[r * 8 + (chunk ^ (r & 7))]);
+        const Pack<O, PER> p = __builtin_bit_cast(Pack<O, PER>, turn[r * 8 + (chunk ^ (r >> 1))]);
         O* at = out + (uint64_t)m * ldo + n;
         if (WHOLE || (m < om && n + PER <= on)) {
           store_past(at, p);

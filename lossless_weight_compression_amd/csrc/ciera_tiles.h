@@ -204,13 +204,16 @@ __device__ __forceinline__ void wave_order() {
 // 8 consecutive columns.
 //
 // The chunks of a line (a row, or a contraction step) are permuted by the line, so that
-// what the lanes of one LDS cycle read lies in different banks: the same chunk of 8 rows,
-// or pieces of 4 contraction steps.
+// what the lanes of one LDS cycle read lies in different banks: pieces of 4 contraction
+// steps, or chunks of 16 lanes, which are not neighbours (0-3, 12-15, 20-23 and 24-27, and
+// so on): with 32 rows to a fragment, even rows 0 2 12 14 20 22 24 26 and their odd
+// neighbours need 8 different places.
 template <bool KC, bool COLS, int S, int R = 256>
 struct StageTile {
   static constexpr int kChunks = R * 8, kPerRow = KC ? 8 : R / 8;
   static __device__ __forceinline__ int swizzle(int line, int c) {
     const int k = (line & 3) | ((line >> 1) & 4);
+    if (KC && S == 32) return c ^ (((line >> 1) & (COLS ? 1 : 3)) | (COLS ? (line >> 2) & 2 : 0) | ((line >> 2) & 4));
     if (KC) return c ^ (COLS ? k : line & 7);
     if (S == 16 && !COLS) return c ^ ((R == 64 ? line & 3 : k) << 1);
     return c ^ ((line & 3) << 2);
