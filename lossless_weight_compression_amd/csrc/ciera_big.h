@@ -55,7 +55,6 @@ struct WaveTile16 {
   typedef StageTile<AKC, false, 16> TA;
   typedef StageTile<BKC, false, 16> TB;
   typedef typename D::V V;
-  static constexpr bool kScaled = false;
   f32x4 acc[8][4];
   V fa[2][4], fb[2][4];
   uint32_t pa, pb;
@@ -133,7 +132,6 @@ struct WaveTile16 {
 struct WaveTile32 {
   typedef StageTile<true, false, 32> TA;
   typedef StageTile<true, true, 32> TB;
-  static constexpr bool kScaled = true;
   f32x16 acc[4][2];
   i32x4 fa[2][4], fb[2][2];
   int xa[4], xb[2], yb[2];  // scale words; yb: of the next stage

@@ -54,7 +54,8 @@ struct StageLoad {
 // Scaled operands: sa, sb, `srow` bytes of scales a row.
 //
 // TEAMS 2: two teams of 4 waves, each with half of the stages; the second one's sums are
-// added to the first's through LDS.  For tiles that are too few to fill the card otherwise.
+// added to the first's through LDS.  For two-byte tiles that are too few to fill the card
+// otherwise.
 template <typename D, bool AKC, bool BKC, typename O, int BM, int TEAMS>
 __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
                                          int klen, O* out, uint64_t ldo, const uint8_t* sa = nullptr,
@@ -65,6 +66,7 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
   typedef StageLoad<AKC, BM> LA;
   typedef StageLoad<BKC, BN> LB;
   typedef typename D::V V;
+  static_assert(TEAMS == 1 || !D::kScaled, "one team for scaled operands");
   constexpr int HALF = TA::kChunks + TB::kChunks;
   static_assert(2 * HALF >= BM * BN / 4, "the joined sums take the place of a team's stages");
   __shared__ i32x4 lds[TEAMS * 2 * HALF];
@@ -81,10 +83,6 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
     const uint64_t k = (uint64_t)steps * BK;
     a += AKC ? k : k * lda;
     b += BKC ? k : k * ldb;
-    if constexpr (D::kScaled) {
-      sa += steps * 8;
-      sb += steps * 8;
-    }
     klen = max(klen - steps * BK, 0);
   } else if (TEAMS > 1) {
     klen = min(klen, steps * BK);

@@ -488,7 +488,7 @@ hipError_t run_mx_mm(const MxMmArgs& a, hipStream_t s) {
   const uint64_t mid = max_row_tiles(rows, groups, 64) * ((a.n + 127) / 128);
   const uint64_t big = max_row_tiles(rows, groups, 256) * ((a.n + 255) / 256);
   dim3 grid;
-    if ((rows <= 16 * groups && mid < kUnits) || (rows <= 64 * groups && mid < kUnits / 4)) {
+  if ((rows <= 16 * groups && mid < kUnits) || (rows <= 64 * groups && mid < kUnits / 4)) {
     if (hipError_t e = tile_grid(max_row_tiles(rows, groups, 16) * ((a.n + 15) / 16), 256, &grid)) return e;
     mx_mm_thin<O><<<grid, dim3(256), 0, s>>>(a);
   } else if (a.kp && rows >= 192 * groups && big >= kUnits / 2 && short_stride(a.kp / 4)) {

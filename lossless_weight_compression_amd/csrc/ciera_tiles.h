@@ -34,14 +34,6 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
 __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-
-// 32 x 32 results over 16 steps
-__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
-}
 // 16 x 16 results over 128 steps: a lane's 32 codes and their scale, in the lowest byte.
 __device__ __forceinline__ f32x4 mfma(i32x4 a, int scale_a, i32x4 b, int scale_b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8{a[0], a[1], a[2], a[3], 0, 0, 0, 0},
@@ -199,7 +191,7 @@ __device__ __forceinline__ void wave_order() {
 // 16-byte chunks.  KC: the contraction is contiguous in memory, 8 chunks to a row; else
 // R / 8 chunks to a contraction step, read back with the transposing load.
 //
-// A fragment is S rows, 16 or 32.  COLS (the operand whose rows are the result's columns):
+// A fragment is S rows, 16 or (4-bit operands, which are KC) 32.  COLS (the operand whose rows are the result's columns):
 // they are taken in an order that gives a lane, which gets 4 of them together as results,
 // 8 consecutive columns.
 //
@@ -210,12 +202,13 @@ __device__ __forceinline__ void wave_order() {
 // neighbours need 8 different places.
 template <bool KC, bool COLS, int S, int R = 256>
 struct StageTile {
+  static_assert(KC || S == 16, "32 rows are read back along the contraction only");
   static constexpr int kChunks = R * 8, kPerRow = KC ? 8 : R / 8;
   static __device__ __forceinline__ int swizzle(int line, int c) {
     const int k = (line & 3) | ((line >> 1) & 4);
     if (KC && S == 32) return c ^ (((line >> 1) & (COLS ? 1 : 3)) | (COLS ? (line >> 2) & 2 : 0) | ((line >> 2) & 4));
     if (KC) return c ^ (COLS ? k : line & 7);
-    if (S == 16 && !COLS) return c ^ ((R == 64 ? line & 3 : k) << 1);
+    if (!COLS) return c ^ ((R == 64 ? line & 3 : k) << 1);
     return c ^ ((line & 3) << 2);
   }
   static __device__ __forceinline__ int pos(int line, int c) { return line * kPerRow + swizzle(line, c); }
@@ -233,15 +226,7 @@ struct StageTile {
   static __device__ __forceinline__ uint32_t place(const i32x4* lds, int r0) {
     const int lane = threadIdx.x & 63, p = lane & 3;
     if (KC) return lds_address(lds) + pos(r0 + first_row(), S == 16 ? lane >> 4 : (lane >> 5) * 4) * 16;
-    const int step = (S == 16 ? (lane >> 4) * 8 : (lane >> 5) * 32) + ((lane >> 2) & 3);
-    int c, half;
-    if (S == 16) {
-      c = COLS ? p : p >> 1;
-      half = COLS ? 0 : p & 1;
-    } else {
-      c = ((lane >> 4) & 1) * 2 + (COLS ? p & 1 : p >> 1);
-      half = COLS ? p >> 1 : p & 1;
-    }
+    const int step = (lane >> 4) * 8 + ((lane >> 2) & 3), c = COLS ? p : p >> 1, half = COLS ? 0 : p & 1;
     return lds_address(lds) + pos(step, r0 / 8 + c) * 16 + half * 8;
   }
   template <int F, int PART>
@@ -249,7 +234,7 @@ struct StageTile {
     constexpr int ROW = S == 32 ? F * 32 : COLS ? (F >> 1) * 32 + (F & 1) * 4 : F * 16;
     if constexpr (KC) return read_lds<s16x8>((place ^ (PART * (S == 16 ? 64 : 16))) + ROW * kPerRow * 16);
     constexpr int FLIP = ROW / 8 * 16, HALF = (ROW & 7) * 2;
-    return read_transposed((place ^ FLIP) + PART * (S == 16 ? 32 : 8) * kPerRow * 16 + HALF, 4 * kPerRow * 16);
+    return read_transposed((place ^ FLIP) + PART * 32 * kPerRow * 16 + HALF, 4 * kPerRow * 16);
   }
 };
 
