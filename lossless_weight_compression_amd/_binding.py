@@ -150,8 +150,6 @@ _lib = _load()
 
 import torch  # noqa: E402  (after _load, which says why it comes first)
 
-# handle of a device's current stream, without the Stream object around it
-_raw_stream = torch._C._cuda_getCurrentRawStream
 _TORCH_CODES = {torch.bfloat16: CIERA_BF16, torch.float32: CIERA_FP32, torch.float16: CIERA_FP16}
 
 
@@ -198,7 +196,8 @@ def _u8(t, what: str, min_numel: int) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        # the handle without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
