@@ -455,7 +455,7 @@ hipError_t run_mm(bool flat, const GroupMmArgs& a, hipStream_t s) {
   // 24 rows 15.6 for 36.7, 64 rows 27.9 for 39.6).  Two teams to a tile where there is one
   // tile to a unit at most (512 rows, 4096 x 1024: 27.4 us for 30.7).  The 256 x 256 kernel
   // takes what gives it half the card, the 128 x 128 one what is large but cannot be read
-  // straight into LDS (13 groups, 40000 rows, 1447 x 777, fp16: 184 us for 219).
+  // straight into LDS (13 groups, 40000 rows, 1447 x 777, fp16: 177 us for 213).
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t nt = (a.n + 127) / 128;
   const uint64_t mid = max_row_tiles(rows, groups, 64) * nt;
