@@ -75,6 +75,8 @@ struct Fp32In {
 };
 
 // 8 consecutive values as words, those from `left` on as zeros.
+// (A branch to each of the last ones: 400000 rows of 31 values, bf16, 32.6 us for 24.2,
+// 40000 of 1447 29.9 for 25.8.)
 template <typename I>
 __device__ __forceinline__ void load8(const typename I::T* p, int left, uint32_t* w) {
   constexpr int N = 8 / I::kPer;
@@ -89,9 +91,13 @@ __device__ __forceinline__ void load8(const typename I::T* p, int left, uint32_t
   }
 #pragma unroll
   for (int i = 0; i < N; i++) w[i] = 0;
+  if (left <= 0) return;
+  // all at once, the last one again in place of those behind it
+  typename I::T v[8];
 #pragma unroll
-  for (int j = 0; j < 8; j++)
-    if (j < left) w[j / I::kPer] |= (uint32_t)p[j] << (I::kPer == 2 ? 16 * (j & 1) : 0);
+  for (int j = 0; j < 8; j++) v[j] = p[min(j, left - 1)];
+#pragma unroll
+  for (int j = 0; j < 8; j++) w[j / I::kPer] |= (j < left ? (uint32_t)v[j] : 0) << (I::kPer == 2 ? 16 * (j & 1) : 0);
 }
 
 // Largest magnitude of N words of one block's values, as one value.
