@@ -300,18 +300,16 @@ __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
       }
       s.x = load16(x + k);
     } else {
+      // all at once: outside the matrix its last row or column again, then zeros
 #pragma unroll
-      for (int j = 0; j < 8; j++)
+      for (int j = 0; j < 8; j++) {
+        const uint16_t* p = w + (uint64_t)min(k + j, a.k - 1) * a.ldw - c;
 #pragma unroll
         for (int i = 0; i < W; i++) {
-          uint32_t v = 0;
-          if (k + j < a.k) {
-            const uint16_t* p = w + (uint64_t)(k + j) * a.ldw + 2 * i;
-            if (c + 2 * i < left) v = p[0];
-            if (c + 2 * i + 1 < left) v |= (uint32_t)p[1] << 16;
-          }
-          s.w[j][i] = v;
+          const uint32_t lo = p[min(c + 2 * i, left - 1)], hi = p[min(c + 2 * i + 1, left - 1)];
+          s.w[j][i] = (k + j < a.k && c + 2 * i < left ? lo : 0) | (k + j < a.k && c + 2 * i + 1 < left ? hi << 16 : 0);
         }
+      }
       s.x = load_some(x + k, a.k - k);
     }
   };
