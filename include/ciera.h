@@ -380,8 +380,8 @@ ciera_status_t ciera_cache_update(const ciera_tensor_t* t, const void* weights_f
  * the extent of one matrix).  data is aligned to its element; rows that start
  * at multiples of 16 bytes are read faster.  rows, cols and groups are below
  * 2^30.  An output's address range (first to last element) must not overlap
- * an input's: INVALID_ARG.  Where a call has nothing to write it returns
- * without looking at the pointers. */
+ * an input's, the offsets' included: INVALID_ARG.  Where a call has nothing to
+ * write it returns without looking at the pointers. */
 typedef struct {
   void* data;
   uint32_t dtype; /* ciera_dtype_t */

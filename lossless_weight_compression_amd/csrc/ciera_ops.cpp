@@ -81,8 +81,10 @@ ciera_status_t launched(const char* what, hipError_t e) {
   return device_error(what, e);
 }
 
-bool bad_offsets(const int32_t* offsets, uint32_t groups) {
-  return (!offsets && groups != 1) || !aligned(offsets, 4);
+// out: the output's range, which the kernels write while they read the offsets.
+bool bad_offsets(const int32_t* offsets, uint32_t groups, Range out) {
+  if (!offsets) return groups != 1;
+  return !aligned(offsets, 4) || overlap(out, Range{reinterpret_cast<uintptr_t>(offsets), ((uint64_t)groups + 1) * 4});
 }
 
 }  // namespace
@@ -138,7 +140,7 @@ ciera_status_t ciera_mx_mm(const ciera_mx_t* a, const ciera_mx_t* b, const int32
     return CIERA_ERR_INVALID_ARG;
   if (b->groups > kMaxGroups) return CIERA_ERR_UNSUPPORTED;
   if (b->groups == 0 || empty(out)) return CIERA_OK;
-  if (bad_offsets(offsets, b->groups)) return CIERA_ERR_INVALID_ARG;
+  if (bad_offsets(offsets, b->groups, ro)) return CIERA_ERR_INVALID_ARG;
   if (bad_data(out) || bad_data(a, ac) || bad_data(b, bc)) return CIERA_ERR_INVALID_ARG;
   if (overlap(ro, ac) || overlap(ro, as) || overlap(ro, bc) || overlap(ro, bs)) return CIERA_ERR_INVALID_ARG;
   const MxMmArgs g = {a->codes, a->scales, b->codes, b->scales, out->data, offsets, out->row_stride,
@@ -160,7 +162,7 @@ ciera_status_t ciera_group_mm(const ciera_matrix_t* x, const ciera_matrix_t* w, 
     return CIERA_ERR_INVALID_ARG;
   if (w->groups > kMaxGroups) return CIERA_ERR_UNSUPPORTED;
   if (w->groups == 0 || empty(out)) return CIERA_OK;
-  if (bad_offsets(offsets, w->groups)) return CIERA_ERR_INVALID_ARG;
+  if (bad_offsets(offsets, w->groups, ro)) return CIERA_ERR_INVALID_ARG;
   if (bad_data(x) || bad_data(w) || bad_data(out)) return CIERA_ERR_INVALID_ARG;
   if (overlap(ro, rx) || overlap(ro, rw)) return CIERA_ERR_INVALID_ARG;
   const GroupMmArgs g = {x->data, w->data, out->data, offsets, x->row_stride, w->row_stride, out->row_stride,
@@ -181,7 +183,7 @@ ciera_status_t ciera_group_wgrad(const ciera_matrix_t* x, const ciera_matrix_t* 
     return CIERA_ERR_INVALID_ARG;
   if (out->groups > kMaxGroups) return CIERA_ERR_UNSUPPORTED;
   if (empty(out)) return CIERA_OK;
-  if (bad_offsets(offsets, out->groups)) return CIERA_ERR_INVALID_ARG;
+  if (bad_offsets(offsets, out->groups, ro)) return CIERA_ERR_INVALID_ARG;
   if (bad_data(x) || bad_data(dy) || bad_data(out)) return CIERA_ERR_INVALID_ARG;
   if (overlap(ro, rx) || overlap(ro, rd)) return CIERA_ERR_INVALID_ARG;
   const GroupWgradArgs g = {x->data, dy->data, out->data, offsets, x->row_stride, dy->row_stride, out->row_stride,

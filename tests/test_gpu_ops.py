@@ -667,3 +667,23 @@ def test_far_ends_of_large_operands():
     close(g, want, mag, 40, BF, "dw")
     qs = MxMatrix(n, k, groups=groups).quantize(g, axis=0)
     check_quantised(g, 0, qs, "far")
+
+
+def test_offsets_next_to_the_output():
+    """Offsets that end where the output begins, or begin where it ends, are taken."""
+    say("[gpu] offsets next to the output")
+    rows, k, n, groups = 40, 64, 96, 3
+    offsets = split(rows, groups, 5, tail=2)
+    x, w = rand((rows, k), BF, 51), rand((groups, k, n), BF, 52, 0.1)
+    want, mag = P.group_mm(np64(x), np64(w), offsets, np.full((rows, n), 7.0))
+    size = rows * n
+    buf = torch.full((size + 16,), 7.0, dtype=BF, device="cuda")
+    y = buf[8:8 + size].view(rows, n)
+    for off in (buf[:8].view(torch.int32), buf[8 + size:].view(torch.int32)):
+        y.fill_(7.0)
+        off.copy_(off_dev(offsets))
+        L.ciera_group_mm(x, w, y, offsets=off)
+        close(y, want, mag, k, BF, "y")
+        assert off.tolist() == offsets
+    with pytest.raises(L.CieraError):
+        L.ciera_group_mm(x, w, y, offsets=buf[6:14].view(torch.int32))

@@ -182,3 +182,25 @@ def test_binding_refuses_another_device(monkeypatch):
             call()
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     assert L.matrix_item(Elsewhere(), "x").rows == 8
+
+
+@pytest.mark.parametrize("at", ["first", "last", "within", "around"])
+def test_outputs_over_the_offsets_are_refused(at):
+    """The kernels read the offsets, of groups + 1 words, while they write the output."""
+    def place(out_bytes, offset_bytes):
+        return {"first": OUT - offset_bytes + 4,       # the last offset in the output's first bytes
+                "last": OUT + out_bytes - 4,           # the first offset in its last bytes
+                "within": OUT + 8,
+                "around": OUT - 8}[at]
+
+    groups = 3 if at != "around" else 400
+    x, out = mat(X, 8, 16), mat(OUT, 8, 24)
+    refused(1, L.ciera_group_mm, x, mat(W, 16, 24, groups=groups), out, offsets=place(8 * 24 * 2, 4 * groups + 4))
+    refused(1, L.ciera_group_mm, x, mat(W, 24, 16, groups=groups), out, offsets=place(8 * 24 * 2, 4 * groups + 4),
+            transpose_w=True)
+    refused(1, L.ciera_mx_mm, L.Mx(0x100000, 0x200000, 1, 0, 8, 100), L.Mx(0x300000, 0x400000, groups, 0, 24, 100), out,
+            offsets=place(8 * 24 * 2, 4 * groups + 4))
+    groups = 3
+    size = 3 * 16 * 24 * 2
+    where = place(size, 16) if at != "around" else OUT + size // 2
+    refused(1, L.ciera_group_wgrad, x, mat(W, 8, 24), mat(OUT, 16, 24, groups=3), offsets=where)
