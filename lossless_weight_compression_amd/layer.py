@@ -17,6 +17,7 @@ only.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -29,6 +30,14 @@ ELEM = {B.CIERA_BF16: 2, B.CIERA_FP32: 4, B.CIERA_FP16: 2}
 
 def _align(x: int, a: int) -> int:
     return (x + a - 1) // a * a
+
+
+def _memory_of(stream):
+    """Where tensors that a call on ``stream`` writes are made.  Memory freed on another
+    stream may still be in use there, and nothing orders that use before the call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
 class LayerCodec:
@@ -118,13 +127,17 @@ class LayerCodec:
     def quantize(self, indices: Sequence[int], axis: int = 0, into: Optional["MxMatrix"] = None,
                  stream=None) -> "MxMatrix":
         """4-bit copy of the rebuilt tensors of these indices (one call), as ciera_mx_mm
-        takes it: axis 0 for [in, out] matrices, 1 for [out, in] ones."""
+        takes it: axis 0 for [in, out] matrices, 1 for [out, in] ones.  Without ``into`` its
+        memory belongs to ``stream``."""
         w = self.stack(indices)
         g, r, c = w.shape
         if axis not in (0, 1):
             raise ValueError(f"axis: {axis}, expected 0 or 1")
         shape = (r, c) if axis else (c, r)
-        q = into if into is not None else MxMatrix(*shape, groups=g, device=self.device)
+        q = into
+        if q is None:
+            with _memory_of(stream):
+                q = MxMatrix(*shape, groups=g, device=self.device)
         q.quantize(w, axis, stream)
         return q
 
@@ -240,8 +253,10 @@ class MxMatrix:
         return self
 
     def dequantize(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """The values ([groups, rows, cols], bf16 unless ``out`` says otherwise)."""
+        """The values ([groups, rows, cols], bf16 unless ``out`` says otherwise; without
+        ``out`` their memory belongs to ``stream``)."""
         if out is None:
-            out = torch.empty(self.groups, self.rows, self.cols, dtype=torch.bfloat16, device=self.codes.device)
+            with _memory_of(stream):
+                out = torch.empty(self.groups, self.rows, self.cols, dtype=torch.bfloat16, device=self.codes.device)
         B.ciera_mx_dequantize(self, out, stream)
         return out

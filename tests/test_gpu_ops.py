@@ -687,3 +687,38 @@ def test_offsets_next_to_the_output():
         assert off.tolist() == offsets
     with pytest.raises(L.CieraError):
         L.ciera_group_mm(x, w, y, offsets=buf[6:14].view(torch.int32))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_results_made_on_a_side_stream(raw):
+    """Outputs that a call on another stream makes itself do not take memory that work
+    still under way on the current one writes."""
+    say(f"[gpu] results made on a side stream, raw handle {raw}")
+    groups, r, c = 3, 256, 512
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    codec = LayerCodec([(r, c)] * groups, BF, 1, 512, "cuda", 10_000)
+    for i in range(groups):
+        codec.out_view(i).copy_(rand((r * c,), BF, 60 + i))
+    want_q = codec.quantize(range(groups))
+    want = want_q.dequantize()
+    a = rand((4096, 4096), BF, 63)
+    b = torch.empty_like(a)
+    torch.cuda.synchronize()
+
+    def under_way(shape, dtype):
+        gone = torch.empty(shape, dtype=dtype, device="cuda")
+        for _ in range(20):
+            torch.mm(a, a, out=b)
+        gone.fill_(7)
+
+    under_way(want.shape, want.dtype)
+    got = want_q.dequantize(stream=stream)
+    under_way(want_q.codes.shape, torch.uint8)
+    under_way(want_q.scales.shape, torch.uint8)
+    got_q = codec.quantize(range(groups), stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert torch.equal(got_q.codes, want_q.codes) and torch.equal(got_q.scales, want_q.scales)
+    codec.quantize(range(groups), stream=0)                # the default stream's handle
+    assert torch.equal(want_q.dequantize(stream=0), want)

@@ -204,3 +204,45 @@ def test_outputs_over_the_offsets_are_refused(at):
     size = 3 * 16 * 24 * 2
     where = place(size, 16) if at != "around" else OUT + size // 2
     refused(1, L.ciera_group_wgrad, x, mat(W, 8, 24), mat(OUT, 16, 24, groups=3), offsets=where)
+
+
+@pytest.mark.parametrize("stream", [None, 0x5000, "side"])
+def test_results_are_allocated_on_the_stream_that_writes_them(stream, monkeypatch):
+    """Memory that another stream has freed may still be in use there: what a call on
+    `stream` makes and writes has to come from that stream's memory."""
+    from lossless_weight_compression_amd import layer
+    active, made, real = [None], [], torch.empty
+
+    class On:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            active.append(self.s)
+
+        def __exit__(self, *a):
+            active.pop()
+
+    def empty(*a, **kw):
+        made.append(active[-1])
+        return real(*a, **{**kw, "device": "cpu"})
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, **kw: handle)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(layer.B, "mx_item", lambda *a: None)
+    for name in ("ciera_mx_quantize", "ciera_mx_dequantize"):
+        monkeypatch.setattr(layer.B, name, lambda *a: made.append(a[-1]))
+    q = layer.MxMatrix(8, 128)
+    made.clear()
+    q.dequantize(stream=stream)
+    assert made == [stream, stream]
+    made.clear()
+    codec = layer.LayerCodec.__new__(layer.LayerCodec)
+    codec.device = "cpu"
+    monkeypatch.setattr(layer.LayerCodec, "stack", lambda self, idx: torch.zeros(2, 128, 8))
+    assert codec.quantize([0, 1], stream=stream).rows == 8
+    assert made == [stream] * 3                            # codes, scales, the call
+    made.clear()
+    codec.quantize([0, 1], into=q, stream=stream)
+    assert made == [stream]
