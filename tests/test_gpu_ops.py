@@ -722,3 +722,90 @@ def test_results_made_on_a_side_stream(raw):
     assert torch.equal(got_q.codes, want_q.codes) and torch.equal(got_q.scales, want_q.scales)
     codec.quantize(range(groups), stream=0)                # the default stream's handle
     assert torch.equal(want_q.dequantize(stream=0), want)
+
+
+# Several tiles one after another to each workgroup of the large kernels, most of them whole,
+# with several stages each, so that the next tile's loads and the last one's stores are under
+# way together.  504 tiles: no half ones at the end; 360: the last ones halved; 481: whole and
+# ragged ones in turn.  rows, K, N, groups, rows behind the last group
+ROUNDS = [(9000, 584, 3584, 2, 3), (9000, 584, 2560, 2, 0), (9000, 328, 3080, 3, 1)]
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F32)])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("shape", ROUNDS)
+def test_group_mm_tile_after_tile(shape, transpose, dtype, out):
+    test_group_mm(shape, transpose, dtype, out)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("shape", ROUNDS + [(9000, 1447, 2560, 2, 0)])
+def test_mx_mm_tile_after_tile(shape, out):
+    test_mx_mm(shape, out)
+
+
+# gradients of K x N: 512, 560 (more groups than a wave has lanes) and 480 tiles
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F32)])
+@pytest.mark.parametrize("shape", [(2100, 2048, 2048, 8, 5), (9000, 512, 1024, 70, 0), (1500, 1288, 2560, 8, 1)])
+def test_group_wgrad_tile_after_tile(shape, dtype, out):
+    test_group_wgrad(shape, dtype, out)
+
+
+# A few rows to each of many groups: 128 columns to a workgroup, whole and ragged ones; one
+# step of the contraction to a wave, several, and ends inside one
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (F16, F16), (BF, F32), (F16, F32)])
+@pytest.mark.parametrize("shape", [(200, 256, 1024, 150, 2), (200, 250, 1000, 150, 0), (190, 1064, 1024, 150, 1),
+                                   (170, 777, 1160, 140, 0)])
+def test_group_mm_few_rows_many_groups(shape, dtype, out):
+    test_group_mm(shape, False, dtype, out)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("hot", [0, 77, 255])
+def test_one_popular_group(hot, transpose):
+    """Nearly all rows in one of many groups."""
+    say(f"[gpu] popular group {hot} transpose={transpose}")
+    rows, k, n, groups = 1500, 200, 520, 256
+    counts = [1 if g % 5 == 0 else 0 for g in range(groups)]
+    counts[hot] += rows - sum(counts)
+    offsets = [0] + np.cumsum(counts).tolist()
+    x, w = rand((rows, k), BF, 71), rand((groups, n, k) if transpose else (groups, k, n), BF, 72, 0.1)
+    y = torch.full((rows, n), 7.0, dtype=BF, device="cuda")
+    L.ciera_group_mm(x, w, y, offsets=off_dev(offsets), transpose_w=transpose)
+    want, mag = P.group_mm(np64(x), np64(w).transpose(0, 2, 1) if transpose else np64(w), offsets, np.zeros((rows, n)))
+    close(y, want, mag, k, BF, "y")
+    qx, qw = MxMatrix(rows, k).quantize(x), MxMatrix(n, k, groups=groups).quantize(w, axis=1 if transpose else 0)
+    L.ciera_mx_mm(qx, qw, y, offsets=off_dev(offsets))
+    want, mag = P.group_mm(mx64(qx)[0], mx64(qw).transpose(0, 2, 1), offsets, np.zeros((rows, n)))
+    close(y, want, mag, k, BF, "4-bit y")
+    dy = rand((rows, n), BF, 73, 0.1)
+    g = torch.full((groups, k, n), 7.0, dtype=F32, device="cuda")
+    L.ciera_group_wgrad(x, dy, g, offsets=off_dev(offsets))
+    want, mag = P.group_wgrad(np64(x), np64(dy), offsets)
+    close(g, want, mag, rows, F32, "dw")
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+def test_stacks_of_other_types(dtype):
+    """fp16 and fp32 layers as stacks: equal distances, 4-bit copies, and products of
+    those that the products take."""
+    say(f"[gpu] stack and quantize of {dtype}")
+    groups, dm, dff, rows = 4, 96, 131, 70
+    codec = LayerCodec([s for _ in range(groups) for s in ((dm, dff), (dff, dm))], dtype, 1, 512, "cuda", 10_000)
+    ws = [rand((dm, dff) if i % 2 == 0 else (dff, dm), dtype, 80 + i, 0.05) for i in range(2 * groups)]
+    codec.seed_cache(ws)
+    codec.encode(0, [w.reshape(-1) for w in ws])
+    assert int(codec.decode().item()) == 0
+    up, down = codec.stack(range(0, 2 * groups, 2)), codec.stack(range(1, 2 * groups, 2))
+    assert up.dtype == dtype and torch.equal(up, torch.stack(ws[0::2])) and torch.equal(down, torch.stack(ws[1::2]))
+    check_quantised(up, 0, codec.quantize(range(0, 2 * groups, 2), axis=0), "up, down the columns")
+    check_quantised(down, 1, codec.quantize(range(1, 2 * groups, 2), axis=1), "down, along the rows")
+    off = split(rows, groups, 5)
+    x, y = rand((rows, dm), dtype, 90), torch.zeros(rows, dff, dtype=dtype, device="cuda")
+    if dtype == F32:
+        with pytest.raises(L.CieraError):
+            L.ciera_group_mm(x, up, y, offsets=off_dev(off))
+        return
+    L.ciera_group_mm(x, up, y, offsets=off_dev(off))
+    want, mag = P.group_mm(np64(x), np64(up), off, np.zeros((rows, dff)))
+    close(y, want, mag, dm, dtype, "y")
