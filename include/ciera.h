@@ -370,8 +370,9 @@ ciera_status_t ciera_cache_update(const ciera_tensor_t* t, const void* weights_f
  * are used for.  The conventions above hold; every call here enqueues kernels
  * only (no scratch, no copies, no allocation), so it may be captured into a
  * graph, and any number of calls may run at once on streams of their own.
- * Sums are held in fp32 and rounded once to the output's type; the order of a
- * sum depends on sizes alone, so equal calls give equal bits.
+ * Sums are held in fp32 and rounded once to the output's type.  The order of a
+ * sum depends on sizes, strides and the alignment of the operands, never on
+ * timing: equal calls on equally laid out operands give equal bits.
  *
  * A matrix, or a stack of `groups` matrices, row-major: element (g, r, c) at
  * data + g * group_stride + r * row_stride + c, strides in elements.  Strides

@@ -483,9 +483,11 @@ uint32_t row_grid(const RowPass& p) { return pass_grid((p.total + 4 * kRun - 1) 
 
 template <typename O>
 hipError_t run_mx_mm(const MxMmArgs& a, hipStream_t s) {
-  // By rows to a group on average; 64 experts of 2048 x 1024, us (where 64 x 128 tiles
-  // leave most of the card idle the thin kernel wins up to 64 rows: one matrix 7168 x 2048,
-  // 24 rows 8.1 for 16.7, 64 rows 11.1 for 17.7; 1 token over 8 experts 8 for 18):
+  // By rows to a group on average; 64 experts of 2048 x 1024, us, the same operands from
+  // call to call (at 1024 rows the large kernel takes 85, with operands from memory 125).
+  // Where 64 x 128 tiles leave most of the card idle the thin kernel wins up to 64 rows (one
+  // matrix 7168 x 2048, 24 rows 8.1 for 16.7, 64 rows 11.1 for 17.7; 1 token over 8 experts
+  // 8 for 18):
   //   rows        4    8   16   24   64  100  128  160  200  256
   //   thin       18   21   21
   //   64 rows    14   15   19   19   20   29   32   36   44   52
