@@ -1,0 +1,479 @@
+"""Timed cases of the experts' gated feed-forward block and of its 4-bit serving form.
+
+  glu    ciera_glu_mm: act(x w_gate) * (x w_up) on the rows of every expert, for training
+         with both projections kept
+  back   its backward pass: ciera_glu_grad (the gradients of both projections from that of
+         the block's output, through w_down) and ciera_glu_xgrad (the gradient of x)
+  quant  ciera_q4_quantize and ciera_q4_dequantize: a stack of matrices to 4-bit integers
+         with a scale (and a zero) for every 32, 64 or 128 values, and back
+  q4     a serving step on such weights: ciera_q4_glu, then ciera_q4_mm with w_down
+
+``run`` computes a case in its plain form (elementary torch operations in 32 bits, rounded
+once) or, where ``own`` is true, through the package's calls.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+BYTES = {"bf16": 2, "fp16": 2, "fp32": 4}
+WEIGHT_STD = 0.02   # of the synthetic expert weights
+
+
+# ------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # one token of a serving step through the gated half of an OLMoE-shaped layer: latency
+        dict(name="glu_token", op="glu", groups=64, top_k=8, tokens=1, k=2048, n=1024, dtype="bf16",
+             transpose=False, act="silu", keep=False, pad=0),
+        # a serving batch of 64 sequences over the 256 experts of a fine-grained layer: the
+        # bytes of the weights are what counts
+        dict(name="glu_batch", op="glu", groups=256, top_k=8, tokens=64, k=7168, n=2048, dtype="bf16",
+             transpose=True, act="silu", keep=False, pad=0),
+        # the forward pass of a training batch on an OLMoE-shaped layer
+        dict(name="glu_layer", op="glu", groups=64, top_k=8, tokens=8192, k=2048, n=1024, dtype="bf16",
+             transpose=False, act="silu", keep=True, pad=0),
+        # a small ragged training batch of odd sizes in a buffer with rows to spare
+        dict(name="glu_odd", op="glu", groups=13, top_k=2, tokens=1117, k=1447, n=777, dtype="fp16",
+             transpose=False, act="gelu", keep=True, pad=5),
+        # the backward pass of the training batch on an OLMoE-shaped layer
+        dict(name="back_layer", op="back", groups=64, top_k=8, tokens=8192, k=2048, n=1024, dtype="bf16",
+             transpose=True, act="silu", pad=0),
+        # the backward pass of a small ragged batch of odd sizes, weights stored [out, in]
+        dict(name="back_odd", op="back", groups=7, top_k=2, tokens=1003, k=777, n=515, dtype="fp16",
+             transpose=False, act="gelu", pad=9),
+        # the 64 gate matrices of an OLMoE-shaped layer to a 4-bit copy: scales down the
+        # columns of [in, out], along the contraction
+        dict(name="quant_experts", op="quant", groups=64, rows=2048, cols=1024, dtype="bf16", axis=0,
+             block=128, scales="bf16", zeros=True),
+        # fp32 master weights of odd sizes, symmetric, small blocks along the rows
+        dict(name="quant_master_odd", op="quant", groups=5, rows=777, cols=1447, dtype="fp32", axis=1,
+             block=32, scales="fp16", zeros=False),
+        # one token of a serving step through the whole gated block on 4-bit experts: latency
+        dict(name="q4_token", op="q4", groups=64, top_k=8, tokens=1, k=2048, n=1024, dtype="bf16",
+             block=128, scales="bf16", zeros=True, act="silu", pad=0),
+        # a serving batch of 64 sequences over the 4-bit experts of a fine-grained layer
+        dict(name="q4_batch", op="q4", groups=256, top_k=8, tokens=64, k=7168, n=2048, dtype="bf16",
+             block=128, scales="bf16", zeros=True, act="silu", pad=0),
+        # a small ragged batch of odd sizes, symmetric, smaller blocks
+        dict(name="q4_odd", op="q4", groups=11, top_k=3, tokens=301, k=1447, n=515, dtype="fp16",
+             block=64, scales="fp16", zeros=False, act="gelu", pad=37),
+        # prompts of 2048 tokens in all on the 4-bit experts of an OLMoE-shaped layer
+        dict(name="q4_prompt", op="q4", groups=64, top_k=8, tokens=2048, k=2048, n=1024, dtype="bf16",
+             block=128, scales="bf16", zeros=True, act="silu", pad=0),
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A size of [lo, hi], spread over its logarithm."""
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+
+def _width(rng, lo, hi):
+    """A matrix side: half of them multiples of 64, the others whatever they are."""
+    v = _spread(rng, lo, hi)
+    return max(64, v // 64 * 64) if rng.random() < 0.5 else v
+
+
+def draw(rng):
+    limit = {}
+    for c in listed():
+        w = work(c)
+        for key in w:
+            limit[key] = max(limit.get(key, 0), w[key])
+    while True:
+        op = rng.choice(["glu", "glu", "back", "quant", "q4", "q4"])
+        if op == "quant":
+            case = dict(op=op, groups=_spread(rng, 1, 64), rows=_width(rng, 1, 8192), cols=_width(rng, 1, 7168),
+                        dtype=rng.choice(["bf16", "fp16", "fp32"]), axis=rng.choice([0, 1]),
+                        block=rng.choice([32, 64, 128]), scales=rng.choice(["bf16", "fp16"]), zeros=rng.random() < 0.7)
+            if case["groups"] * case["rows"] * case["cols"] > 64 * 2048 * 1024:
+                continue
+            return case
+        case = dict(op=op, groups=_spread(rng, 1, 256), top_k=rng.choice([1, 2, 4, 8]),
+                    tokens=_spread(rng, 1, 2048 if op == "q4" else 8192),
+                    k=_width(rng, 16, 7168), n=_width(rng, 16, 7168), dtype=rng.choice(["bf16", "fp16"]),
+                    act=rng.choice(["silu", "silu", "gelu"]), pad=rng.choice([0, 0, rng.randrange(1, 64)]))
+        if op == "q4":
+            case.update(block=rng.choice([32, 64, 128, 128]), scales=rng.choice(["bf16", "fp16"]),
+                        zeros=rng.random() < 0.7)
+        else:
+            case["transpose"] = rng.random() < 0.5
+        if op == "glu":
+            case["keep"] = rng.random() < 0.5
+        if case["top_k"] > case["groups"]:
+            continue
+        w = work(case)
+        # the plain forms go expert by expert: no more than 2 GB of each matrix's weights
+        # drawn, so that a drawn case stays cheaper than the largest listed one
+        if (w["flops"] <= limit["flops"] and w["bytes"] <= limit["bytes"] // 2
+                and case["groups"] * case["k"] * case["n"] <= 1 << 30):
+            return case
+
+
+def _experts_hit(case):
+    """Experts that an even routing of the tokens reaches, on average."""
+    g = case["groups"]
+    return g * (1.0 - (1.0 - case["top_k"] / g) ** case["tokens"])
+
+
+def work(case):
+    op, e = case["op"], BYTES[case["dtype"]]
+    if op == "quant":
+        numel = case["groups"] * case["rows"] * case["cols"]
+        per = 0.5 + (3 if case["zeros"] else 2) / case["block"]
+        # read once, written as codes and scales, read from there and written as values
+        return {"bytes": int(numel * (2 * e + 2 * per)), "flops": 4 * numel}
+    rows, k, n = case["tokens"] * case["top_k"], case["k"], case["n"]
+    weights = _experts_hit(case) * k * n
+    if op == "glu":
+        return {"bytes": int(rows * k * e + 2 * weights * e + rows * n * e * (3 if case["keep"] else 1)),
+                "flops": 4 * rows * k * n}
+    if op == "back":
+        return {"bytes": int(rows * k * e + 3 * weights * e + 4 * rows * n * e + rows * k * e),
+                "flops": 6 * rows * k * n}
+    per = 0.5 + (3 if case["zeros"] else 2) / case["block"]
+    return {"bytes": int(2 * rows * k * e + 3 * weights * per + rows * n * e), "flops": 6 * rows * k * n}
+
+
+# ------------------------------------------------------------------ inputs
+
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(shape, dtype, g, std):
+    out = torch.empty(shape, dtype=dtype, device="cuda")
+    flat = out.view(-1)
+    step = 1 << 28
+    for a in range(0, flat.numel(), step):
+        part = flat[a:a + step]
+        part.copy_(torch.randn(part.numel(), device="cuda", generator=g) * std)
+    return out
+
+
+def _activations(rows, cols, dtype, g):
+    """Normal values whose channels differ in size, a few of them by much."""
+    x = _normal((rows, cols), torch.float32, g, 1.0)
+    channel = torch.exp(0.5 * torch.randn(cols, device="cuda", generator=g))
+    channel = torch.where(torch.rand(cols, device="cuda", generator=g) < 0.005, channel * 10, channel)
+    return (x * channel).to(dtype)
+
+
+def _routing(case, g):
+    """Rows of every expert: each token takes top_k experts, some experts more popular."""
+    bias = 0.7 * torch.randn(case["groups"], device="cuda", generator=g)
+    u = torch.rand(case["tokens"], case["groups"], device="cuda", generator=g).clamp_min(1e-20)
+    score = bias - torch.log((-torch.log(u)).clamp_min(1e-20))
+    chosen = score.topk(case["top_k"], dim=1).indices.reshape(-1)
+    counts = torch.bincount(chosen, minlength=case["groups"]).tolist()
+    ends = [0]
+    for c in counts:
+        ends.append(ends[-1] + c)
+    return ends
+
+
+def _q4_weights(groups, rows, cols, case, g):
+    """A stack [groups, rows, cols] of 4-bit weights as a program holds it: codes, scales and
+    zeros of normal weights (blocks along the rows, cols padded to 128)."""
+    kp, block = -(-cols // 128) * 128, case["block"]
+    codes = torch.empty(groups, rows, kp // 2, dtype=torch.uint8, device="cuda")
+    flat = codes.view(-1)
+    step = 1 << 27
+    for a in range(0, flat.numel(), step):
+        part = flat[a:a + step]
+        q = torch.randn(2, part.numel(), device="cuda", generator=g)
+        q = (q * 2.9 + 7.5).round_().clamp_(0, 15).to(torch.uint8)
+        part.copy_(q[0] | (q[1] << 4))
+    sizes = (groups, rows, kp // block)
+    spread = torch.exp(0.15 * torch.randn(sizes, device="cuda", generator=g))
+    scales = (WEIGHT_STD / 2.9 * spread).to(DTYPES[case["scales"]])
+    zeros = None
+    if case["zeros"]:
+        zeros = torch.randint(5, 11, sizes, dtype=torch.uint8, device="cuda", generator=g)
+    return dict(codes=codes, scales=scales, zeros=zeros, groups=groups, rows=rows, cols=cols, block=block)
+
+
+def _inputs(case, seed):
+    g = _generator(seed)
+    dtype, op = DTYPES[case["dtype"]], case["op"]
+    if op == "quant":
+        x = _normal((case["groups"], case["rows"], case["cols"]), dtype, g, WEIGHT_STD)
+        return dict(x=x)
+    groups, k, n = case["groups"], case["k"], case["n"]
+    ends = _routing(case, g)
+    rows = ends[-1] + case["pad"]
+    d = dict(ends=ends, rows=rows)
+    if op == "glu":
+        shape = (groups, n, k) if case["transpose"] else (groups, k, n)
+        d["x"] = _activations(rows, k, dtype, g)
+        d["w_gate"], d["w_up"] = _normal(shape, dtype, g, WEIGHT_STD), _normal(shape, dtype, g, WEIGHT_STD)
+    elif op == "back":
+        # the forward pass's operands: k model width, n the experts' width
+        inner = (groups, k, n) if case["transpose"] else (groups, n, k)
+        outer = (groups, n, k) if case["transpose"] else (groups, k, n)
+        d["dy"] = _normal((rows, k), dtype, g, 0.05)
+        d["gate"], d["up"] = _normal((rows, n), dtype, g, 1.0), _normal((rows, n), dtype, g, 1.0)
+        d["w_gate"], d["w_up"] = _normal(inner, dtype, g, WEIGHT_STD), _normal(inner, dtype, g, WEIGHT_STD)
+        d["w_down"] = _normal(outer, dtype, g, WEIGHT_STD)
+    else:
+        d["x"] = _activations(rows, k, dtype, g)
+        d["gate"], d["up"] = _q4_weights(groups, n, k, case, g), _q4_weights(groups, n, k, case, g)
+        d["down"] = _q4_weights(groups, k, n, case, g)
+    return d
+
+
+def prepare(case, seed):
+    s = dict(case=case, **_inputs(case, seed))
+    dtype, op = DTYPES[case["dtype"]], case["op"]
+    if op != "quant":
+        s["offsets"] = torch.tensor(s["ends"], dtype=torch.int32, device="cuda")
+
+    # the buffers that a program keeps its results in; rows behind the last expert's stay as they are
+    def buffer(cols):
+        return torch.zeros(s["rows"], cols, dtype=dtype, device="cuda")
+
+    if op == "quant":
+        g, r, c = s["x"].shape
+        s["out"] = torch.zeros((g, r, c) if case["axis"] else (g, c, r), dtype=dtype, device="cuda")
+    elif op == "glu":
+        s["out"] = buffer(case["n"])
+        s["gate"], s["up"] = (buffer(case["n"]), buffer(case["n"])) if case["keep"] else (None, None)
+    elif op == "back":
+        s["dgate"], s["dup"], s["dx"] = buffer(case["n"]), buffer(case["n"]), buffer(case["k"])
+    else:
+        s["h"], s["y"] = buffer(case["n"]), buffer(case["k"])
+    if own:
+        import lossless_weight_compression_amd as ciera
+        from lossless_weight_compression_amd.layer import Q4Matrix
+        s["ciera"] = ciera
+        if op == "quant":
+            g, r, c = s["out"].shape
+            s["q"] = Q4Matrix(r, c, groups=g, block=case["block"], dtype=DTYPES[case["scales"]],
+                              with_zeros=case["zeros"])
+        elif op == "q4":
+            for name in ("gate", "up", "down"):
+                w = s[name]
+                s["q_" + name] = Q4Matrix(w["rows"], w["cols"], groups=w["groups"], block=w["block"],
+                                          codes=w["codes"], scales=w["scales"], zeros=w["zeros"])
+    return s
+
+
+def run(state):
+    return _run_own(state) if own else _run_plain(state)
+
+
+def _run_own(s):
+    case, ciera = s["case"], s["ciera"]
+    op = case["op"]
+    if op == "glu":
+        ciera.ciera_glu_mm(s["x"], s["w_gate"], s["w_up"], s["out"], offsets=s["offsets"],
+                           transpose_w=case["transpose"], act=case["act"], gate=s["gate"], up=s["up"])
+        return (s["out"], s["gate"], s["up"]) if case["keep"] else s["out"]
+    if op == "back":
+        ciera.ciera_glu_grad(s["dy"], s["w_down"], s["gate"], s["up"], s["dgate"], s["dup"], offsets=s["offsets"],
+                             transpose_w=case["transpose"], act=case["act"])
+        ciera.ciera_glu_xgrad(s["dgate"], s["dup"], s["w_gate"], s["w_up"], s["dx"], offsets=s["offsets"],
+                              transpose_w=case["transpose"])
+        return s["dgate"], s["dup"], s["dx"]
+    if op == "quant":
+        ciera.ciera_q4_quantize(s["x"], s["q"], axis=case["axis"])
+        ciera.ciera_q4_dequantize(s["q"], s["out"])
+        return s["out"]
+    ciera.ciera_q4_glu(s["x"], s["q_gate"], s["q_up"], s["h"], offsets=s["offsets"], act=case["act"])
+    ciera.ciera_q4_mm(s["h"], s["q_down"], s["y"], offsets=s["offsets"])
+    return s["h"], s["y"]
+
+
+# -------------------------------------------------------------- plain forms
+
+def _gate_factor(x, act):
+    """What the activation multiplies its argument with, and the derivative of the factor's
+    own argument."""
+    if act == "silu":
+        return torch.sigmoid(x), torch.ones_like(x)
+    c = math.sqrt(2 / math.pi)
+    return torch.sigmoid(2 * c * (x + 0.044715 * x * x * x)), 2 * c * (1 + 3 * 0.044715 * x * x)
+
+
+def _act(x, act):
+    return x * _gate_factor(x, act)[0]
+
+
+def _act_grad(x, act):
+    f, d = _gate_factor(x, act)
+    return f + x * f * (1 - f) * d
+
+
+def _unpack(w, e=slice(None)):
+    """Values in 32 bits of the 4-bit matrices e of a stack: of every 128 values of a row,
+    byte b of word 4 q + u holds value 32 u + 8 q + b in its low half and the one 4 further
+    in its high half."""
+    codes = w["codes"][e]
+    lead = codes.shape[:-1]
+    c = codes.reshape(*lead, -1, 4, 4, 1, 4)
+    q = torch.cat((c & 15, c >> 4), dim=-2)                # [.., blocks, q, u, half, b]
+    q = q.transpose(-4, -3).reshape(*lead, -1, w["block"]).float()
+    z = 8.0 if w["zeros"] is None else w["zeros"][e].unsqueeze(-1).float()
+    v = (q - z) * w["scales"][e].unsqueeze(-1).float()
+    return v.reshape(*lead, -1)[..., :w["cols"]]
+
+
+def _grouped(ends, out, one):
+    """out[a:b] = one(g, a, b) for the rows of every expert that has some."""
+    for e in range(len(ends) - 1):
+        if ends[e] < ends[e + 1]:
+            for o, v in zip(out, one(e, ends[e], ends[e + 1])):
+                o[ends[e]:ends[e + 1]] = v.to(o.dtype)
+
+
+def _run_plain(s):
+    case = s["case"]
+    op, act = case["op"], case.get("act")
+    if op == "quant":
+        return _round_trip(s)
+    t = case.get("transpose")
+
+    def w(name, e):
+        m = s[name][e].float()
+        return m.t() if t else m
+
+    if op == "glu":
+        out = (s["out"], s["gate"], s["up"]) if case["keep"] else (s["out"],)
+
+        def forward(e, a, b):
+            x = s["x"][a:b].float()
+            g, u = x @ w("w_gate", e), x @ w("w_up", e)
+            return _act(g, act) * u, g, u
+
+        _grouped(s["ends"], out, forward)
+        return out if case["keep"] else s["out"]
+    if op == "back":
+        def backward(e, a, b):
+            d, g, u = s["dy"][a:b].float() @ w("w_down", e), s["gate"][a:b].float(), s["up"][a:b].float()
+            dg, du = d * u * _act_grad(g, act), d * _act(g, act)
+            return dg, du, dg @ w("w_gate", e) + du @ w("w_up", e)
+
+        out = (s["dgate"], s["dup"], s["dx"])
+        _grouped(s["ends"], out, backward)
+        return out
+
+    def serve(e, a, b):
+        x = s["x"][a:b].float()
+        h = _act(x @ _unpack(s["gate"], e).t(), act) * (x @ _unpack(s["up"], e).t())
+        return h, h @ _unpack(s["down"], e).t()
+
+    _grouped(s["ends"], (s["h"], s["y"]), serve)
+    return s["h"], s["y"]
+
+
+def _round_trip(s):
+    """x to 4 bits in blocks along the contraction, and back."""
+    case, out = s["case"], s["out"]
+    x = s["x"] if case["axis"] else s["x"].transpose(1, 2)
+    k, block = x.shape[-1], case["block"]
+    v = torch.nn.functional.pad(x.float(), (0, -k % block)).reshape(*x.shape[:-1], -1, block)
+    if case["zeros"]:
+        lo, hi = v.amin(-1, keepdim=True).clamp_max(0), v.amax(-1, keepdim=True).clamp_min(0)
+        scale = ((hi - lo) / 15).to(DTYPES[case["scales"]]).float()
+        zero = torch.where(scale > 0, -lo / scale, 0.0).round().clamp(0, 15)
+    else:
+        scale = (v.abs().amax(-1, keepdim=True) / 7).to(DTYPES[case["scales"]]).float()
+        zero = 8.0
+    q = (torch.where(scale > 0, v / scale, 0.0).round() + zero).clamp(0, 15)
+    out.copy_(((q - zero) * scale).reshape(*x.shape[:-1], -1)[..., :k])
+    return out
+
+
+# ------------------------------------------------- the definition in 64 bits
+
+def _quantised(x, case):
+    """x [rows, k] in 64 bits as the 4-bit format holds it: of every block the scale that
+    spreads the 16 codes over its range (with 0 in it), and the nearest code's value."""
+    out = torch.zeros_like(x)
+    to = DTYPES[case["scales"]]
+    for a in range(0, x.shape[1], case["block"]):
+        b = x[:, a:a + case["block"]]
+        if case["zeros"]:
+            low = torch.minimum(b.min(1).values, torch.zeros_like(b[:, 0]))
+            high = torch.maximum(b.max(1).values, torch.zeros_like(b[:, 0]))
+            s = ((high - low) / 15).to(to).double().unsqueeze(1)
+            first = -torch.round(-low.unsqueeze(1) / s).clamp(0, 15)
+        else:
+            s = (b.abs().max(1).values / 7).to(to).double().unsqueeze(1)
+            first = torch.full_like(s, -8.0)
+        steps = torch.minimum(torch.maximum(torch.round(b / s), first), first + 15)
+        out[:, a:a + case["block"]] = torch.where(s > 0, steps * s, 0.0)
+    return out
+
+
+def _stack_values(w, e):
+    """Matrix e of a 4-bit stack in 64 bits, [cols, rows]."""
+    n, kp = w["rows"], w["codes"].shape[-1] * 2
+    i = torch.arange(kp, device="cuda")
+    inner = i % 128
+    word = inner // 8 % 4 * 4 + inner // 32
+    at = i // 128 * 64 + word * 4 + inner % 4
+    byte = w["codes"][e].index_select(1, at).long()
+    code = torch.where((inner % 8 >= 4).unsqueeze(0), byte // 16, byte % 16).double()
+    zero = torch.full((n, kp // w["block"]), 8.0, dtype=torch.float64, device="cuda")
+    if w["zeros"] is not None:
+        zero = w["zeros"][e].double()
+    rep = w["block"]
+    v = w["scales"][e].double().repeat_interleave(rep, 1) * (code - zero.repeat_interleave(rep, 1))
+    return v[:, :w["cols"]].t().contiguous()
+
+
+def _phi(x, act):
+    """The activation and its derivative."""
+    if act == "silu":
+        p = 1 / (1 + torch.exp(-x))
+        return x * p, p + x * p * (1 - p)
+    c = math.sqrt(2 / math.pi)
+    t = torch.tanh(c * (x + 0.044715 * x ** 3))
+    return x * (1 + t) / 2, (1 + t) / 2 + x * (1 - t * t) / 2 * c * (1 + 0.134145 * x ** 2)
+
+
+def exact(case, seed):
+    d = _inputs(case, seed)
+    op, act = case["op"], case.get("act")
+    if op == "quant":
+        return torch.stack([_quantised(m.double() if case["axis"] else m.double().t().contiguous(), case)
+                            for m in d["x"]])
+    widths = dict(glu=[case["n"]] * 3, back=[case["n"], case["n"], case["k"]], q4=[case["n"], case["k"]])[op]
+    outs = [torch.zeros(d["rows"], c, dtype=torch.float64, device="cuda") for c in widths]
+    row = torch.arange(d["rows"], device="cuda")
+    expert = torch.searchsorted(torch.tensor(d["ends"][1:], device="cuda"), row, right=True)
+
+    def weights(name, e):
+        if op == "q4":
+            return _stack_values(d[name], e)
+        m = d["w_" + name][e].double()
+        return m.t().contiguous() if case["transpose"] else m
+
+    for e in range(case["groups"]):
+        mine = (expert == e).nonzero().squeeze(1)
+        if mine.numel() == 0:
+            continue
+        if op == "back":
+            dh = torch.mm(d["dy"].index_select(0, mine).double(), weights("down", e))
+            value, slope = _phi(d["gate"].index_select(0, mine).double(), act)
+            res = [dh * d["up"].index_select(0, mine).double() * slope, dh * value]
+            res.append(torch.mm(res[0], weights("gate", e)) + torch.mm(res[1], weights("up", e)))
+        else:
+            x = d["x"].index_select(0, mine).double()
+            gate, up = torch.mm(x, weights("gate", e)), torch.mm(x, weights("up", e))
+            h = _phi(gate, act)[0] * up
+            res = [h, gate, up] if op == "glu" else [h, torch.mm(h, weights("down", e))]
+        for o, v in zip(outs, res):
+            o.index_copy_(0, mine, v)
+    if op == "glu":
+        return tuple(outs) if case["keep"] else outs[0]
+    return tuple(outs)
