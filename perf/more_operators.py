@@ -4,9 +4,9 @@
          with both projections kept
   back   its backward pass: ciera_glu_grad (the gradients of both projections from that of
          the block's output, through w_down) and ciera_glu_xgrad (the gradient of x)
-  quant  ciera_q4_quantize and ciera_q4_dequantize: a stack of matrices to 4-bit integers
+  quant  ciera_gq_quantize and ciera_gq_dequantize: a stack of matrices to 4-bit integers
          with a scale (and a zero) for every 32, 64 or 128 values, and back
-  q4     a serving step on such weights: ciera_q4_glu, then ciera_q4_mm with w_down
+  q4     a serving step on such weights: ciera_gq_glu, then ciera_gq_mm with w_down
 
 ``run`` computes a case in its plain form (elementary torch operations in 32 bits, rounded
 once) or, where ``own`` is true, through the package's calls.
@@ -252,16 +252,16 @@ def prepare(case, seed):
         s["h"], s["y"] = buffer(case["n"]), buffer(case["k"])
     if own:
         import lossless_weight_compression_amd as ciera
-        from lossless_weight_compression_amd.layer import Q4Matrix
+        from lossless_weight_compression_amd.layer import GqMatrix
         s["ciera"] = ciera
         if op == "quant":
             g, r, c = s["out"].shape
-            s["q"] = Q4Matrix(r, c, groups=g, block=case["block"], dtype=DTYPES[case["scales"]],
+            s["q"] = GqMatrix(r, c, groups=g, block=case["block"], dtype=DTYPES[case["scales"]],
                               with_zeros=case["zeros"])
         elif op == "q4":
             for name in ("gate", "up", "down"):
                 w = s[name]
-                s["q_" + name] = Q4Matrix(w["rows"], w["cols"], groups=w["groups"], block=w["block"],
+                s["q_" + name] = GqMatrix(w["rows"], w["cols"], groups=w["groups"], block=w["block"],
                                           codes=w["codes"], scales=w["scales"], zeros=w["zeros"])
     return s
 
@@ -284,11 +284,11 @@ def _run_own(s):
                               transpose_w=case["transpose"])
         return s["dgate"], s["dup"], s["dx"]
     if op == "quant":
-        ciera.ciera_q4_quantize(s["x"], s["q"], axis=case["axis"])
-        ciera.ciera_q4_dequantize(s["q"], s["out"])
+        ciera.ciera_gq_quantize(s["x"], s["q"], axis=case["axis"])
+        ciera.ciera_gq_dequantize(s["q"], s["out"])
         return s["out"]
-    ciera.ciera_q4_glu(s["x"], s["q_gate"], s["q_up"], s["h"], offsets=s["offsets"], act=case["act"])
-    ciera.ciera_q4_mm(s["h"], s["q_down"], s["y"], offsets=s["offsets"])
+    ciera.ciera_gq_glu(s["x"], s["q_gate"], s["q_up"], s["h"], offsets=s["offsets"], act=case["act"])
+    ciera.ciera_gq_mm(s["h"], s["q_down"], s["y"], offsets=s["offsets"])
     return s["h"], s["y"]
 
 
