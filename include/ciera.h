@@ -453,6 +453,93 @@ ciera_status_t ciera_group_mm(const ciera_matrix_t* x, const ciera_matrix_t* w, 
 ciera_status_t ciera_group_wgrad(const ciera_matrix_t* x, const ciera_matrix_t* dy, const int32_t* offsets,
                                  const ciera_matrix_t* out, void* stream);
 
+/* The experts' gated feed-forward block, h = act(G) U with G = x w_gate_g and
+ * U = x w_up_g on the rows of every group g, and its backward pass.  Types,
+ * offsets, transpose_w and sums as in ciera_group_mm (transpose_w 1: both
+ * stacks are groups x N x K); the activation is computed in fp32 from the
+ * unrounded sums:
+ *   CIERA_ACT_SILU  act(v) = v s(v), s(z) = 1 / (1 + exp(-z))
+ *   CIERA_ACT_GELU  act(v) = v s(2 c (v + 0.044715 v^3)), c = sqrt(2 / pi)
+ * Results that a call writes together are of one type, and may lie side by side
+ * as columns of one buffer (equal row strides); else their address ranges must
+ * not overlap, nor overlap an input's: INVALID_ARG. */
+typedef enum { CIERA_ACT_SILU = 1, CIERA_ACT_GELU = 2 } ciera_act_t;
+
+/* ciera_glu_mm -- out = act(G) U in one pass over x.  w_gate and w_up are of one
+ * shape.  gate and up, both or neither: where G and U are kept for the backward
+ * pass, each rounded once. */
+ciera_status_t ciera_glu_mm(const ciera_matrix_t* x, const ciera_matrix_t* w_gate, const ciera_matrix_t* w_up,
+                            uint32_t transpose_w, uint32_t act, const int32_t* offsets, const ciera_matrix_t* out,
+                            const ciera_matrix_t* gate, const ciera_matrix_t* up, void* stream);
+
+/* ciera_glu_grad -- the gradients of G and U from the gradient dy of y = h w_down:
+ * with D = dy w_g (transpose_w as in ciera_group_mm, so with y = h w_down the
+ * other one), dgate = D U act'(G) and dup = D act(G).  D stays in fp32 and is not
+ * written.  gate and up as ciera_glu_mm kept them; gate, up, dgate and dup are of
+ * one type, that of dy or fp32. */
+ciera_status_t ciera_glu_grad(const ciera_matrix_t* dy, const ciera_matrix_t* w_down, uint32_t transpose_w,
+                              uint32_t act, const int32_t* offsets, const ciera_matrix_t* gate,
+                              const ciera_matrix_t* up, const ciera_matrix_t* dgate, const ciera_matrix_t* dup,
+                              void* stream);
+
+/* ciera_glu_xgrad -- the gradient of x: out = dgate w_gate_g + dup w_up_g
+ * (transpose_w as in ciera_group_mm), both products in one sum.  The gradients
+ * of the weights are ciera_group_wgrad(x, dgate) and ciera_group_wgrad(x, dup). */
+ciera_status_t ciera_glu_xgrad(const ciera_matrix_t* dgate, const ciera_matrix_t* dup, const ciera_matrix_t* w_gate,
+                               const ciera_matrix_t* w_up, uint32_t transpose_w, const int32_t* offsets,
+                               const ciera_matrix_t* out, void* stream);
+
+/* A stack of matrices in 4-bit integers with a scale, and optionally a zero, for
+ * every `block` (32, 64 or 128) values of a row.  Per row, cols padded to a
+ * multiple of 128 (kp), all dense:
+ *   codes  [groups][rows][kp / 2]: of every 128 values of a row, byte b of word
+ *     4 q + u (words of 4 bytes; b, q, u from 0 to 3) holds value 32 u + 8 q + b
+ *     in its low half and value 32 u + 8 q + b + 4 in its high half; 16-byte
+ *     aligned
+ *   scales [groups][rows][kp / block] of scale_dtype (bf16 or fp16); 4-byte aligned
+ *   zeros  [groups][rows][kp / block] bytes of 0 to 15, 4-byte aligned; NULL: every
+ *     zero is 8
+ * Code q of a block with scale s and zero z stands for s (q - z).  Codes past cols
+ * count for nothing as long as their scales are finite. */
+typedef struct {
+  uint8_t* codes;
+  void* scales;
+  uint8_t* zeros;
+  uint32_t groups, block, scale_dtype, reserved;
+  uint64_t rows, cols;
+} ciera_gq_t;
+
+/* ciera_gq_sizes -- bytes of the codes, the scales and the zeros.  Host only. */
+ciera_status_t ciera_gq_sizes(uint32_t groups, uint64_t rows, uint64_t cols, uint32_t block, uint64_t* code_bytes,
+                              uint64_t* scale_bytes, uint64_t* zero_bytes);
+
+/* ciera_gq_quantize -- x (bf16, fp16 or fp32) to 4 bits, blocks along `axis` as in
+ * ciera_mx_quantize.  With zeros, lo = min(block, 0) and hi = max(block, 0): s is
+ * (hi - lo) / 15 in fp32, rounded to scale_dtype, z = clamp(rint(-lo / s), 0, 15)
+ * and q = clamp(rint(v / s) + z, 0, 15) (quotients in fp32, ties to even).
+ * Without, s is max |v| / 7, rounded, and z is 8.  A scale below 2^-126 becomes 0,
+ * all codes then z, z 0 if kept.  A block with an infinity, a NaN or a scale past
+ * the end of its type gets the scale NaN, codes and zero 0.  The end of a last
+ * block, past q.cols, counts as zeros. */
+ciera_status_t ciera_gq_quantize(const ciera_matrix_t* x, uint32_t axis, const ciera_gq_t* q, void* stream);
+
+/* ciera_gq_dequantize -- the values q stands for, rounded once to out's type.  out
+ * has q's groups, rows and cols. */
+ciera_status_t ciera_gq_dequantize(const ciera_gq_t* q, const ciera_matrix_t* out, void* stream);
+
+/* ciera_gq_mm -- out[i, n] = sum_k x[i, k] w_g[n, k] for the group g of row i: x
+ * (bf16 or fp16) one group, rows x K; w groups x N x K; out rows x N, of x's type
+ * or fp32.  No weight is rounded: the sums of a block's x and of its x q are held
+ * in fp32, then scaled.  A row of x with an infinity or a NaN gives NaN. */
+ciera_status_t ciera_gq_mm(const ciera_matrix_t* x, const ciera_gq_t* w, const int32_t* offsets,
+                           const ciera_matrix_t* out, void* stream);
+
+/* ciera_gq_glu -- out = act(x w_gate_g^T) (x w_up_g^T), as ciera_gq_mm and
+ * ciera_glu_mm.  w_gate and w_up agree in everything but their pointers, and both
+ * or neither have zeros. */
+ciera_status_t ciera_gq_glu(const ciera_matrix_t* x, const ciera_gq_t* w_gate, const ciera_gq_t* w_up, uint32_t act,
+                            const int32_t* offsets, const ciera_matrix_t* out, void* stream);
+
 const char* ciera_status_str(ciera_status_t s);
 uint32_t ciera_abi_version(void);
 

@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libciera.so
 CIERA_BF16, CIERA_FP32, CIERA_FP16 = 1, 2, 3
 RAW, COMPRESSED, BLOCK, CODED = 0, 1, 2, 3  # encode item `compress` values and stream modes
 CIERA_TENSOR_CODED = 1  # Tensor.flags: the tensor's streams may be CODED
+CIERA_ACT_SILU, CIERA_ACT_GELU = 1, 2
 CIERA_OK, CIERA_ERR_INVALID_ARG, CIERA_ERR_BUFFER_TOO_SMALL, CIERA_ERR_UNSUPPORTED, CIERA_ERR_DEVICE = range(5)
 CIERA_ST_MAGIC, CIERA_ST_FIELD, CIERA_ST_LENGTH, CIERA_ST_PATCH, CIERA_ST_BITMAP = 1, 2, 4, 8, 16
 HEADER_BYTES = 64
@@ -23,7 +24,8 @@ EXPORTS = ["ciera_plan", "ciera_plan_batch", "ciera_select", "ciera_shard", "cie
            "ciera_encode_prepare", "ciera_encode_launch", "ciera_decode_scratch_bytes",
            "ciera_decode", "ciera_decode_prepare", "ciera_decode_launch", "ciera_cache_update",
            "ciera_hash_update", "ciera_mx_sizes", "ciera_mx_quantize", "ciera_mx_dequantize", "ciera_mx_mm",
-           "ciera_group_mm", "ciera_group_wgrad", "ciera_set_sync_polls", "ciera_encode_noalloc", "ciera_decode_launch_bounded",
+           "ciera_group_mm", "ciera_group_wgrad", "ciera_glu_mm", "ciera_glu_grad", "ciera_glu_xgrad", "ciera_gq_sizes",
+           "ciera_gq_quantize", "ciera_gq_dequantize", "ciera_gq_mm", "ciera_gq_glu", "ciera_set_sync_polls", "ciera_encode_noalloc", "ciera_decode_launch_bounded",
            "ciera_status_str", "ciera_abi_version", "ciera_last_error"]
 
 
@@ -82,6 +84,13 @@ class Mx(ctypes.Structure):
                 ("rows", c_uint64), ("cols", c_uint64)]
 
 
+class Gq(ctypes.Structure):
+    """A stack of 4-bit integer matrices: codes, scales and zeros in device memory."""
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p), ("zeros", c_void_p), ("groups", c_uint32),
+                ("block", c_uint32), ("scale_dtype", c_uint32), ("reserved", c_uint32), ("rows", c_uint64),
+                ("cols", c_uint64)]
+
+
 class Batch(ctypes.Structure):
     """Host handle of a prepared batch (CIERA_BATCH_BYTES opaque bytes)."""
     _fields_ = [("opaque", c_uint64 * 512)]
@@ -134,6 +143,19 @@ def _load() -> ctypes.CDLL:
         "ciera_group_mm": (c_int, [POINTER(Matrix), POINTER(Matrix), c_uint32, c_void_p, POINTER(Matrix),
                                    c_void_p]),
         "ciera_group_wgrad": (c_int, [POINTER(Matrix), POINTER(Matrix), c_void_p, POINTER(Matrix), c_void_p]),
+        "ciera_glu_mm": (c_int, [POINTER(Matrix), POINTER(Matrix), POINTER(Matrix), c_uint32, c_uint32, c_void_p,
+                                 POINTER(Matrix), POINTER(Matrix), POINTER(Matrix), c_void_p]),
+        "ciera_glu_grad": (c_int, [POINTER(Matrix), POINTER(Matrix), c_uint32, c_uint32, c_void_p, POINTER(Matrix),
+                                   POINTER(Matrix), POINTER(Matrix), POINTER(Matrix), c_void_p]),
+        "ciera_glu_xgrad": (c_int, [POINTER(Matrix), POINTER(Matrix), POINTER(Matrix), POINTER(Matrix), c_uint32,
+                                    c_void_p, POINTER(Matrix), c_void_p]),
+        "ciera_gq_sizes": (c_int, [c_uint32, c_uint64, c_uint64, c_uint32, POINTER(c_uint64), POINTER(c_uint64),
+                                   POINTER(c_uint64)]),
+        "ciera_gq_quantize": (c_int, [POINTER(Matrix), c_uint32, POINTER(Gq), c_void_p]),
+        "ciera_gq_dequantize": (c_int, [POINTER(Gq), POINTER(Matrix), c_void_p]),
+        "ciera_gq_mm": (c_int, [POINTER(Matrix), POINTER(Gq), c_void_p, POINTER(Matrix), c_void_p]),
+        "ciera_gq_glu": (c_int, [POINTER(Matrix), POINTER(Gq), POINTER(Gq), c_uint32, c_void_p, POINTER(Matrix),
+                                 c_void_p]),
         "ciera_set_sync_polls": (None, [c_uint32]),
         "ciera_encode_noalloc": (c_int, [POINTER(EncodeItem), c_uint32, c_void_p]),
         "ciera_status_str": (c_char_p, [c_int]),
@@ -495,3 +517,118 @@ def ciera_group_wgrad(x, dy, out, offsets=None, stream=None) -> None:
     mo = matrix_item(out, "out")
     _check(_lib.ciera_group_wgrad(byref(matrix_item(x, "x")), byref(matrix_item(dy, "dy")),
                                   _offsets(offsets, mo.groups), byref(mo), _stream(stream)), "ciera_group_wgrad")
+
+
+# ----------------------------- the gated feed-forward block, group-scaled 4-bit weights
+
+_ACTS = {"silu": CIERA_ACT_SILU, "gelu": CIERA_ACT_GELU}
+
+
+def _act(act) -> int:
+    code = _ACTS.get(act, act)
+    if type(code) is not int:
+        raise ValueError(f"act: {act!r}, expected 'silu' or 'gelu'")
+    return code
+
+
+def gq_item(codes, scales, zeros, groups: int, rows: int, cols: int, block: int = 128, scale_dtype=None) -> Gq:
+    """codes and zeros: byte tensors (or addresses), scales: a bf16 or fp16 tensor (or an
+    address, with scale_dtype), of ciera_gq_sizes bytes; zeros None: every zero is 8."""
+    need = ciera_gq_sizes(groups, rows, cols, block)
+    ptrs = []
+    for t, n, what in ((codes, need[0], "codes"), (scales, need[1] // 2, "scales"), (zeros, need[2], "zeros")):
+        if t is not None and not isinstance(t, int):
+            if what == "scales":
+                code = _TORCH_CODES.get(t.dtype)
+                if code not in (CIERA_BF16, CIERA_FP16) or (scale_dtype is not None and scale_dtype != code):
+                    raise ValueError(f"scales: dtype {t.dtype}, expected bfloat16 or float16"
+                                     + ("" if scale_dtype is None else " as scale_dtype says"))
+                scale_dtype = code
+            elif t.dtype is not torch.uint8:
+                raise ValueError(f"{what}: dtype {t.dtype}, expected uint8")
+            _on_current_device(t, what)
+        ptrs.append(_ptr(t, what, numel=n))
+    if scale_dtype is None:
+        raise ValueError("scales: an address needs a scale_dtype")
+    return Gq(ptrs[0], ptrs[1], ptrs[2], groups, block, scale_dtype, 0, rows, cols)
+
+
+def _gq(q) -> Gq:
+    """The Gq of a GqMatrix on the current device (a Gq is passed through)."""
+    if type(q) is Gq:
+        return q
+    if q.codes.get_device() != torch.cuda.current_device():
+        _on_current_device(q.codes, "4-bit matrix")
+    return q.item
+
+
+def ciera_gq_sizes(groups: int, rows: int, cols: int, block: int = 128) -> Tuple[int, int, int]:
+    """Bytes of the codes, the scales and the zeros of a stack."""
+    c, s, z = c_uint64(), c_uint64(), c_uint64()
+    _check(_lib.ciera_gq_sizes(groups, rows, cols, block, byref(c), byref(s), byref(z)), "ciera_gq_sizes")
+    return c.value, s.value, z.value
+
+
+def ciera_gq_quantize(x, q, axis: int = 1, stream=None) -> None:
+    """x [rows, cols] or [groups, rows, cols] to the 4-bit stack q, blocks along
+    axis 1 (the rows) or 0 (the columns: q is the transpose)."""
+    if axis not in (0, 1):
+        raise ValueError(f"axis: {axis}, expected 0 or 1")
+    _check(_lib.ciera_gq_quantize(byref(matrix_item(x, "x")), axis, byref(_gq(q)), _stream(stream)),
+           "ciera_gq_quantize")
+
+
+def ciera_gq_dequantize(q, out, stream=None) -> None:
+    """The values that the 4-bit stack q stands for."""
+    _check(_lib.ciera_gq_dequantize(byref(_gq(q)), byref(matrix_item(out, "out")), _stream(stream)),
+           "ciera_gq_dequantize")
+
+
+def ciera_gq_mm(x, w, out, offsets=None, stream=None) -> None:
+    """out[i] = x[i] w_g^T for the rows offsets[g] <= i < offsets[g + 1] of every group g of the
+    4-bit stack w [groups, N, K]."""
+    qw = _gq(w)
+    _check(_lib.ciera_gq_mm(byref(matrix_item(x, "x")), byref(qw), _offsets(offsets, qw.groups),
+                            byref(matrix_item(out, "out")), _stream(stream)), "ciera_gq_mm")
+
+
+def ciera_gq_glu(x, w_gate, w_up, out, offsets=None, act="silu", stream=None) -> None:
+    """out[i] = act(x[i] w_gate_g^T) * (x[i] w_up_g^T) on the rows of every group g of two 4-bit stacks."""
+    qg = _gq(w_gate)
+    _check(_lib.ciera_gq_glu(byref(matrix_item(x, "x")), byref(qg), byref(_gq(w_up)), _act(act),
+                             _offsets(offsets, qg.groups), byref(matrix_item(out, "out")), _stream(stream)),
+           "ciera_gq_glu")
+
+
+def _optional(t, what: str):
+    return None if t is None else byref(matrix_item(t, what))
+
+
+def ciera_glu_mm(x, w_gate, w_up, out, offsets=None, transpose_w: bool = False, act="silu", gate=None, up=None,
+                 stream=None) -> None:
+    """out[i] = act(x[i] w_gate_g) * (x[i] w_up_g) (transpose_w: the weights are [groups, N, K]) for
+    the rows of every group g; gate and up: where both products are kept for ciera_glu_grad."""
+    wg = matrix_item(w_gate, "w_gate")
+    _check(_lib.ciera_glu_mm(byref(matrix_item(x, "x")), byref(wg), byref(matrix_item(w_up, "w_up")), int(transpose_w),
+                             _act(act), _offsets(offsets, wg.groups), byref(matrix_item(out, "out")),
+                             _optional(gate, "gate"), _optional(up, "up"), _stream(stream)), "ciera_glu_mm")
+
+
+def ciera_glu_grad(dy, w_down, gate, up, dgate, dup, offsets=None, transpose_w: bool = False, act="silu",
+                   stream=None) -> None:
+    """dgate = D * up * act'(gate) and dup = D * act(gate) with D[i] = dy[i] w_down_g (transpose_w:
+    dy[i] w_down_g^T) for the rows of every group g."""
+    mw = matrix_item(w_down, "w_down")
+    _check(_lib.ciera_glu_grad(byref(matrix_item(dy, "dy")), byref(mw), int(transpose_w), _act(act),
+                               _offsets(offsets, mw.groups), byref(matrix_item(gate, "gate")),
+                               byref(matrix_item(up, "up")), byref(matrix_item(dgate, "dgate")),
+                               byref(matrix_item(dup, "dup")), _stream(stream)), "ciera_glu_grad")
+
+
+def ciera_glu_xgrad(dgate, dup, w_gate, w_up, out, offsets=None, transpose_w: bool = False, stream=None) -> None:
+    """out[i] = dgate[i] w_gate_g + dup[i] w_up_g (transpose_w: with their transposes) for the rows of
+    every group g: the gradient of ciera_glu_mm's x, with the other transpose_w."""
+    wg = matrix_item(w_gate, "w_gate")
+    _check(_lib.ciera_glu_xgrad(byref(matrix_item(dgate, "dgate")), byref(matrix_item(dup, "dup")), byref(wg),
+                                byref(matrix_item(w_up, "w_up")), int(transpose_w), _offsets(offsets, wg.groups),
+                                byref(matrix_item(out, "out")), _stream(stream)), "ciera_glu_xgrad")

@@ -17,10 +17,10 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void group_mm_mid(GroupMmArgs a) {
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
   // the last tile ends with the matrix: it gives some columns a second time, the same values
   const int n0 = TRANS ? tn * 128 : max(min(tn * 128, a.n - 128), 0);
-  mid_tile<D, true, TRANS, O, BM, TEAMS>(
+  mid_tile<D, true, TRANS, BM, TEAMS>(
       static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, t.count - t.m * BM,
       static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, a.n - n0, a.k,
-      static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo);
+      MidStore<O>{static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo});
 }
 
 template <typename D, typename O, int BM, int TEAMS>
@@ -37,9 +37,10 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void group_wgrad_mid(GroupWgradArgs
   group_range(a.offsets, g, a.rows, &begin, &count);
   begin = __builtin_amdgcn_readfirstlane(begin);
   count = __builtin_amdgcn_readfirstlane(count);
-  mid_tile<D, false, false, O, BM, TEAMS>(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
-                                   static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, a.n - n0, count,
-                                   static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo);
+  mid_tile<D, false, false, BM, TEAMS>(
+      static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, a.k - m0,
+      static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, a.n - n0, count,
+      MidStore<O>{static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo});
 }
 
 template <typename D, bool TRANS, typename O>

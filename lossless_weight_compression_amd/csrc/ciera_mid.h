@@ -17,8 +17,26 @@ struct StageLoad {
   uint64_t ld;
   int line, col, left;  // of the first chunk; columns left from there (not KC)
 
-  __device__ __forceinline__ void init(const uint16_t* base, uint64_t l, int lines) {
+  // PAIR: the first half of the rows (KC) or columns from `base`, the other one from `base2`.
+  template <bool PAIR = false>
+  __device__ __forceinline__ void init(const uint16_t* base, uint64_t l, int lines, const uint16_t* base2 = nullptr,
+                                       uint64_t l2 = 0) {
     const int tid = threadIdx.x & 255;
+    if constexpr (PAIR) {
+      constexpr int H = R / 2;
+      line = tid / Any::kPerRow;
+      col = tid % Any::kPerRow * 8;
+      const bool second = !KC && col >= H;
+      ld = second ? l2 : l;
+      left = lines - (col & (H - 1));
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const int k = line + i * (256 / Any::kPerRow);
+        if (KC) p[i] = (i < N / 2 ? base + (uint64_t)min(k, lines - 1) * l : base2 + (uint64_t)min(k - H, lines - 1) * l2) + col;
+        else p[i] = (second ? base2 - H : base) + (uint64_t)k * ld + col;
+      }
+      return;
+    }
     ld = l;
     line = tid / Any::kPerRow;
     col = tid % Any::kPerRow * 8;
@@ -45,6 +63,21 @@ struct StageLoad {
   }
 };
 
+// What becomes of a tile's results: put(row, column, columns left from there, values of 8
+// columns), for rows of the tile only.
+template <typename O>
+struct MidStore {
+  O* out;
+  uint64_t ldo;
+  __device__ __forceinline__ void put(int r, int c, int left, f32x4 lo, f32x4 hi) const {
+    store_row8(out + (uint64_t)r * ldo + c, left, lo, hi);
+  }
+};
+
+// PLAIN: C = A B.  PAIR: A B and A B2, 64 columns of each in the place of the tile's 128;
+// put() gets both products' values.  SUM: A B + A2 B2, one product to each of two teams.
+enum class Mid { PLAIN, PAIR, SUM };
+
 // One BM x 128 tile of C = A B, 4 waves of BM / 2 x 64.  Stages of 64 contraction steps
 // (256 codes) go from memory into registers, DEPTH of them under way (4 are no faster than
 // 2), from there into one half of LDS while the other is multiplied.  A has `am` rows left, B `bn` columns.  The
@@ -56,17 +89,20 @@ struct StageLoad {
 // TEAMS 2: two teams of 4 waves, each with half of the stages; the second one's sums are
 // added to the first's through LDS.  For two-byte tiles that are too few to fill the card
 // otherwise.
-template <typename D, bool AKC, bool BKC, typename O, int BM, int TEAMS>
+template <typename D, bool AKC, bool BKC, int BM, int TEAMS, Mid KIND = Mid::PLAIN, typename Out>
 __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
-                                         int klen, O* out, uint64_t ldo, const uint8_t* sa = nullptr,
-                                         const uint8_t* sb = nullptr, uint32_t srow = 0) {
-  constexpr int BN = 128, BK = 64, WM = BM / 32, WN = 4, ROWS = BM + BN, DEPTH = 2;
+                                         int klen, Out out, const uint8_t* sa = nullptr, const uint8_t* sb = nullptr,
+                                         uint32_t srow = 0, const uint16_t* b2 = nullptr, uint64_t ldb2 = 0,
+                                         const uint16_t* a2 = nullptr, uint64_t lda2 = 0) {
+  constexpr bool PAIR = KIND == Mid::PAIR, SUM = KIND == Mid::SUM;
+  constexpr int BN = 128, BK = 64, WM = BM / 32, WN = 4, ROWS = BM + BN, DEPTH = 2, COLUMNS = PAIR ? BN / 2 : BN;
   typedef StageTile<AKC, false, 16, BM> TA;
   typedef StageTile<BKC, true, 16, BN> TB;
   typedef StageLoad<AKC, BM> LA;
   typedef StageLoad<BKC, BN> LB;
   typedef typename D::V V;
-  static_assert(TEAMS == 1 || !D::kScaled, "one team for scaled operands");
+  static_assert((TEAMS == 1 && KIND == Mid::PLAIN) || !D::kScaled, "one team and one product for scaled operands");
+  static_assert(TEAMS == 2 || !SUM, "a team to each product");
   constexpr int HALF = TA::kChunks + TB::kChunks;
   static_assert(2 * HALF >= BM * BN / 4, "the joined sums take the place of a team's stages");
   __shared__ i32x4 lds[TEAMS * 2 * HALF];
@@ -77,21 +113,29 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
   i32x4* const lb[2] = {la[0] + TA::kChunks, la[1] + TA::kChunks};
   uint32_t* const ls[2] = {scales[team * 2], scales[team * 2 + 1]};
   // the team's stages; the second one's may be one less, and then end with zeros
-  const int steps = ((klen + BK - 1) / BK + TEAMS - 1) / TEAMS;
-  const int whole = TEAMS == 1 ? klen / BK : max(klen / BK - steps, 0);  // that every team has
-  if (TEAMS > 1 && team) {
+  const int steps = SUM ? (klen + BK - 1) / BK : ((klen + BK - 1) / BK + TEAMS - 1) / TEAMS;
+  const int whole = TEAMS == 1 || SUM ? klen / BK : max(klen / BK - steps, 0);  // that every team has
+  if (SUM) {
+    if (team) {
+      a = a2;
+      lda = lda2;
+      b = b2;
+      ldb = ldb2;
+    }
+  } else if (TEAMS > 1 && team) {
     const uint64_t k = (uint64_t)steps * BK;
     a += AKC ? k : k * lda;
     b += BKC ? k : k * ldb;
+    if (PAIR) b2 += BKC ? k : k * ldb2;
     klen = max(klen - steps * BK, 0);
   } else if (TEAMS > 1) {
     klen = min(klen, steps * BK);
   }
-  const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * 64;
+  const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * (COLUMNS / 2);
   LA ga;
   LB gb;
   ga.init(a, lda, am);
-  gb.init(b, ldb, bn);
+  gb.template init<PAIR>(b, ldb, bn, b2, ldb2);
   const uint8_t* ps = nullptr;
   if constexpr (D::kScaled)
     ps = tid < BM ? sa + (uint64_t)min(tid, am - 1) * srow : sb + (uint64_t)min(tid - BM, bn - 1) * srow;  // all in range
@@ -138,7 +182,7 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
       V fa[WM], fb[WN];
       int xa[WM], xb[WN];
       each<WN>([&](auto j) {
-        fb[j.v] = __builtin_bit_cast(V, TB::template fragment<j.v, part.v>(pb));
+        fb[j.v] = __builtin_bit_cast(V, TB::template fragment<j.v, part.v, PAIR ? 64 : 32>(pb));
         if constexpr (D::kScaled)
           xb[j.v] = reinterpret_cast<const uint8_t*>(
               ls[h])[(part.v * ROWS + BM + c0 + TB::first_row() + (j.v >> 1) * 32 + (j.v & 1) * 4) * 4 + (lane >> 4)];
@@ -159,7 +203,7 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
   };
   Regs r[DEPTH];  // stage s in r[s % DEPTH], then in half s % 2 of LDS
   int s = 0;
-  const int full = (AKC || am >= BM) && (BKC || bn >= BN) ? whole : 0;
+  const int full = (AKC || am >= BM) && (BKC || bn >= COLUMNS) ? whole : 0;
   each<DEPTH>([&](auto i) {
     if (full >= DEPTH) load_whole(r[i.v], i.v);
     else if (i.v < steps) load(r[i.v], i.v);
@@ -194,22 +238,18 @@ __device__ __forceinline__ void mid_tile(const uint16_t* a, uint64_t lda, int am
     each<WM * WN>([&](auto i) { acc[i.v / WN][i.v % WN] += __builtin_bit_cast(f32x4, sums[i.v * 64]); });
   }
   // a lane: row lane % 16 of each fragment, of its columns 8 * (lane / 16) ... in each 32
-  const int n = bn - c0 - (lane >> 4) * 8;
-  O* at = out + (uint64_t)(r0 + (lane & 15)) * ldo + c0 + (lane >> 4) * 8;
+  const int c = c0 + (lane >> 4) * 8;
 #pragma unroll
   for (int i = 0; i < WM; i++) {
-    if (r0 + i * 16 + (lane & 15) < am) {
-#pragma unroll
-      for (int j = 0; j < WN; j += 2) {
-        if (j * 16 + 8 <= n) {
-          store8(at + j * 16, acc[i][j], acc[i][j + 1]);
-        } else {
-          store4(at, j * 16, n, acc[i][j]);
-          store4(at, j * 16 + 4, n, acc[i][j + 1]);
-        }
+    const int r = r0 + i * 16 + (lane & 15);
+    if (r < am) {
+      if constexpr (PAIR) {
+        out.put(r, c, bn - c, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      } else {
+        out.put(r, c, bn - c, acc[i][0], acc[i][1]);
+        out.put(r, c + 32, bn - c - 32, acc[i][2], acc[i][3]);
       }
     }
-    at += 16 * ldo;
   }
 }
 

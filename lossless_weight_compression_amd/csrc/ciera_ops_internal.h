@@ -62,6 +62,80 @@ struct MxDequantArgs {
   int32_t groups, rows, cols;
 };
 
+// The gated block: with G = x Wg and U = x Wu, out = act(G) U; gate and up, where not null,
+// take G and U.
+struct GluMmArgs {
+  const void* x;
+  const void* wg;
+  const void* wu;
+  void* out;
+  void* gate;
+  void* up;
+  const int32_t* offsets;
+  uint64_t ldx, ldg, ldu, gsg, gsu;  // gs: of the stacks
+  uint64_t ldo, ldog, ldou;
+  int32_t rows, k, n, groups, act;
+};
+
+// With D = dy W: dgate = D up act'(gate), dup = D act(gate).
+struct GluGradArgs {
+  const void* dy;
+  const void* w;
+  const void* gate;
+  const void* up;
+  void* dgate;
+  void* dup;
+  const int32_t* offsets;
+  uint64_t ldx, ldw, gsw;
+  uint64_t ldg, ldu, lddg, lddu;
+  int32_t rows, k, n, groups, act;
+};
+
+// out = xg Wg + xu Wu.
+struct GluXgradArgs {
+  const void* xg;
+  const void* xu;
+  const void* wg;
+  const void* wu;
+  void* out;
+  const int32_t* offsets;
+  uint64_t ldxg, ldxu, ldg, ldu, gsg, gsu, ldo;
+  int32_t rows, k, n, groups;
+};
+
+// 4-bit integers with group scales; zeros null: all 8.
+struct GqStack {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint8_t* zeros;
+};
+// out = x W^T, or with w2 (GLU) act(x W^T) (x W2^T).
+struct GqMmArgs {
+  const void* x;
+  GqStack w[2];
+  void* out;
+  const int32_t* offsets;
+  uint64_t ldx, ldo;
+  int32_t rows, k, n, groups, act;
+  int32_t half;  // scales are fp16, else bf16
+};
+struct GqQuantArgs {
+  const void* x;
+  uint8_t* codes;
+  uint16_t* scales;
+  uint8_t* zeros;
+  uint64_t ldx, gsx;
+  int32_t groups, rows, cols;  // of x
+  int32_t half;
+};
+struct GqDequantArgs {
+  GqStack q;
+  void* out;
+  uint64_t ldo, gso;
+  int32_t groups, rows, cols;
+  int32_t half;
+};
+
 // Most row tiles of height bm that ascending offsets can make of `rows` rows.
 inline uint64_t max_row_tiles(uint64_t rows, uint64_t groups, uint64_t bm) {
   if (groups == 1) return (rows + bm - 1) / bm;
@@ -84,5 +158,13 @@ hipError_t launch_group_wgrad(int dtype, bool out_f32, bool flat, const GroupWgr
 hipError_t launch_mx_mm(int out_dtype, const MxMmArgs& a, hipStream_t s);
 hipError_t launch_mx_quantize(int dtype, int axis, const MxQuantArgs& a, hipStream_t s);
 hipError_t launch_mx_dequantize(int dtype, const MxDequantArgs& a, hipStream_t s);
+
+hipError_t launch_glu_mm(int dtype, bool out_f32, bool transpose_w, bool flat, const GluMmArgs& a, hipStream_t s);
+hipError_t launch_glu_grad(int dtype, bool out_f32, bool transpose_w, bool flat, const GluGradArgs& a, hipStream_t s);
+hipError_t launch_glu_xgrad(int dtype, bool out_f32, bool transpose_w, bool flat, const GluXgradArgs& a, hipStream_t s);
+// glu: the gated form
+hipError_t launch_gq_mm(int dtype, bool out_f32, bool glu, int block, const GqMmArgs& a, hipStream_t s);
+hipError_t launch_gq_quantize(int dtype, int axis, int block, const GqQuantArgs& a, hipStream_t s);
+hipError_t launch_gq_dequantize(int dtype, int block, const GqDequantArgs& a, hipStream_t s);
 
 }  // namespace ciera

@@ -229,9 +229,10 @@ struct StageTile {
     const int step = (lane >> 4) * 8 + ((lane >> 2) & 3), c = COLS ? p : p >> 1, half = COLS ? 0 : p & 1;
     return lds_address(lds) + pos(step, r0 / 8 + c) * 16 + half * 8;
   }
-  template <int F, int PART>
+  // GAP: COLS, from one pair of fragments to the next.
+  template <int F, int PART, int GAP = 32>
   static __device__ __forceinline__ s16x8 fragment(uint32_t place) {
-    constexpr int ROW = S == 32 ? F * 32 : COLS ? (F >> 1) * 32 + (F & 1) * 4 : F * 16;
+    constexpr int ROW = S == 32 ? F * 32 : COLS ? (F >> 1) * GAP + (F & 1) * 4 : F * 16;
     if constexpr (KC) return read_lds<s16x8>((place ^ (PART * (S == 16 ? 64 : 16))) + ROW * kPerRow * 16);
     constexpr int FLIP = ROW / 8 * 16, HALF = (ROW & 7) * 2;
     return read_transposed((place ^ FLIP) + PART * 32 * kPerRow * 16 + HALF, 4 * kPerRow * 16);
@@ -284,6 +285,18 @@ __device__ __forceinline__ void store4(O* row, int col, int cols, f32x4 v) {
       if (col + i < cols) row[col + i] = (O)v[i];
   }
 }
+// Up to 8 consecutive values of a row, zeros behind.
+template <typename O>
+__device__ __forceinline__ void load_row8(const O* at, int left, float* v) {
+  if (left >= 8) {
+    const Pack<O, 8> p = *reinterpret_cast<const Pack<O, 8>*>(at);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = (float)p.v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = i < left ? (float)at[i] : 0.f;
+  }
+}
 // 8 outputs: one store in two-byte types, two in fp32.
 template <typename O>
 __device__ __forceinline__ void store8(O* at, f32x4 lo, f32x4 hi) {
@@ -293,6 +306,16 @@ __device__ __forceinline__ void store8(O* at, f32x4 lo, f32x4 hi) {
   for (int i = 0; i < 8; i++) p[i / N].v[i % N] = (O)(i < 4 ? lo[i & 3] : hi[i & 3]);
 #pragma unroll
   for (int i = 0; i < 8 / N; i++) reinterpret_cast<Pack<O, N>*>(at)[i] = p[i];
+}
+// Up to 8.
+template <typename O>
+__device__ __forceinline__ void store_row8(O* at, int left, f32x4 lo, f32x4 hi) {
+  if (left >= 8) {
+    store8(at, lo, hi);
+  } else {
+    store4(at, 0, left, lo);
+    store4(at, 4, left, hi);
+  }
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ buffers, what one rank keeps across iterations and receives each iteration:
 and issues one batched ``ciera_encode`` (a rank's shards of every tensor) or one
 batched ``ciera_decode`` (every tensor from all W slots) per call.  ``stack``
 views the same matrix of several experts as one operand of the grouped products,
-``quantize`` makes its 4-bit copy.  torch is used for device memory and streams
+``quantize`` and ``quantize_groups`` make its 4-bit copies.  torch is used for device memory and streams
 only.
 """
 from __future__ import annotations
@@ -141,6 +141,24 @@ class LayerCodec:
         q.quantize(w, axis, stream)
         return q
 
+    def quantize_groups(self, indices: Sequence[int], axis: int = 0, block: int = 128,
+                        scale_dtype: torch.dtype = torch.bfloat16, zeros: bool = True,
+                        into: Optional["GqMatrix"] = None, stream=None) -> "GqMatrix":
+        """4-bit integer copy with a scale (and zero) for every ``block`` values of the rebuilt
+        tensors of these indices (one call), as ciera_gq_mm and ciera_gq_glu take it: axis 0 for
+        [in, out] matrices, 1 for [out, in] ones.  Without ``into`` its memory belongs to ``stream``."""
+        w = self.stack(indices)
+        g, r, c = w.shape
+        if axis not in (0, 1):
+            raise ValueError(f"axis: {axis}, expected 0 or 1")
+        shape = (r, c) if axis else (c, r)
+        q = into
+        if q is None:
+            with _memory_of(stream):
+                q = GqMatrix(*shape, groups=g, block=block, dtype=scale_dtype, with_zeros=zeros, device=self.device)
+        q.quantize(w, axis, stream)
+        return q
+
     def seed_cache(self, weights: Sequence[torch.Tensor], stream=None) -> None:
         """cache <- exponents of the given full tensors (exponent reuse switched on)."""
         for i, w in enumerate(weights):
@@ -259,4 +277,42 @@ class MxMatrix:
             with _memory_of(stream):
                 out = torch.empty(self.groups, self.rows, self.cols, dtype=torch.bfloat16, device=self.codes.device)
         B.ciera_mx_dequantize(self, out, stream)
+        return out
+
+
+class GqMatrix:
+    """Device memory of a stack of 4-bit integer matrices ([groups, rows, cols]) with a scale and
+    (``with_zeros``) a zero for every ``block`` values of a row: ``codes`` [groups, rows, kp / 2]
+    bytes, ``scales`` [groups, rows, kp / block] of ``dtype`` (bf16 or fp16), ``zeros`` the same in
+    bytes or None, kp = cols rounded up to 128; or the caller's own tensors of these sizes."""
+
+    def __init__(self, rows: int, cols: int, groups: int = 1, block: int = 128, dtype: torch.dtype = torch.bfloat16,
+                 with_zeros: bool = True, device="cuda", codes: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, zeros: Optional[torch.Tensor] = None):
+        B.ciera_gq_sizes(groups, rows, cols, block)  # refuses sizes the library does not take
+        kp = _align(cols, 128)
+        self.groups, self.rows, self.cols, self.block = groups, rows, cols, block
+        if (codes is None) != (scales is None) or (codes is None and zeros is not None):
+            raise ValueError("codes and scales: give both, or nothing")
+        if codes is None:
+            if dtype not in (torch.bfloat16, torch.float16):
+                raise ValueError(f"dtype: {dtype}, expected bfloat16 or float16")
+            codes = torch.empty(groups, rows, kp // 2, dtype=torch.uint8, device=device)
+            scales = torch.empty(groups, rows, kp // block, dtype=dtype, device=device)
+            if with_zeros:
+                zeros = torch.empty(groups, rows, kp // block, dtype=torch.uint8, device=device)
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.item = B.gq_item(codes, scales, zeros, groups, rows, cols, block)
+
+    def quantize(self, x: torch.Tensor, axis: int = 1, stream=None) -> "GqMatrix":
+        B.ciera_gq_quantize(x, self, axis, stream)
+        return self
+
+    def dequantize(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The values ([groups, rows, cols], bf16 unless ``out`` says otherwise; without
+        ``out`` their memory belongs to ``stream``)."""
+        if out is None:
+            with _memory_of(stream):
+                out = torch.empty(self.groups, self.rows, self.cols, dtype=torch.bfloat16, device=self.codes.device)
+        B.ciera_gq_dequantize(self, out, stream)
         return out
