@@ -42,6 +42,7 @@ __device__ __forceinline__ f32x4 gated(f32x4 g, f32x4 u, int act) {
 // Where a tile of the gated block goes: h, and G and U where they are kept.
 template <typename O>
 struct GluOut {
+  typedef O T;
   O *out, *gate, *up;
   uint64_t ldo, ldog, ldou;
   int act;
@@ -61,6 +62,7 @@ struct GluOut {
 // dG = D U act'(G) and dU = D act(G), G and U from memory.
 template <typename O>
 struct GradOut {
+  typedef O T;
   const O *gate, *up;
   O *dgate, *dup;
   uint64_t ldg, ldu, lddg, lddu;

@@ -1,5 +1,6 @@
 // The engine of the large products: 256 x 256 tiles fed straight into LDS.
 #pragma once
+#include "ciera_act.h"
 #include "ciera_tiles.h"
 
 namespace ciera {
@@ -23,6 +24,12 @@ __device__ __forceinline__ void load_lds16(const char* base, uint32_t offset, i3
                : "memory");
 }
 
+// A pointer that all lanes agree on, in scalar registers, where the compiler does not see that.
+__device__ __forceinline__ const char* scalar(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const char*>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v) |
+                                       (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32);
+}
 // 4 bytes per lane.
 __device__ __forceinline__ void load_lds4(const void* p, void* lds) {
   const uint32_t at = lds_address(lds);
@@ -43,6 +50,15 @@ __device__ __forceinline__ void store_past(O* at, const P& p) {
   __builtin_nontemporal_store(__builtin_bit_cast(i32x4, p), reinterpret_cast<i32x4_any*>(at));
 }
 
+// Where a tile's results go.
+template <typename O>
+struct BigOut {
+  typedef O T;
+  O* out;
+  uint64_t ldo;
+  __device__ __forceinline__ BigOut at(uint64_t row, int col) const { return BigOut{out + row * ldo + col, ldo}; }
+};
+
 // What a wave does with a stage in LDS: 128 x 64 results, by quarters of 4 parts.
 // read<U, I> fetches what part I of quarter U needs new, multiply<U, I> multiplies it; the
 // parts of a quarter may be read while the quarter before is multiplied.
@@ -55,6 +71,14 @@ struct WaveTile16 {
   typedef StageTile<AKC, false, 16> TA;
   typedef StageTile<BKC, false, 16> TB;
   typedef typename D::V V;
+  static constexpr int kCols = 256, kRows = 128;  // of a tile, of a wave
+  static constexpr bool kReads = false;  // the results' store reads other operands
+  template <typename O>
+  static constexpr int stores() {  // store instructions of a whole tile
+    return 8 * (int)sizeof(O);
+  }
+  static __device__ __forceinline__ int row0(int wave) { return (wave >> 2) * 128; }
+  static __device__ __forceinline__ int col0(int wave) { return (wave & 3) * 64; }
   f32x4 acc[8][4];
   V fa[2][4], fb[2][4];
   uint32_t pa, pb;
@@ -92,7 +116,9 @@ struct WaveTile16 {
   // of 2048 x 1024 took 294 us for 285, the input gradient 310 for 291).
   static constexpr int kTurn = 128;
   template <bool WHOLE, typename O>
-  __device__ __forceinline__ void store(O* out, uint64_t ldo, int om, int on, i32x4* turn) {
+  __device__ __forceinline__ void store(const BigOut<O>& o, int om, int on, i32x4* turn) {
+    O* const out = o.out;
+    const uint64_t ldo = o.ldo;
     constexpr int PER = 16 / sizeof(O), SPLIT = sizeof(O) / 2;
     const int l = afresh(threadIdx.x & 63), row = l & 15, q = l >> 4, chunk = l & 7;
     each<8 * SPLIT>([&](auto step) {
@@ -132,6 +158,14 @@ struct WaveTile16 {
 struct WaveTile32 {
   typedef StageTile<true, false, 32> TA;
   typedef StageTile<true, true, 32> TB;
+  static constexpr int kCols = 256, kRows = 128;  // of a tile, of a wave
+  static constexpr bool kReads = false;  // the results' store reads other operands
+  template <typename O>
+  static constexpr int stores() {
+    return 8 * (int)sizeof(O);
+  }
+  static __device__ __forceinline__ int row0(int wave) { return (wave >> 2) * 128; }
+  static __device__ __forceinline__ int col0(int wave) { return (wave & 3) * 64; }
   f32x16 acc[4][2];
   i32x4 fa[2][4], fb[2][2];
   int xa[4], xb[2], yb[2];  // scale words; yb: of the next stage
@@ -171,7 +205,9 @@ struct WaveTile32 {
   // instruction, a tile of every unit took 7 us longer.)
   static constexpr int kTurn = 128;
   template <bool WHOLE, typename O>
-  __device__ __forceinline__ void store(O* out, uint64_t ldo, int om, int on, i32x4* turn) {
+  __device__ __forceinline__ void store(const BigOut<O>& o, int om, int on, i32x4* turn) {
+    O* const out = o.out;
+    const uint64_t ldo = o.ldo;
     constexpr int PER = 16 / sizeof(O), SPLIT = sizeof(O) / 2;
     const int l = afresh(threadIdx.x & 63), row = l & 15, h = l >> 5, chunk = l & 7;
     each<8 * SPLIT>([&](auto step) {
@@ -204,6 +240,170 @@ struct WaveTile32 {
     });
   }
 };
+// 16 rows of results and 64 / SPLIT columns to `out` through LDS, as WaveTile16::store: part
+// j of the columns is val(j), 4 columns of a row in a lane.
+template <bool WHOLE, typename O, typename F>
+__device__ __forceinline__ void store_rows16(F val, O* out, uint64_t ldo, int om, int on, i32x4* turn) {
+  constexpr int PER = 16 / sizeof(O), SPLIT = sizeof(O) / 2;
+  const int l = afresh(threadIdx.x & 63), row = l & 15, q = l >> 4, chunk = l & 7;
+#pragma unroll
+  for (int j = 0; j < 4 / SPLIT; j++) {
+    const f32x4 v = val(j);
+    const int at = SPLIT == 1 ? j * 2 + (q >> 1) : j * 4 + q;
+    Pack<O, 4> p;
+#pragma unroll
+    for (int e = 0; e < 4; e++) p.v[e] = (O)v[e];
+    char* to = reinterpret_cast<char*>(turn + row * 8 + (at ^ (row >> 1)));
+    __builtin_memcpy(__builtin_assume_aligned(to + (SPLIT == 1 ? (q & 1) * 8 : 0), 8 * SPLIT), &p, sizeof(p));
+  }
+  wave_order();
+#pragma unroll
+  for (int t = 0; t < 2; t++) {
+    const int r = t * 8 + (l >> 3), n = chunk * PER;
+    const Pack<O, PER> p = __builtin_bit_cast(Pack<O, PER>, turn[r * 8 + (chunk ^ (r >> 1))]);
+    O* at = out + (uint64_t)r * ldo + n;
+    if (WHOLE || (r < om && n + PER <= on)) {
+      store_past(at, p);
+    } else if (r < om) {
+#pragma unroll
+      for (int e = 0; e < PER; e++)
+        if (n + e < on) at[e] = p.v[e];
+    }
+  }
+  wave_order();
+}
+
+// Two products of the same rows: 64 rows and 64 columns of each to a wave.  The second
+// operands' halves of a stage lie behind each other, and a quarter is one product in half of
+// the stage.  So a lane holds both products of an element, and rows of 128 bytes of act(G) U
+// come out of one wave.
+template <typename D, bool AKC, bool BKC, bool KEEP>
+struct WaveTilePair {
+  typedef StageTile<AKC, false, 16> TA;
+  typedef StageTile<BKC, false, 16, 128> TB;
+  typedef typename D::V V;
+  static constexpr int kCols = 128, kRows = 64, kTurn = 128;
+  static constexpr bool kReads = false;
+  template <typename O>
+  static constexpr int stores() {
+    return 4 * (int)sizeof(O) * (KEEP ? 3 : 1);
+  }
+  static __device__ __forceinline__ int row0(int wave) { return (wave >> 1) * 64; }
+  static __device__ __forceinline__ int col0(int wave) { return (wave & 1) * 64; }
+  f32x4 acc[4][8];
+  V fa[2][4], fb[2][4];
+  uint32_t pa, pb;
+
+  __device__ __forceinline__ void init(const i32x4* lds, int r0, int c0) {
+    pa = TA::place(lds, r0);
+    pb = TB::place(lds + TA::kChunks, c0);
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+#pragma unroll
+      for (int j = 0; j < 8; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+  }
+  template <int U, int I>
+  __device__ __forceinline__ void read(uint32_t half) {
+    fb[U & 1][I] = __builtin_bit_cast(V, TB::template fragment<I, U / 2>(pb + half + (U & 1) * TB::kChunks * 16));
+    if constexpr (U % 2 == 0) fa[U / 2][I] = __builtin_bit_cast(V, TA::template fragment<I, U / 2>(pa + half));
+  }
+  template <int U, int I>
+  __device__ __forceinline__ void multiply() {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      f32x4& c = acc[i][(U & 1) * 4 + I];
+      c = mfma(fb[U & 1][I], fa[U / 2][i], c);
+    }
+  }
+  __device__ __forceinline__ void next_stage() {}
+  template <bool WHOLE, typename O>
+  __device__ __forceinline__ void store(const GluOut<O>& o, int om, int on, i32x4* turn) {
+    constexpr int SPLIT = sizeof(O) / 2;
+    each<4 * SPLIT>([&](auto step) {
+      constexpr int I = step.v / SPLIT, J = step.v % SPLIT * 2, C = J * 16;
+      const int m = om - I * 16, n = on - C;
+      store_rows16<WHOLE>([&](int j) { return gated(acc[I][J + j], acc[I][4 + J + j], o.act); },
+                          o.out + (uint64_t)(I * 16) * o.ldo + C, o.ldo, m, n, turn);
+      if constexpr (KEEP) {
+        store_rows16<WHOLE>([&](int j) { return acc[I][J + j]; }, o.gate + (uint64_t)(I * 16) * o.ldog + C, o.ldog, m, n, turn);
+        store_rows16<WHOLE>([&](int j) { return acc[I][4 + J + j]; }, o.up + (uint64_t)(I * 16) * o.ldou + C, o.ldou, m, n,
+                            turn);
+      }
+    });
+  }
+};
+
+// A product D that is not written itself: dG = D U act'(G) and dU = D act(G).  8 rows at a
+// time go through LDS in fp32, so that a lane has 8 consecutive columns for whole-line reads
+// of G and U and writes of dG and dU, and D is not rounded.
+template <typename D, bool AKC, bool BKC>
+struct WaveTileGrad : WaveTile16<D, AKC, BKC> {
+  static constexpr bool kReads = true;
+  template <typename O>
+  static constexpr int stores() {
+    return 16 * (int)sizeof(O);
+  }
+  template <typename O>
+  struct Eight {
+    Pack<O, 16 / sizeof(O)> v[sizeof(O) / 2];
+    __device__ __forceinline__ float operator[](int i) const { return (float)v[i * sizeof(O) / 16].v[i % (16 / sizeof(O))]; }
+  };
+  template <bool WHOLE, typename O>
+  __device__ __forceinline__ void store(const GradOut<O>& o, int om, int on, i32x4* turn) {
+    constexpr int AHEAD = 2, PER = 16 / sizeof(O);  // rows' operands under way; values of 16 bytes
+    const int l = afresh(threadIdx.x & 63), row = l & 15, q = l >> 4, r = l >> 3, c = (l & 7) * 8;
+    // a lane's place from the first of 8 rows (their strides are short), which all lanes agree on
+    const char *pg = scalar(reinterpret_cast<const char*>(o.gate)), *pu = scalar(reinterpret_cast<const char*>(o.up));
+    char* pdg = const_cast<char*>(scalar(reinterpret_cast<const char*>(o.dgate)));
+    char* pdu = const_cast<char*>(scalar(reinterpret_cast<const char*>(o.dup)));
+    const uint32_t og = (r * (uint32_t)o.ldg + c) * sizeof(O), ou = (r * (uint32_t)o.ldu + c) * sizeof(O);
+    const uint32_t odg = (r * (uint32_t)o.lddg + c) * sizeof(O), odu = (r * (uint32_t)o.lddu + c) * sizeof(O);
+    Eight<O> g[AHEAD], u[AHEAD];
+    auto load = [&](int s) {
+      g[s % AHEAD] = *reinterpret_cast<const Eight<O>*>(pg + og);
+      u[s % AHEAD] = *reinterpret_cast<const Eight<O>*>(pu + ou);
+      pg += 8 * o.ldg * sizeof(O);
+      pu += 8 * o.ldu * sizeof(O);
+    };
+    if (WHOLE) each<AHEAD - 1>([&](auto s) { load(s.v); });
+    each<16>([&](auto s) {
+      constexpr int I = s.v / 2, UP = s.v % 2;
+      if (WHOLE && s.v + AHEAD - 1 < 16) load(s.v + AHEAD - 1);
+      if ((row >> 3) == UP) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          turn[(row & 7) * 16 + ((j * 4 + q) ^ ((row & 7) * 2))] = __builtin_bit_cast(i32x4, this->acc[I][j]);
+      }
+      wave_order();
+      const f32x4 lo = __builtin_bit_cast(f32x4, turn[r * 16 + ((l & 7) ^ r) * 2]);
+      const f32x4 hi = __builtin_bit_cast(f32x4, turn[r * 16 + ((l & 7) ^ r) * 2 + 1]);
+      if constexpr (WHOLE) {
+        Eight<O> dg, du;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const float d = i < 4 ? lo[i & 3] : hi[i & 3];
+          float value, slope;
+          act_grad(g[s.v % AHEAD][i], o.act, &value, &slope);
+          dg.v[i / PER].v[i % PER] = (O)(d * u[s.v % AHEAD][i] * slope);
+          du.v[i / PER].v[i % PER] = (O)(d * value);
+        }
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(O) / 2; i++) {
+          store_past(reinterpret_cast<O*>(pdg + odg) + i * PER, dg.v[i]);
+          store_past(reinterpret_cast<O*>(pdu + odu) + i * PER, du.v[i]);
+        }
+        pdg += 8 * o.lddg * sizeof(O);
+        pdu += 8 * o.lddu * sizeof(O);
+      } else {
+        if (s.v * 8 + r < om) o.put(s.v * 8 + r, c, on - c, lo, hi);
+      }
+      wave_order();
+    });
+  }
+};
+
 template <typename D, bool AKC, bool BKC>
 struct WaveTileOf {
   typedef WaveTile16<D, AKC, BKC> T;
@@ -222,25 +422,33 @@ struct WaveTileOf<Mx4, true, true> {
 // before this one's results are stored, and do not wait for these stores.
 //
 // Scaled (4-bit) operands have the same shape in bytes.
-template <typename D, bool AKC, bool BKC, typename O>
+//
+// Big::PAIR: two second operands, 128 columns of each.  Big::SUM: a second pair of operands with
+// the strides of the first, whose stages follow on those of the first.
+enum class Big { PLAIN, PAIR, SUM };
+template <typename D, bool AKC, bool BKC, typename Out, Big KIND = Big::PLAIN,
+          typename Wave = typename WaveTileOf<D, AKC, BKC>::T>
 struct BigTiles {
-  static constexpr int BM = 256, BN = 256, BK = 64, T = 512;
-  typedef typename WaveTileOf<D, AKC, BKC>::T Wave;
+  typedef typename Out::T O;
+  static constexpr bool PAIR = KIND == Big::PAIR, SUM = KIND == Big::SUM;
+  static constexpr int BM = 256, BN = Wave::kCols, BK = 64, T = 512;
   typedef typename Wave::TA TA;
   typedef typename Wave::TB TB;
   static constexpr int kParts = TA::kChunks / T;  // of a stage's loads of one operand
-  static constexpr int kCodes = TA::kChunks + TB::kChunks;
+  static constexpr int kCodes = 2 * TA::kChunks;
   static constexpr int kStage = kCodes + (D::kScaled ? 256 : 0);  // chunks; scales: [operand][half][row] words
   static constexpr int kLds = 2 * kStage + 8 * Wave::kTurn;
   static constexpr int kLoads = 2 * kParts + (D::kScaled ? 2 : 0);  // a wave's load instructions for a stage
-  static constexpr int kStores = sizeof(O) == 2 ? 16 : 32;          // and its store instructions for a whole tile
+  static constexpr int kStores = Wave::template stores<O>();        // and its store instructions, where its part of the tile is whole
 
   i32x4* lds;
   int wave, lane, r0, c0;
-  bool ahead;                  // a whole tile's stores may still be under way
+  bool ahead;                  // the stores of all the wave's part of a tile may still be under way
   // the tile being loaded
   const char *pa, *pb;         // its operands at the next stage
-  uint64_t da, db;             // bytes from stage to stage
+  const char *pa2, *pb2;       // PAIR: the other second operand; SUM: the second pair
+  uint64_t da, db, db2;        // bytes from stage to stage
+  int again;                   // SUM: steps of the second pair, not begun yet
   uint32_t oa[kParts], ob[kParts];  // this lane's chunks of a stage, bytes from there
   int left;                    // contraction steps not loaded yet
   const char *sa, *sb;         // scaled: its scales at the next stage
@@ -252,8 +460,8 @@ struct BigTiles {
     lds = l;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     lane = threadIdx.x & 63;
-    r0 = (wave >> 2) * 128;
-    c0 = (wave & 3) * 64;
+    r0 = Wave::row0(wave);
+    c0 = Wave::col0(wave);
     ahead = false;
     tile.init(lds, r0, c0);
   }
@@ -261,12 +469,19 @@ struct BigTiles {
   // there; rows and columns past the tile's end repeat the last one.  Asks for the
   // first stage into half `buf` and the second, if there is one, into the other.
   __device__ __forceinline__ void start(const uint16_t* a, uint64_t lda, int am, const uint16_t* b, uint64_t ldb, int bn,
-                                        int klen, int buf) {
+                                        int klen, int buf, const uint16_t* b2 = nullptr, uint64_t ldb2 = 0,
+                                        const uint16_t* a2 = nullptr) {
     pa = reinterpret_cast<const char*>(a);
     pb = reinterpret_cast<const char*>(b);
     da = AKC ? BK * 2 : BK * 2 * lda;
     db = BKC ? BK * 2 : BK * 2 * ldb;
     left = klen;
+    if constexpr (PAIR) db2 = BKC ? BK * 2 : BK * 2 * ldb2;
+    if constexpr (PAIR || SUM) pb2 = reinterpret_cast<const char*>(b2);
+    if constexpr (SUM) {
+      pa2 = reinterpret_cast<const char*>(a2);
+      again = klen;
+    }
     const int tid = afresh(threadIdx.x);
 #pragma unroll
     for (int i = 0; i < kParts; i++) {
@@ -275,12 +490,24 @@ struct BigTiles {
     }
 #pragma unroll
     for (int i = 0; i < kParts; i++) {
-      const int p = i * T + tid, line = p / TB::kPerRow, c = TB::swizzle(line, p % TB::kPerRow) * 8;
-      ob[i] = 2 * (BKC ? (uint32_t)min(line, bn - 1) * (uint32_t)ldb + c : line * (uint32_t)ldb + min(c, bn - 8));
+      const int p = b_chunk(i, tid), line = p / TB::kPerRow, c = TB::swizzle(line, p % TB::kPerRow) * 8;
+      const uint32_t ld = PAIR && i >= kParts / 2 ? (uint32_t)ldb2 : (uint32_t)ldb;
+      ob[i] = 2 * (BKC ? (uint32_t)min(line, bn - 1) * ld + c : line * ld + min(c, bn - 8));
     }
+    keep_scalar();
     load(buf);
-    if (klen > BK) load(buf ^ 1);
+    if (klen > BK || SUM) load(buf ^ 1);
   }
+  // (all lanes agree on the operands' addresses, which the compiler loses sight of in these
+  // forms)
+  __device__ __forceinline__ void keep_scalar() {
+    if constexpr (SUM || Wave::kReads) {
+      pa = scalar(pa);
+      pb = scalar(pb);
+    }
+  }
+  // This lane's chunk of part i of the second operand (PAIR: of its operand)
+  static __device__ __forceinline__ int b_chunk(int i, int tid) { return (PAIR ? i % (kParts / 2) : i) * T + tid; }
   // The same for scaled operands of `row` bytes of scales a row; to be called before start.
   __device__ __forceinline__ void scales(const uint8_t* a, int am, const uint8_t* b, int bn, uint32_t row) {
     const int tid = afresh(threadIdx.x), r = tid & 255, h = tid >> 8;
@@ -302,10 +529,11 @@ struct BigTiles {
   template <bool FULL>
   __device__ __forceinline__ void load_b(int buf, int i) {
     i32x4* at = lds + buf * kStage + TA::kChunks + wave * 64 + i * T;
-    if (FULL) return load_lds16(pb, ob[i], at);
-    const int p = i * T + afresh(threadIdx.x), line = p / TB::kPerRow;
+    const char* from = PAIR && i >= kParts / 2 ? pb2 : pb;
+    if (FULL) return load_lds16(from, ob[i], at);
+    const int p = b_chunk(i, afresh(threadIdx.x)), line = p / TB::kPerRow;
     const int k = BKC ? TB::swizzle(line, p % TB::kPerRow) * 8 : line;
-    load_lds16(k < left ? pb + ob[i] : reinterpret_cast<const char*>(&kZeros), at);
+    load_lds16(k < left ? from + ob[i] : reinterpret_cast<const char*>(&kZeros), at);
   }
   template <bool FULL>
   __device__ __forceinline__ void load_scales(int buf) {
@@ -324,11 +552,21 @@ struct BigTiles {
   __device__ __forceinline__ void loaded() {
     pa += da;
     pb += db;
+    if constexpr (PAIR) pb2 += db2;
     if constexpr (D::kScaled) {
       sa += 8;
       sb += 8;
     }
     left -= BK;
+    if constexpr (SUM) {
+      if (left <= 0 && again) {
+        pa = pa2;
+        pb = pb2;
+        left = again;
+        again = 0;
+      }
+    }
+    keep_scalar();
   }
   __device__ __forceinline__ void load(int buf) {
     if (left >= BK) {
@@ -347,9 +585,11 @@ struct BigTiles {
     loaded();
   }
   // All but the last N of this wave's loads and stores are done (they end in order),
-  // as are its LDS reads; then the same for every wave.
-  template <int N>
+  // as are its LDS reads; then the same for every wave.  The counter has six bits: with more
+  // stores than that under way it waits for some of them too.
+  template <int MANY>
   static __device__ __forceinline__ void arrive() {
+    constexpr int N = MANY < 63 ? MANY : 63;
     __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0070);  // vmcnt N, lgkmcnt 0
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -394,7 +634,9 @@ struct BigTiles {
   // WORK: not for a wave without rows of the tile, which only loads.
   template <bool WORK>
   __device__ __forceinline__ void run(int klen, int* half) {
-    const int steps = max((klen + BK - 1) / BK, 1), full = klen / BK;
+    // (SUM: a whole stage may follow on one that is not)
+    const int steps = SUM ? 2 * ((klen + BK - 1) / BK) : max((klen + BK - 1) / BK, 1);
+    const int full = !SUM ? klen / BK : klen % BK ? 0 : steps;
     int buf = *half;
     // stage 0 is here; the second stage's loads and the last tile's stores may not be
     if (!ahead) arrive<0>();
@@ -426,14 +668,13 @@ struct BigTiles {
     else run<false>(klen, half);
   }
   // The last quarter, and the results.
-  __device__ __forceinline__ void finish(O* out, uint64_t ldo, int om, int on) {
-    ahead = om >= BM && on >= BN;
+  __device__ __forceinline__ void finish(const Out& out, int om, int on) {
+    ahead = om - r0 >= Wave::kRows && on - c0 >= 64;
     if (r0 >= om) return;
     each<4>([&](auto i) { tile.template multiply<3, i.v>(); });
-    out += (uint64_t)r0 * ldo + c0;
     i32x4* turn = lds + 2 * kStage + wave * Wave::kTurn;
-    if (ahead) tile.template store<true>(out, ldo, om - r0, on - c0, turn);
-    else tile.template store<false>(out, ldo, om - r0, on - c0, turn);
+    if (ahead) tile.template store<true>(out.at(r0, c0), om - r0, on - c0, turn);
+    else tile.template store<false>(out.at(r0, c0), om - r0, on - c0, turn);
   }
 };
 

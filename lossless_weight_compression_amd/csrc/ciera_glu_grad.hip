@@ -1,0 +1,66 @@
+// The gated block's backward pass: the gradients of both projections.
+#include "ciera_glu.h"
+
+namespace ciera {
+namespace {
+
+template <typename D, bool TRANS, typename O, int BM, int TEAMS>
+__global__ __launch_bounds__(256 * TEAMS, 2) void glu_grad_mid(GluGradArgs a) {
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + 127) / 128, blockIdx.x, &t, &tn)) return;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
+  const int n0 = TRANS ? tn * 128 : max(min(tn * 128, a.n - 128), 0);
+  const GradOut<O> out = {static_cast<const O*>(a.gate), static_cast<const O*>(a.up), static_cast<O*>(a.dgate),
+                          static_cast<O*>(a.dup), a.ldg, a.ldu, a.lddg, a.lddu, a.act};
+  mid_tile<D, true, TRANS, BM, TEAMS>(
+      static_cast<const uint16_t*>(a.dy) + row * a.ldx, a.ldx, t.count - t.m * BM,
+      static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, a.n - n0, a.k,
+      out.at(row, n0));
+}
+
+template <typename D, bool TRANS, typename O>
+__global__ __launch_bounds__(512) void glu_grad_big(GluGradArgs a) {
+  typedef BigTiles<D, true, TRANS, GradOut<O>, Big::PLAIN, WaveTileGrad<D, true, TRANS>> Tiles;
+  __shared__ i32x4 lds[Tiles::kLds];
+  Tiles big;
+  big.init(lds);
+  const GradOut<O> all = {static_cast<const O*>(a.gate), static_cast<const O*>(a.up), static_cast<O*>(a.dgate),
+                          static_cast<O*>(a.dup), a.ldg, a.ldu, a.lddg, a.lddu, a.act};
+  big_tiles<Tiles, GradOut<O>>(a.offsets, a.groups, a.rows, a.n, a.k, big, [&](int g, uint64_t row, int om, int n0, int on, int half) {
+    big.start(static_cast<const uint16_t*>(a.dy) + row * a.ldx, a.ldx, om, weights<TRANS>(a.w, g, a.gsw, a.ldw, n0), a.ldw, on,
+              a.k, half);
+    return all.at(row, n0);
+  });
+}
+
+template <typename D, bool TRANS, typename O>
+hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
+  if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 256) && short_stride(a.ldx) && short_stride(a.ldw) &&
+      short_stride(a.ldg) && short_stride(a.ldu) && short_stride(a.lddg) && short_stride(a.lddu)) {
+    glu_grad_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 64) * ((a.n + 127) / 128), 256, &grid)) return e;
+  glu_grad_mid<D, TRANS, O, 64, 1><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+struct RunGrad {
+  bool flat;
+  const GluGradArgs& a;
+  hipStream_t s;
+  template <typename D, bool TRANS, typename O>
+  hipError_t run() {
+    return run_glu_grad<D, TRANS, O>(flat, a, s);
+  }
+};
+
+}  // namespace
+
+hipError_t launch_glu_grad(int dtype, bool out_f32, bool transpose_w, bool flat, const GluGradArgs& a, hipStream_t s) {
+  return by_type(dtype, out_f32, transpose_w, RunGrad{flat, a, s});
+}
+
+}  // namespace ciera

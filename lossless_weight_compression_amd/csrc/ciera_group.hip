@@ -45,15 +45,17 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void group_wgrad_mid(GroupWgradArgs
 
 template <typename D, bool TRANS, typename O>
 __global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
-  __shared__ i32x4 lds[BigTiles<D, true, TRANS, O>::kLds];
+  typedef BigTiles<D, true, TRANS, BigOut<O>> Tiles;
+  __shared__ i32x4 lds[Tiles::kLds];
   GroupTiles<256> tiles;
   tiles.init(a.offsets, a.groups, a.rows);
   const uint32_t nt = (a.n + 255) / 256;
   TileList list;
   list.init((uint64_t)tiles.total * nt);
-  BigTiles<D, true, TRANS, O> big;
+  Tiles big;
   big.init(lds);
-  O* out;
+  const BigOut<O> all = {static_cast<O*>(a.out), a.ldo};
+  BigOut<O> out;
   int om, on, half = 0;
   // false: no more tiles, or a half without rows
   auto start = [&](uint32_t i) {
@@ -66,7 +68,7 @@ __global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
     om = min(t.count - t.m * 256 - r0, rows);
     on = a.n - n0;
     if (om <= 0) return false;
-    out = static_cast<O*>(a.out) + row * a.ldo + n0;
+    out = all.at(row, n0);
     big.start(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, om,
               static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (TRANS ? (uint64_t)n0 * a.ldw : n0), a.ldw, on,
               a.k, half);
@@ -75,10 +77,10 @@ __global__ __launch_bounds__(512) void group_mm_big(GroupMmArgs a) {
   if (!start(0)) return;
   for (uint32_t i = 1;; i++) {
     big.stages(om, a.k, &half);
-    O* done = out;
+    const BigOut<O> done = out;
     const int dm = om, dn = on;
     const bool more = start(i);
-    big.finish(done, a.ldo, dm, dn);
+    big.finish(done, dm, dn);
     if (!more) return;
   }
 }
@@ -201,16 +203,17 @@ struct GradTiles {
 
 template <typename D, typename O>
 __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
-  __shared__ i32x4 lds[BigTiles<D, false, false, O>::kLds];
+  typedef BigTiles<D, false, false, BigOut<O>> Tiles;
+  __shared__ i32x4 lds[Tiles::kLds];
   const uint32_t nt = (a.n + 255) / 256, stride = gridDim.x / kXcds, me = blockIdx.x / kXcds;
   GradTiles tiles;
   tiles.share(a, (uint32_t)((a.k + 255) / 256) * nt, blockIdx.x % kXcds);
   // the die's tiles are dealt to its workgroups forth and back: the first have most work
   uint64_t round = 0, tile = me;
   if (tile >= tiles.many) return;
-  BigTiles<D, false, false, O> big;
+  Tiles big;
   big.init(lds);
-  O* out;
+  BigOut<O> out;
   int om, on, count, half = 0;
   auto start = [&]() {
     int g, begin;
@@ -219,20 +222,20 @@ __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
     const int m0 = (int)(in / nt) * 256, n0 = (int)(in % nt) * 256;
     om = a.k - m0;
     on = a.n - n0;
-    out = static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0;
+    out = BigOut<O>{static_cast<O*>(a.out) + (uint64_t)g * a.gso + (uint64_t)m0 * a.ldo + n0, a.ldo};
     big.start(static_cast<const uint16_t*>(a.x) + (uint64_t)begin * a.ldx + m0, a.ldx, om,
               static_cast<const uint16_t*>(a.dy) + (uint64_t)begin * a.ldy + n0, a.ldy, on, count, half);
   };
   start();
   for (;;) {
     big.stages(om, count, &half);
-    O* done = out;
+    const BigOut<O> done = out;
     const int dm = om, dn = on;
     round++;
     tile = round * stride + (round & 1 ? stride - 1 - me : me);
     const bool more = tile < tiles.many;
     if (more) start();
-    big.finish(done, a.ldo, dm, dn);
+    big.finish(done, dm, dn);
     if (!more) return;
   }
 }

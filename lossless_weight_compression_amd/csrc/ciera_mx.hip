@@ -320,18 +320,19 @@ __global__ __launch_bounds__(256, 2) void mx_mm_mid(MxMmArgs a) {
 // Large products: 256 x 256 tiles, 256 codes of every row at a time.
 template <typename O>
 __global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
-  typedef BigTiles<Mx4, true, true, O> Big;
-  __shared__ i32x4 lds[Big::kLds];
+  typedef BigTiles<Mx4, true, true, BigOut<O>> Tiles;
+  __shared__ i32x4 lds[Tiles::kLds];
   GroupTiles<256> tiles;
   tiles.init(a.offsets, a.groups, a.rows);
   const uint32_t nt = (a.n + 255) / 256;
   TileList list;
   list.init((uint64_t)tiles.total * nt);
-  Big big;
+  Tiles big;
   big.init(lds);
   const int units = a.kp / 4;
   const uint32_t srow = a.kp / 32;
-  O* out;
+  const BigOut<O> all = {static_cast<O*>(a.out), a.ldo};
+  BigOut<O> out;
   int om, on, half = 0;
   auto start = [&](uint32_t i) {
     uint64_t tile;
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
     om = min(t.count - t.m * 256 - r0, rows);
     on = a.n - n0;
     if (om <= 0) return false;
-    out = static_cast<O*>(a.out) + row * a.ldo + n0;
+    out = all.at(row, n0);
     big.scales(a.sa + row * srow, om, a.sb + brow * srow, on, srow);
     big.start(reinterpret_cast<const uint16_t*>(a.a) + row * units, units, om,
               reinterpret_cast<const uint16_t*>(a.b) + brow * units, units, on, units, half);
@@ -352,10 +353,10 @@ __global__ __launch_bounds__(512) void mx_mm_big(MxMmArgs a) {
   if (!start(0)) return;
   for (uint32_t i = 1;; i++) {
     big.stages(om, units, &half);
-    O* done = out;
+    const BigOut<O> done = out;
     const int dm = om, dn = on;
     const bool more = start(i);
-    big.finish(done, a.ldo, dm, dn);
+    big.finish(done, dm, dn);
     if (!more) return;
   }
 }
