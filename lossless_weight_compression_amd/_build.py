@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libciera.so")
 SOURCES = ["ciera_api.cpp", "ciera_ops.cpp", "ciera_kernels.hip", "ciera_group.hip", "ciera_mx.hip", "ciera_glu.hip", "ciera_glu_grad.hip",
-           "ciera_glu_xgrad.hip", "ciera_gq.hip"]
+           "ciera_glu_xgrad.hip", "ciera_gq.hip", "ciera_gq_mm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,18 +1,11 @@
-// 4-bit integer weights with group scales: quantisation, its reverse, and the products of
-// two-byte activations with them.
+// 4-bit integer weights with group scales: quantisation and its reverse.
 //
 // A block of 32, 64 or 128 values v of a row shares a scale s and a zero z (0 to 15, 8 where
 // none are kept): code q stands for s (q - z).  With zeros s spreads the 16 codes over the
 // block's range, 0 in it: s = (hi - lo) / 15, z = rint(-lo / s), q = rint(v / s) + z, all
 // clamped to 0 ... 15; without, s = max |v| / 7.
-//
-// A word holds 8 consecutive values, byte b the codes of values b and b + 4.  The nibbles of
-// a byte, taken as an 8-bit float (4 exponent, 3 mantissa bits), are its subnormals and first
-// binade: q 2^-9 exactly.  So one conversion with the scale 2^9 makes two codes two-byte
-// floats, 7 vector instructions to a word (shifting codes into the mantissa of 16 took 8, and
-// left 16 + q to be corrected: 41 clocks a word with the matrix instruction, for 47).
 #include "ciera.h"
-#include "ciera_act.h"
+#include "ciera_gq.h"
 #include "ciera_ops_internal.h"
 #include "ciera_rows.h"
 #include "ciera_tiles.h"
@@ -20,11 +13,6 @@
 namespace ciera {
 namespace {
 
-constexpr uint32_t kCodeMask = 0x0f0f0f0fu;
-
-__device__ __forceinline__ float scale_of(uint32_t bits, int half) {
-  return half ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __builtin_bit_cast(float, bits << 16);
-}
 // s rounded to the scales' type, its bits; a scale below 2^-126 becomes 0.
 __device__ __forceinline__ uint32_t scale_bits(float s, int half) {
   if (half) return __builtin_bit_cast(uint16_t, (_Float16)s);
@@ -256,124 +244,6 @@ __global__ __launch_bounds__(256) void gq_dequantize(GqDequantArgs a, RowPass pa
   }
 }
 
-// 8 codes as two-byte floats, in order.
-__device__ __forceinline__ i32x4 expand(uint32_t w, Bf16) {
-  const uint32_t lo = w & kCodeMask, hi = w >> 4 & kCodeMask;
-  return i32x4{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true))};
-}
-__device__ __forceinline__ i32x4 expand(uint32_t w, Fp16) {
-  const uint32_t lo = w & kCodeMask, hi = w >> 4 & kCodeMask;
-  return i32x4{__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.f, false)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.f, true)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.f, false)),
-               __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.f, true))};
-}
-__device__ __forceinline__ i32x4 ones(Bf16) { return i32x4{0x3f803f80, 0x3f803f80, 0x3f803f80, 0x3f803f80}; }
-__device__ __forceinline__ i32x4 ones(Fp16) { return i32x4{0x3c003c00, 0x3c003c00, 0x3c003c00, 0x3c003c00}; }
-
-// y[m, n] = sum over blocks b of s[n, b] (sum_k x[m, k] q[n, k] - z[n, b] sum_k x[m, k]):
-// codes are exact in two bytes, both sums over a block come from matrix instructions (the
-// second one with ones for codes), and a lane has the scale and the zero of the one column
-// whose results it holds.
-//
-// 16 rows and 16 columns (of each matrix) to a workgroup.  Its waves take 128 contraction
-// steps in turn: 16 bytes of codes to a lane, which belong to four groups of 32 steps, and
-// the 32 steps' 4 chunks of x.  Their sums are joined through LDS in order.
-constexpr int kGqWaves = 4;
-
-template <typename D, typename O, int BLOCK, bool GLU>
-__global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
-  constexpr int BN = 16, LD = BN + 4, M = GLU ? 2 : 1, S = 128 / BLOCK;
-  __shared__ __attribute__((aligned(16))) float part[M][kGqWaves * 16 * LD];
-  GroupTile t;
-  int tn;
-  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
-  typedef typename D::V V;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
-  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
-  const int blocks = (a.k + 127) / 128;  // of 128 steps
-  const uint64_t wr = (uint64_t)t.g * a.n + n0 + min(lane & 15, left - 1);
-  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx + q * 8;
-  const V one = __builtin_bit_cast(V, ones(D()));
-  f32x4 acc[M];
-#pragma unroll
-  for (int m = 0; m < M; m++) acc[m] = f32x4{0, 0, 0, 0};
-  for (int b = wave; b < blocks; b += kGqWaves) {
-    i32x4 w[M], xv[4];
-    float s[M][S], z[M][S];
-#pragma unroll
-    for (int m = 0; m < M; m++) {
-      w[m] = reinterpret_cast<const i32x4*>(a.w[m].codes)[(wr * blocks + b) * 4 + q];
-#pragma unroll
-      for (int i = 0; i < S; i++) {
-        const uint64_t at = (wr * blocks + b) * S + i;
-        s[m][i] = scale_of(a.w[m].scales[at], a.half);
-        z[m][i] = a.w[m].zeros ? (float)a.w[m].zeros[at] : 8.f;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; u++) xv[u] = load_some(x + b * 128 + u * 32, a.k - b * 128 - u * 32 - q * 8);
-    f32x4 sum = {0, 0, 0, 0}, xsum = {0, 0, 0, 0}, sum2 = {0, 0, 0, 0};
-#pragma unroll
-    for (int u = 0; u < 4; u++) {
-      const V xu = __builtin_bit_cast(V, xv[u]);
-      sum = mfma(xu, __builtin_bit_cast(V, expand(w[0][u], D())), sum);
-      if (GLU) sum2 = mfma(xu, __builtin_bit_cast(V, expand(w[M - 1][u], D())), sum2);
-      xsum = mfma(xu, one, xsum);
-      if ((u + 1) * 32 % BLOCK == 0) {
-        const int i = u * 32 / BLOCK;
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          acc[0][e] += s[0][i] * (sum[e] - z[0][i] * xsum[e]);
-          if (GLU) acc[M - 1][e] += s[M - 1][i] * (sum2[e] - z[M - 1][i] * xsum[e]);
-        }
-        sum = sum2 = xsum = f32x4{0, 0, 0, 0};
-      }
-    }
-  }
-  // a lane: column lane % 16, rows lane / 16 * 4 + e
-#pragma unroll
-  for (int m = 0; m < M; m++)
-#pragma unroll
-    for (int e = 0; e < 4; e++) part[m][(wave * 16 + q * 4 + e) * LD + (lane & 15)] = acc[m][e];
-  __syncthreads();
-  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
-  if (threadIdx.x < 64) {
-    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
-    if (r >= rows || c >= left) return;
-    f32x4 v[M];
-#pragma unroll
-    for (int m = 0; m < M; m++) {
-      v[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < kGqWaves; i++) v[m] += *reinterpret_cast<const f32x4*>(part[m] + (i * 16 + r) * LD + c);
-    }
-    store4(out + (uint64_t)r * a.ldo, c, left, GLU ? gated(v[0], v[M - 1], a.act) : v[0]);
-  }
-}
-
-template <typename D, typename O, bool GLU, int BLOCK>
-hipError_t run_gq_mm(const GqMmArgs& a, hipStream_t s) {
-  dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 16) * ((a.n + 15) / 16), 256, &grid)) return e;
-  gq_mm_thin<D, O, BLOCK, GLU><<<grid, dim3(256), 0, s>>>(a);
-  return hipGetLastError();
-}
-template <typename D, typename O, bool GLU>
-hipError_t by_block(int block, const GqMmArgs& a, hipStream_t s) {
-  if (block == 32) return run_gq_mm<D, O, GLU, 32>(a, s);
-  if (block == 64) return run_gq_mm<D, O, GLU, 64>(a, s);
-  return run_gq_mm<D, O, GLU, 128>(a, s);
-}
-template <typename D, typename O>
-hipError_t by_form(bool glu, int block, const GqMmArgs& a, hipStream_t s) {
-  return glu ? by_block<D, O, true>(block, a, s) : by_block<D, O, false>(block, a, s);
-}
-
 template <typename I, int BLOCK>
 hipError_t run_quantize(int axis, const GqQuantArgs& a, hipStream_t s) {
   if (axis) {
@@ -409,13 +279,6 @@ hipError_t dequantize_by_block(int block, const GqDequantArgs& a, const RowPass&
 }
 
 }  // namespace
-
-hipError_t launch_gq_mm(int dtype, bool out_f32, bool glu, int block, const GqMmArgs& a, hipStream_t s) {
-  (void)hipGetLastError();
-  if (dtype == CIERA_BF16)
-    return out_f32 ? by_form<Bf16, float>(glu, block, a, s) : by_form<Bf16, __bf16>(glu, block, a, s);
-  return out_f32 ? by_form<Fp16, float>(glu, block, a, s) : by_form<Fp16, _Float16>(glu, block, a, s);
-}
 
 hipError_t launch_gq_quantize(int dtype, int axis, int block, const GqQuantArgs& a, hipStream_t s) {
   (void)hipGetLastError();

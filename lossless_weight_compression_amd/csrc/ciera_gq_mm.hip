@@ -1,0 +1,394 @@
+// Products of two-byte activations with 4-bit integer weights that have group scales.
+//
+// y[m, n] = sum over blocks b of s[n, b] (sum_k x[m, k] q[n, k] - z[n, b] sum_k x[m, k]):
+// codes are exact in two bytes, both sums over a block come from matrix instructions (the
+// second one with ones for codes), and are scaled in fp32: no weight is rounded.  x is the
+// instruction's first operand, so that a lane holds results of one column, whose scale and
+// zero it needs, for 4 rows.
+#include "ciera.h"
+#include "ciera_act.h"
+#include "ciera_gq.h"
+#include "ciera_mid.h"
+#include "ciera_ops_internal.h"
+#include "ciera_tiles.h"
+
+namespace ciera {
+namespace {
+
+// acc += s (sum - z xsum)
+__device__ __forceinline__ void add_block(f32x4& acc, f32x4 sum, f32x4 xsum, float s, float z) {
+#pragma unroll
+  for (int e = 0; e < 4; e++) acc[e] = __builtin_fmaf(s, __builtin_fmaf(-z, xsum[e], sum[e]), acc[e]);
+}
+
+// Keeps the order of what comes before, up to v, and of what uses v afterwards: the sums of
+// one block at a time take registers.
+template <typename V>
+__device__ __forceinline__ void in_order(V& v) {
+  asm volatile("" : "+v"(v));
+}
+
+// N bytes at any address.
+template <int N>
+struct __attribute__((packed, aligned(1))) Raw {
+  uint32_t v[N / 4];
+};
+template <>
+struct __attribute__((packed, aligned(1))) Raw<2> {
+  uint16_t v[1];
+};
+
+// N scales, or zeros, of a row.
+template <int N>
+struct Scales {
+  Raw<2 * N> s;
+  Raw<N> z;
+  __device__ __forceinline__ void load(const GqStack& w, uint64_t at) {
+    s = *reinterpret_cast<const Raw<2 * N>*>(w.scales + at);
+    if (w.zeros) {
+      z = *reinterpret_cast<const Raw<N>*>(w.zeros + at);
+    } else {
+#pragma unroll
+      for (auto& v : z.v) v = (decltype(v + 0))0x08080808u;
+    }
+  }
+  __device__ __forceinline__ float scale(int i, int half) const { return scale_of(s.v[i / 2] >> (i & 1 ? 16 : 0) & 0xffffu, half); }
+  __device__ __forceinline__ float zero(int i) const { return (float)((uint32_t)z.v[i / 4] >> 8 * (i & 3) & 255u); }
+};
+
+// ------------------------------------------------------------------ few rows to a group
+// What counts is how fast the codes are read, once for every 16 rows of a group.  A workgroup
+// takes 16 rows and NF * 16 columns (GLU: 16 of each matrix); its waves take 256 contraction steps in
+// turn, from memory into registers, the next ones' values under way while these are
+// multiplied: of every column 2 x 16 bytes of codes to a lane, which hold 4 words of 32 steps
+// each, and the scales of those steps in one load.  The waves' sums are joined through LDS in
+// order.
+constexpr int kGqWaves = 4;
+
+template <typename D, int BLOCK, bool GLU, int NF>
+__global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
+  constexpr int BN = 16 * NF, LD = BN + 4, M = GLU ? 2 : 1, F = M * NF, S = 256 / BLOCK;
+  __shared__ __attribute__((aligned(16))) float part[M][kGqWaves * 16 * LD];
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  typedef typename D::V V;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
+  const int blocks = (a.k + 127) / 128;  // of 128 steps
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx + q * 8;
+  uint64_t wb[NF];  // the lane's rows' first blocks
+#pragma unroll
+  for (int j = 0; j < NF; j++) wb[j] = ((uint64_t)t.g * a.n + n0 + min((lane & 15) + j * 16, left - 1)) * blocks;
+  struct Step {
+    i32x4 w[F][2], x[8];
+    Scales<S> s[F];
+  };
+  auto load = [&](Step& s, int b) {
+    if (b + 2 <= blocks) {
+#pragma unroll
+      for (int f = 0; f < F; f++) {
+        const i32x4* p = reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + (wb[f % NF] + b) * 4 + q;
+        s.w[f][0] = p[0];
+        s.w[f][1] = p[4];
+        s.s[f].load(a.w[f / NF], (wb[f % NF] + b) * (S / 2));
+      }
+    } else {
+      // one block is left: zeros behind it
+#pragma unroll
+      for (int f = 0; f < F; f++) {
+        const uint64_t at = wb[f % NF] + b;
+        s.w[f][0] = (reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + at * 4)[q];
+        s.w[f][1] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (auto& v : s.s[f].s.v) v = 0;
+#pragma unroll
+        for (auto& v : s.s[f].z.v) v = 0;
+#pragma unroll
+        for (int i = 0; i < S / 2; i++) {
+          s.s[f].s.v[i / 2] |= (uint32_t)a.w[f / NF].scales[at * (S / 2) + i] << (i & 1 ? 16 : 0);
+          s.s[f].z.v[i / 4] |= (a.w[f / NF].zeros ? (uint32_t)a.w[f / NF].zeros[at * (S / 2) + i] : 8u) << 8 * (i & 3);
+        }
+      }
+    }
+    if (b * 128 + 256 <= a.k) {
+#pragma unroll
+      for (int u = 0; u < 8; u++) s.x[u] = load16(x + b * 128 + u * 32);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; u++) s.x[u] = load_some(x + b * 128 + u * 32, a.k - b * 128 - u * 32 - q * 8);
+    }
+  };
+  const V one = ones(D());
+  f32x4 acc[F];
+#pragma unroll
+  for (int f = 0; f < F; f++) acc[f] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](const Step& s) {
+    f32x4 sum[F], xsum = {0, 0, 0, 0};
+#pragma unroll
+    for (int f = 0; f < F; f++) sum[f] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      V xu = __builtin_bit_cast(V, s.x[u]);
+      if (u * 32 % BLOCK == 0) in_order(xu);
+#pragma unroll
+      for (int f = 0; f < F; f++) sum[f] = mfma(xu, expand(s.w[f][u / 4][u % 4], D()), sum[f]);
+      xsum = mfma(xu, one, xsum);
+      if ((u + 1) * 32 % BLOCK == 0) {
+        const int i = u * 32 / BLOCK;
+#pragma unroll
+        for (int f = 0; f < F; f++) {
+          add_block(acc[f], sum[f], xsum, s.s[f].scale(i, a.half), s.s[f].zero(i));
+          in_order(acc[f]);
+          sum[f] = f32x4{0, 0, 0, 0};
+        }
+        xsum = f32x4{0, 0, 0, 0};
+      }
+    }
+  };
+  constexpr int STEP = 2 * kGqWaves;
+  int b = wave * 2;
+  Step s[2];
+  if (b < blocks) load(s[0], b);
+  while (b < blocks) {
+    if (b + STEP < blocks) load(s[1], b + STEP);
+    multiply(s[0]);
+    b += STEP;
+    if (b >= blocks) break;
+    if (b + STEP < blocks) load(s[0], b + STEP);
+    multiply(s[1]);
+    b += STEP;
+  }
+  // a lane: column lane % 16 of each 16, rows lane / 16 * 4 + e
+#pragma unroll
+  for (int f = 0; f < F; f++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) part[f / NF][(wave * 16 + q * 4 + e) * LD + f % NF * 16 + (lane & 15)] = acc[f][e];
+  __syncthreads();
+  const int r = threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
+  if (r >= min(rows, 16) || c >= left) return;
+  f32x4 v[M];
+#pragma unroll
+  for (int m = 0; m < M; m++) {
+    v[m] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kGqWaves; i++) v[m] += *reinterpret_cast<const f32x4*>(part[m] + (i * 16 + r) * LD + c);
+  }
+  if (GLU) v[0] = gated(v[0], v[M - 1], a.act);
+  const uint64_t at = (row + r) * a.ldo + n0;
+  if (a.out_f32) store4(static_cast<float*>(a.out) + at, c, left, v[0]);
+  else store4(static_cast<typename D::T*>(a.out) + at, c, left, v[0]);
+}
+
+// ------------------------------------------------------------------------ more rows
+// BM x 128 tiles (GLU: 64 columns of each matrix), 4 waves of BM / 2 x 64.  x goes through
+// LDS, 64 steps at a time, two stages; codes go from memory into the registers of the waves
+// that multiply them, since a code is 4 times smaller than what it expands to and two waves
+// share it at most.  A block's sums are kept apart from the tile's: as many registers again.
+template <typename D, int BLOCK, bool GLU, int BM>
+__global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
+  constexpr int WM = BM / 32, WN = 4, COLUMNS = GLU ? 64 : 128, S = 128 / BLOCK, LD = 68;
+  typedef StageTile<true, false, 16, BM> TA;
+  typedef StageLoad<true, BM> LA;
+  typedef typename D::V V;
+  __shared__ i32x4 lds[2 * TA::kChunks > 4 * 16 * LD / 4 ? 2 * TA::kChunks : 4 * 16 * LD / 4];  // or the results
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + COLUMNS - 1) / COLUMNS, blockIdx.x, &t, &tn)) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
+  const int n0 = tn * COLUMNS, left = a.n - n0, rows = t.count - t.m * BM;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
+  const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * (COLUMNS / 2), blocks = (a.k + 127) / 128;
+  LA ga;
+  ga.init(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, rows);
+  // fragment j: 16 columns of the matrix j / (WN / 2) (GLU) or the only one; the lane's
+  // row's first block, counted from that of column n0
+  uint32_t wb[WN];
+#pragma unroll
+  for (int j = 0; j < WN; j++) wb[j] = (uint32_t)min(c0 + (GLU ? j % 2 : j) * 16 + (lane & 15), left - 1) * (uint32_t)blocks;
+  const uint64_t first = ((uint64_t)t.g * a.n + n0) * blocks;
+  // of half a block: two words of every fragment, and its scales and zeros (BLOCK 128: with
+  // the second half)
+  constexpr int SH = S > 1 ? S / 2 : 1;
+  struct Codes {
+    Raw<8> w[WN];
+    Raw<2 * SH> s[WN];
+    uint32_t z[WN];
+  };
+  auto load_codes = [&](Codes& c, int b, auto h) {
+#pragma unroll
+    for (int j = 0; j < WN; j++) {
+      const GqStack& w = a.w[GLU ? j / 2 : 0];
+      const uint32_t at = wb[j] + b, sc = at * S + (S > 1 ? h.v * SH : 0);
+      c.w[j] = *reinterpret_cast<const Raw<8>*>(w.codes + first * 64 + (at * 64 + q * 16 + h.v * 8));
+      if (S == 1 && h.v == 0) continue;
+      c.s[j] = *reinterpret_cast<const Raw<2 * SH>*>(reinterpret_cast<const char*>(w.scales + first * S) + sc * 2);
+      c.z[j] = 0x0808u;
+      if (w.zeros) {
+        if constexpr (SH == 2) c.z[j] = reinterpret_cast<const Raw<2>*>(w.zeros + first * S + sc)->v[0];
+        else c.z[j] = *(w.zeros + first * S + sc);
+      }
+    }
+  };
+  i32x4 xr[LA::N];
+  auto load_x = [&](int stage) {
+    if (stage * 64 + 64 <= a.k) ga.load(xr, stage * 64);
+    else ga.load(xr, stage * 64, a.k);
+  };
+  auto put = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < LA::N; i++) lds[h * TA::kChunks + TA::pos(ga.line + i * (256 / TA::kPerRow), ga.col / 8)] = xr[i];
+  };
+  f32x4 acc[WM][WN];
+#pragma unroll
+  for (int i = 0; i < WM; i++)
+#pragma unroll
+    for (int j = 0; j < WN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+  const V one = ones(D());
+  f32x4 sum[WM][WN], xsum[WM];
+  auto clear = [&]() {
+#pragma unroll
+    for (int i = 0; i < WM; i++) {
+      xsum[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < WN; j++) sum[i][j] = f32x4{0, 0, 0, 0};
+    }
+  };
+  clear();
+  // half h of a block of 128 steps, from half h of LDS
+  auto multiply = [&](const Codes& c, auto h) {
+    const uint32_t pa = TA::place(lds + h.v * TA::kChunks, r0);
+    each<2>([&](auto part) {
+      constexpr int U = h.v * 2 + part.v;
+      V fx[WM];
+      each<WM>([&](auto i) {
+        fx[i.v] = __builtin_bit_cast(V, TA::template fragment<i.v, part.v>(pa));
+        in_order(fx[i.v]);
+      });
+#pragma unroll
+      for (int i = 0; i < WM; i++) xsum[i] = mfma(fx[i], one, xsum[i]);
+#pragma unroll
+      for (int j = 0; j < WN; j++) {
+        V fw = expand(c.w[j].v[part.v], D());
+        in_order(fw);
+#pragma unroll
+        for (int i = 0; i < WM; i++) sum[i][j] = mfma(fx[i], fw, sum[i][j]);
+      }
+      if constexpr ((U + 1) * 32 % BLOCK == 0) {
+        constexpr int B = SH == 2 ? part.v : 0;
+#pragma unroll
+        for (int j = 0; j < WN; j++) {
+          const float sc = scale_of(B ? c.s[j].v[0] >> 16 : c.s[j].v[0] & 0xffffu, a.half);
+          const float ze = (float)(c.z[j] >> 8 * B & 255u);
+#pragma unroll
+          for (int i = 0; i < WM; i++) {
+            add_block(acc[i][j], sum[i][j], xsum[i], sc, ze);
+            in_order(acc[i][j]);
+          }
+        }
+        clear();
+      }
+    });
+  };
+  Codes c[2];
+  if (blocks > 0) {
+    load_x(0);
+    load_codes(c[0], 0, Int<0>());
+    put(0);
+  }
+  __syncthreads();
+  // the codes of a block's first half are here, as is its x
+  for (int b = 0; b < blocks; b++) {
+    load_x(2 * b + 1);
+    load_codes(c[1], b, Int<1>());
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(c[0], Int<0>());
+    put(1);
+    __syncthreads();
+    if (b + 1 < blocks) {
+      load_x(2 * b + 2);
+      load_codes(c[0], b + 1, Int<0>());
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(c[1], Int<1>());
+    if (b + 1 < blocks) put(0);
+    __syncthreads();
+  }
+  // a lane: column lane % 16 of each fragment, rows lane / 16 * 4 + e; turned around in LDS,
+  // 16 rows at a time, to 16 (GLU: 8) consecutive columns of a row
+  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * LD;
+#pragma unroll
+  for (int i = 0; i < WM; i++) {
+    constexpr int N = GLU ? 2 : 4;
+#pragma unroll
+    for (int j = 0; j < N; j++) {
+      const f32x4 v = GLU ? gated(acc[i][j], acc[i][(j + 2) % WN], a.act) : acc[i][j];
+#pragma unroll
+      for (int e = 0; e < 4; e++) turn[(q * 4 + e) * LD + j * 16 + (lane & 15)] = v[e];
+    }
+    wave_order();
+    const int r = r0 + i * 16 + (lane >> 2), c = (lane & 3) * 4 * N;
+#pragma unroll
+    for (int h = 0; h < N / 2; h++) {
+      const f32x4 lo = *reinterpret_cast<const f32x4*>(turn + (lane >> 2) * LD + c + h * 8);
+      const f32x4 hi = *reinterpret_cast<const f32x4*>(turn + (lane >> 2) * LD + c + h * 8 + 4);
+      const uint64_t at = (row + r) * a.ldo + n0 + c0 + c + h * 8;
+      const int more = left - c0 - c - h * 8;
+      if (r < rows) {
+        if (a.out_f32) store_row8(static_cast<float*>(a.out) + at, more, lo, hi);
+        else store_row8(static_cast<typename D::T*>(a.out) + at, more, lo, hi);
+      }
+    }
+    wave_order();
+  }
+}
+
+template <typename D, int BLOCK, bool GLU, int NF>
+hipError_t run_thin(uint64_t row_tiles, const GqMmArgs& a, hipStream_t s) {
+  dim3 grid;
+  if (hipError_t e = tile_grid(row_tiles * ((a.n + 16 * NF - 1) / (16 * NF)), 256, &grid)) return e;
+  gq_mm_thin<D, BLOCK, GLU, NF><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename D, int BLOCK, bool GLU, int BM>
+hipError_t run_mid(const GqMmArgs& a, hipStream_t s) {
+  constexpr int COLUMNS = GLU ? 64 : 128;
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + COLUMNS - 1) / COLUMNS), 256, &grid)) return e;
+  gq_mm_mid<D, BLOCK, GLU, BM><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename D, int BLOCK, bool GLU>
+hipError_t run_gq_mm(const GqMmArgs& a, hipStream_t s) {
+  const int64_t rows = a.rows, groups = a.groups;
+  const uint64_t thin = max_row_tiles(rows, groups, 16);
+  // (the tiles count blocks of 128 rows in 32 bits)
+  if (rows <= 16 * groups || a.k > 1 << 25) {
+    if constexpr (!GLU)
+      if (thin * ((a.n + 31) / 32) >= 4 * kUnits) return run_thin<D, BLOCK, GLU, 2>(thin, a, s);
+    return run_thin<D, BLOCK, GLU, 1>(thin, a, s);
+  }
+  if (rows <= 96 * groups) return run_mid<D, BLOCK, GLU, 64>(a, s);
+  return run_mid<D, BLOCK, GLU, 128>(a, s);
+}
+template <typename D, bool GLU>
+hipError_t by_block(int block, const GqMmArgs& a, hipStream_t s) {
+  if (block == 32) return run_gq_mm<D, 32, GLU>(a, s);
+  if (block == 64) return run_gq_mm<D, 64, GLU>(a, s);
+  return run_gq_mm<D, 128, GLU>(a, s);
+}
+template <typename D>
+hipError_t by_form(bool glu, int block, const GqMmArgs& a, hipStream_t s) {
+  return glu ? by_block<D, true>(block, a, s) : by_block<D, false>(block, a, s);
+}
+
+}  // namespace
+
+hipError_t launch_gq_mm(int dtype, bool glu, int block, const GqMmArgs& a, hipStream_t s) {
+  (void)hipGetLastError();
+  return dtype == CIERA_BF16 ? by_form<Bf16>(glu, block, a, s) : by_form<Fp16>(glu, block, a, s);
+}
+
+}  // namespace ciera

@@ -16,10 +16,12 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 struct Bf16 {
+  typedef __bf16 T;
   typedef bf16x8 V;
   static constexpr bool kScaled = false;
 };
 struct Fp16 {
+  typedef _Float16 T;
   typedef f16x8 V;
   static constexpr bool kScaled = false;
 };
