@@ -57,6 +57,14 @@ struct GluOut {
       store_row8(up + (uint64_t)r * ldou + c, left, ulo, uhi);
     }
   }
+  // of 4 columns; `cols` columns are left from column 0
+  __device__ __forceinline__ void put4(int r, int c, int cols, f32x4 g, f32x4 u) const {
+    store4(out + (uint64_t)r * ldo, c, cols, gated(g, u, act));
+    if (gate) {
+      store4(gate + (uint64_t)r * ldog, c, cols, g);
+      store4(up + (uint64_t)r * ldou, c, cols, u);
+    }
+  }
 };
 
 // dG = D U act'(G) and dU = D act(G), G and U from memory.

@@ -5,6 +5,7 @@
 #include "ciera_big.h"
 #include "ciera_mid.h"
 #include "ciera_ops_internal.h"
+#include "ciera_thin.h"
 #include "ciera_tiles.h"
 
 namespace ciera {

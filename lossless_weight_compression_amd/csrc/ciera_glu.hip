@@ -37,12 +37,40 @@ __global__ __launch_bounds__(512) void glu_mm_big(GluMmArgs a) {
   });
 }
 
+// Few rows to a group: 16 rows, and 16 * VEC columns ([N, K]: 16) of both products.
+template <typename D, bool TRANS, typename O, int VEC>
+__global__ __launch_bounds__(512) void glu_mm_thin(GluMmArgs a) {
+  typedef typename ThinOf<D, TRANS, VEC, 2>::T Thin;
+  constexpr int BN = Thin::BN;
+  __shared__ ThinPart<BN, 2> part;
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
+  Thin thin;
+  thin.run(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, rows, left, a.k,
+           {weights<TRANS>(a.wg, t.g, a.gsg, a.ldg, n0), weights<TRANS>(a.wu, t.g, a.gsu, a.ldu, n0)}, {a.ldg, a.ldu});
+  thin.put(part);
+  const GluOut<O> all = {static_cast<O*>(a.out), static_cast<O*>(a.gate), static_cast<O*>(a.up), a.ldo, a.ldog, a.ldou, a.act};
+  const GluOut<O> out = all.at(row, n0);
+  part.join(rows, left, [&](int m, int c, const f32x4* v) { out.put4(m, c, left, v[0], v[1]); });
+}
+
 template <typename D, bool TRANS, typename O>
 hipError_t run_glu_mm(bool flat, const GluMmArgs& a, hipStream_t s) {
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 128) && short_stride(a.ldx) && short_stride(a.ldg) &&
       short_stride(a.ldu)) {
     if (a.gate) glu_mm_big<D, TRANS, O, true><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     else glu_mm_big<D, TRANS, O, false><<<dim3(kUnits), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const uint64_t thin = max_row_tiles(a.rows, a.groups, 16);
+  if (a.rows <= 16 * (int64_t)a.groups) {
+    constexpr int VEC = 4, BN = TRANS ? 16 : 16 * VEC;
+    dim3 grid;
+    if (hipError_t e = tile_grid(thin * ((a.n + BN - 1) / BN), 512, &grid)) return e;
+    glu_mm_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
   dim3 grid;

@@ -34,11 +34,40 @@ __global__ __launch_bounds__(512) void glu_grad_big(GluGradArgs a) {
   });
 }
 
+// Few rows to a group.
+template <typename D, bool TRANS, typename O, int VEC>
+__global__ __launch_bounds__(512) void glu_grad_thin(GluGradArgs a) {
+  typedef typename ThinOf<D, TRANS, VEC, 1>::T Thin;
+  constexpr int BN = Thin::BN;
+  __shared__ ThinPart<BN, 1> part;
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
+  Thin thin;
+  thin.run(static_cast<const uint16_t*>(a.dy) + row * a.ldx, a.ldx, rows, left, a.k,
+           {weights<TRANS>(a.w, t.g, a.gsw, a.ldw, n0)}, {a.ldw});
+  thin.put(part);
+  const GradOut<O> all = {static_cast<const O*>(a.gate), static_cast<const O*>(a.up), static_cast<O*>(a.dgate),
+                          static_cast<O*>(a.dup), a.ldg, a.ldu, a.lddg, a.lddu, a.act};
+  const GradOut<O> out = all.at(row, n0);
+  part.join(rows, left, [&](int m, int c, const f32x4* v) { out.put(m, c, min(left - c, 4), v[0], f32x4{0, 0, 0, 0}); });
+}
+
 template <typename D, bool TRANS, typename O>
 hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 256) && short_stride(a.ldx) && short_stride(a.ldw) &&
       short_stride(a.ldg) && short_stride(a.ldu) && short_stride(a.lddg) && short_stride(a.lddu)) {
     glu_grad_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const uint64_t thin = max_row_tiles(a.rows, a.groups, 16);
+  if (a.rows <= 16 * (int64_t)a.groups) {
+    constexpr int VEC = 4, BN = TRANS ? 16 : 16 * VEC;
+    dim3 grid;
+    if (hipError_t e = tile_grid(thin * ((a.n + BN - 1) / BN), 512, &grid)) return e;
+    glu_grad_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
   dim3 grid;

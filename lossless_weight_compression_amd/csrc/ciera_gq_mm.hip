@@ -62,19 +62,22 @@ struct Scales {
 // turn, from memory into registers, the next ones' values under way while these are
 // multiplied: of every column 2 x 16 bytes of codes to a lane, which hold 4 words of 32 steps
 // each, and the scales of those steps in one load.  The waves' sums are joined through LDS in
-// order.
+// order.  SIDE: each wave has all of the steps, and columns of its own: fewer and longer
+// workgroups where there are enough of them.
 constexpr int kGqWaves = 4;
 
-template <typename D, int BLOCK, bool GLU, int NF>
+template <typename D, int BLOCK, bool GLU, int NF, bool SIDE>
 __global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
   constexpr int BN = 16 * NF, LD = BN + 4, M = GLU ? 2 : 1, F = M * NF, S = 256 / BLOCK;
+  constexpr int WIDE = SIDE ? kGqWaves * BN : BN;  // columns of a workgroup
   __shared__ __attribute__((aligned(16))) float part[M][kGqWaves * 16 * LD];
   GroupTile t;
   int tn;
-  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + WIDE - 1) / WIDE, blockIdx.x, &t, &tn)) return;
   typedef typename D::V V;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
+  const int n0 = tn * WIDE + (SIDE ? wave * BN : 0), left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
+  if (SIDE && left <= 0) return;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
   const int blocks = (a.k + 127) / 128;  // of 128 steps
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx + q * 8;
@@ -147,8 +150,8 @@ __global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
       }
     }
   };
-  constexpr int STEP = 2 * kGqWaves;
-  int b = wave * 2;
+  constexpr int STEP = SIDE ? 2 : 2 * kGqWaves;
+  int b = SIDE ? 0 : wave * 2;
   Step s[2];
   if (b < blocks) load(s[0], b);
   while (b < blocks) {
@@ -165,20 +168,25 @@ __global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
   for (int f = 0; f < F; f++)
 #pragma unroll
     for (int e = 0; e < 4; e++) part[f / NF][(wave * 16 + q * 4 + e) * LD + f % NF * 16 + (lane & 15)] = acc[f][e];
-  __syncthreads();
-  const int r = threadIdx.x / (BN / 4), c = threadIdx.x % (BN / 4) * 4;
-  if (r >= min(rows, 16) || c >= left) return;
+  if (SIDE) wave_order();
+  else __syncthreads();
+  for (int p = SIDE ? lane : threadIdx.x; p < 4 * BN; p += SIDE ? 64 : 256) {
+  const int r = p / (BN / 4), c = p % (BN / 4) * 4;
+  if (r >= rows || c >= left) continue;
   f32x4 v[M];
 #pragma unroll
   for (int m = 0; m < M; m++) {
     v[m] = f32x4{0, 0, 0, 0};
+    if (SIDE) v[m] = *reinterpret_cast<const f32x4*>(part[m] + (wave * 16 + r) * LD + c);
+    else
 #pragma unroll
-    for (int i = 0; i < kGqWaves; i++) v[m] += *reinterpret_cast<const f32x4*>(part[m] + (i * 16 + r) * LD + c);
+      for (int i = 0; i < kGqWaves; i++) v[m] += *reinterpret_cast<const f32x4*>(part[m] + (i * 16 + r) * LD + c);
   }
   if (GLU) v[0] = gated(v[0], v[M - 1], a.act);
   const uint64_t at = (row + r) * a.ldo + n0;
   if (a.out_f32) store4(static_cast<float*>(a.out) + at, c, left, v[0]);
   else store4(static_cast<typename D::T*>(a.out) + at, c, left, v[0]);
+  }
 }
 
 // ------------------------------------------------------------------------ more rows
@@ -344,11 +352,12 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
   }
 }
 
-template <typename D, int BLOCK, bool GLU, int NF>
+template <typename D, int BLOCK, bool GLU, int NF, bool SIDE>
 hipError_t run_thin(uint64_t row_tiles, const GqMmArgs& a, hipStream_t s) {
+  constexpr int WIDE = 16 * NF * (SIDE ? kGqWaves : 1);
   dim3 grid;
-  if (hipError_t e = tile_grid(row_tiles * ((a.n + 16 * NF - 1) / (16 * NF)), 256, &grid)) return e;
-  gq_mm_thin<D, BLOCK, GLU, NF><<<grid, dim3(256), 0, s>>>(a);
+  if (hipError_t e = tile_grid(row_tiles * ((a.n + WIDE - 1) / WIDE), 256, &grid)) return e;
+  gq_mm_thin<D, BLOCK, GLU, NF, SIDE><<<grid, dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename D, int BLOCK, bool GLU, int BM>
@@ -366,9 +375,9 @@ hipError_t run_gq_mm(const GqMmArgs& a, hipStream_t s) {
   const uint64_t thin = max_row_tiles(rows, groups, 16);
   // (the tiles count blocks of 128 rows in 32 bits)
   if (rows <= 16 * groups || a.k > 1 << 25) {
-    if constexpr (!GLU)
-      if (thin * ((a.n + 31) / 32) >= 4 * kUnits) return run_thin<D, BLOCK, GLU, 2>(thin, a, s);
-    return run_thin<D, BLOCK, GLU, 1>(thin, a, s);
+    constexpr int NF = GLU ? 1 : 2;
+    if (thin * ((a.n + 64 * NF - 1) / (64 * NF)) >= 8 * kUnits) return run_thin<D, BLOCK, GLU, NF, true>(thin, a, s);
+    return run_thin<D, BLOCK, GLU, 1, false>(thin, a, s);
   }
   if (rows <= 96 * groups) return run_mid<D, BLOCK, GLU, 64>(a, s);
   return run_mid<D, BLOCK, GLU, 128>(a, s);

@@ -4,6 +4,7 @@
 #include "ciera_big.h"
 #include "ciera_mid.h"
 #include "ciera_ops_internal.h"
+#include "ciera_thin.h"
 #include "ciera_tiles.h"
 
 namespace ciera {
@@ -241,181 +242,40 @@ __global__ __launch_bounds__(512) void group_wgrad_big(GroupWgradArgs a) {
 }
 
 // ------------------------------------------------------- few rows to a group
-// What counts then is how fast the weights are read, once for every 16 rows of a group
-// (64 tokens over 8 of 256 experts each, 7168 x 2048, [K, N]: 959 us, 6.0 TB/s).  A
-// workgroup takes 16 rows of a group and some columns; its 8 waves take the contraction steps in turn, so
-// that all of them read at once, from memory into registers, the next step's values
-// under way while this one's are multiplied; their sums are joined through LDS in the
-// order of the waves.
-constexpr int kThinWaves = 8;
-
-// The joined sums: cols columns of 16 rows, of which `rows` are stored.  part: each
-// wave's [16][kLd] floats.
-template <typename O, int COLS>
-struct ThinJoin {
-  static constexpr int kLd = COLS + 4;
-  static __device__ __forceinline__ void store(const float* part, O* out, uint64_t ldo, int rows, int cols) {
-    for (int p = threadIdx.x; p < 16 * COLS / 4; p += kThinWaves * 64) {
-      const int m = p / (COLS / 4), c = p % (COLS / 4) * 4;
-      if (m >= rows || c >= cols) continue;
-      f32x4 v = {0, 0, 0, 0};
-#pragma unroll
-      for (int w = 0; w < kThinWaves; w++) v += *reinterpret_cast<const f32x4*>(part + (w * 16 + m) * kLd + c);
-      store4(out + (uint64_t)m * ldo, c, cols, v);
-    }
-  }
-};
-
-// W [K, N]: a lane holds 8 contraction steps of VEC columns (two-byte values, 2 * VEC
-// bytes of 8 rows) and turns them around in registers; 16 lanes cover 16 * VEC columns.
+// W [K, N]
 template <typename D, typename O, int VEC>
 __global__ __launch_bounds__(512) void group_mm_thin(GroupMmArgs a) {
-  constexpr int BN = 16 * VEC, W = VEC / 2;  // words of a row's columns in a lane
-  typedef ThinJoin<O, BN> Join;
-  __shared__ __attribute__((aligned(16))) float part[kThinWaves * 16 * Join::kLd];
+  constexpr int BN = 16 * VEC;
+  __shared__ ThinPart<BN, 1> part;
   GroupTile t;
   int tn;
   if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
-  const int c = (lane & 15) * VEC, q = lane >> 4;
-  const uint16_t* w = static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + n0 + c;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx;
-
-  struct Step {
-    uint32_t w[8][W];
-    i32x4 x;
-  };
-  auto load = [&](Step& s, int k0) {
-    const int k = k0 + q * 8;
-    if (k0 + 32 <= a.k && left >= BN) {
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const uint16_t* p = w + (uint64_t)(k + j) * a.ldw;
-        if constexpr (VEC == 8) {
-          const i32x4 v = load16(p);
-#pragma unroll
-          for (int i = 0; i < 4; i++) s.w[j][i] = v[i];
-        } else {
-          const Pack<uint32_t, 2> v = *reinterpret_cast<const Pack<uint32_t, 2>*>(p);
-          s.w[j][0] = v.v[0];
-          s.w[j][1] = v.v[1];
-        }
-      }
-      s.x = load16(x + k);
-    } else {
-      // All at once: outside the matrix its last row or column again, then zeros (100 rows
-      // over 13 groups, 2048 x 1000: 21.1 us, 40.8 with a branch to each value).
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const uint16_t* p = w + (uint64_t)min(k + j, a.k - 1) * a.ldw - c;
-#pragma unroll
-        for (int i = 0; i < W; i++) {
-          const uint32_t lo = p[min(c + 2 * i, left - 1)], hi = p[min(c + 2 * i + 1, left - 1)];
-          s.w[j][i] = (k + j < a.k && c + 2 * i < left ? lo : 0) | (k + j < a.k && c + 2 * i + 1 < left ? hi << 16 : 0);
-        }
-      }
-      s.x = load_some(x + k, a.k - k);
-    }
-  };
-  f32x4 acc[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; j++) acc[j] = f32x4{0, 0, 0, 0};
-  auto multiply = [&](const Step& s) {
-#pragma unroll
-    for (int j = 0; j < VEC; j++) {
-      i32x4 v;
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        v[i] = __builtin_amdgcn_perm(s.w[2 * i + 1][j / 2], s.w[2 * i][j / 2], j & 1 ? 0x07060302u : 0x05040100u);
-      acc[j] = mfma(__builtin_bit_cast(typename D::V, v), __builtin_bit_cast(typename D::V, s.x), acc[j]);
-    }
-  };
-  constexpr int STEP = 32 * kThinWaves;
-  int k0 = wave * 32;
-  Step s[2];
-  if (k0 < a.k) load(s[0], k0);
-  while (k0 < a.k) {
-    if (k0 + STEP < a.k) load(s[1], k0 + STEP);
-    multiply(s[0]);
-    k0 += STEP;
-    if (k0 >= a.k) break;
-    if (k0 + STEP < a.k) load(s[0], k0 + STEP);
-    multiply(s[1]);
-    k0 += STEP;
-  }
-  // results of a lane: row lane % 16, columns (lane / 16 * 4 + i) * VEC + j
-  float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4 * VEC;
-#pragma unroll
-  for (int i = 0; i < 4; i++)
-#pragma unroll
-    for (int j = 0; j < VEC; j += 4)
-      *reinterpret_cast<f32x4*>(mine + i * VEC + j) = f32x4{acc[j][i], acc[j + 1][i], acc[j + 2][i], acc[j + 3][i]};
-  __syncthreads();
-  Join::store(part, static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, rows, left);
+  ThinN<D, VEC, 1> thin;
+  thin.run(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, rows, left, a.k,
+           {static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + n0}, {a.ldw});
+  thin.put(part);
+  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
+  part.join(rows, left, [&](int m, int c, const f32x4* v) { store4(out + (uint64_t)m * a.ldo, c, left, v[0]); });
 }
 
-// W [N, K]: a lane reads 64 bytes of one of 16 rows of W (4 loads, so that 4 lanes cover 256
-// bytes of a row).
+// W [N, K]
 template <typename D, typename O>
 __global__ __launch_bounds__(512) void group_mm_thin_t(GroupMmArgs a) {
   constexpr int BN = 16;
-  typedef ThinJoin<O, BN> Join;
-  __shared__ __attribute__((aligned(16))) float part[kThinWaves * 16 * Join::kLd];
+  __shared__ ThinPart<BN, 1> part;
   GroupTile t;
   int tn;
   if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
-  const int q = lane >> 4;
-  const uint16_t* w =
-      static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (uint64_t)(n0 + min(lane & 15, left - 1)) * a.ldw;
-  const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx;
-  struct Step {
-    i32x4 w[4], x[4];
-  };
-  auto load = [&](Step& s, int k0) {
-    const int k = k0 + q * 32;
-    if (k0 + 128 <= a.k) {
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        s.w[u] = load16(w + k + u * 8);
-        s.x[u] = load16(x + k + u * 8);
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; u++) {
-        s.w[u] = load_some(w + k + u * 8, a.k - k - u * 8);
-        s.x[u] = load_some(x + k + u * 8, a.k - k - u * 8);
-      }
-    }
-  };
-  f32x4 acc = {0, 0, 0, 0};
-  auto multiply = [&](const Step& s) {
-#pragma unroll
-    for (int u = 0; u < 4; u++)
-      acc = mfma(__builtin_bit_cast(typename D::V, s.w[u]), __builtin_bit_cast(typename D::V, s.x[u]), acc);
-  };
-  constexpr int STEP = 128 * kThinWaves;
-  int k0 = wave * 128;
-  Step s[2];
-  if (k0 < a.k) load(s[0], k0);
-  while (k0 < a.k) {
-    if (k0 + STEP < a.k) load(s[1], k0 + STEP);
-    multiply(s[0]);
-    k0 += STEP;
-    if (k0 >= a.k) break;
-    if (k0 + STEP < a.k) load(s[0], k0 + STEP);
-    multiply(s[1]);
-    k0 += STEP;
-  }
-  // results of a lane: row lane % 16, columns lane / 16 * 4 + i
-  float* mine = part + (wave * 16 + (lane & 15)) * Join::kLd + (lane >> 4) * 4;
-  *reinterpret_cast<f32x4*>(mine) = acc;
-  __syncthreads();
-  Join::store(part, static_cast<O*>(a.out) + row * a.ldo + n0, a.ldo, rows, left);
+  ThinT<D, 1> thin;
+  thin.run(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, rows, left, a.k,
+           {static_cast<const uint16_t*>(a.w) + (uint64_t)t.g * a.gsw + (uint64_t)n0 * a.ldw}, {a.ldw});
+  thin.put(part);
+  O* out = static_cast<O*>(a.out) + row * a.ldo + n0;
+  part.join(rows, left, [&](int m, int c, const f32x4* v) { store4(out + (uint64_t)m * a.ldo, c, left, v[0]); });
 }
 
 // Narrow columns to a workgroup where wide ones would not make enough workgroups for the

@@ -159,20 +159,61 @@ __device__ __forceinline__ void die_run(uint64_t all, uint32_t x, uint64_t* firs
 }
 
 // Row tile and column tile of workgroup `bid`, one tile each; false: beyond the
-// last tile (the grid covers the largest possible number).
+// last tile (the grid covers the largest possible number).  Four times 64 groups at a time,
+// whose offsets are loaded at once and, up to 256 groups, once: what a workgroup with little
+// work waits for first.
 template <int BM>
 __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, int rows, int ntiles, uint32_t bid,
                                                 GroupTile* t, int* n) {
-  GroupTiles<BM> tiles;
-  tiles.init(off, groups, rows);
+  int begin[4], count[4], incl[4];
+  uint32_t sums[4];
+  auto four = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int g = c + i * 64 + (threadIdx.x & 63);
+      begin[i] = count[i] = 0;
+      if (g < groups) group_range(off, g, rows, &begin[i], &count[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      sums[i] = incl[i] = 0;
+      if (c + i * 64 >= groups) continue;
+      incl[i] = wave_inclusive_sum((count[i] + BM - 1) / BM);
+      sums[i] = (uint32_t)__builtin_amdgcn_readlane(incl[i], 63);
+    }
+    return sums[0] + sums[1] + sums[2] + sums[3];
+  };
+  uint32_t total = 0;
+  for (int c = 0; c < groups; c += 256) total += four(c);
   uint64_t first;
-  uint32_t count;
-  die_run((uint64_t)tiles.total * ntiles, bid % kXcds, &first, &count);
-  if (bid / kXcds >= count) return false;
+  uint32_t many;
+  die_run((uint64_t)total * ntiles, bid % kXcds, &first, &many);
+  if (bid / kXcds >= many) return false;
   const uint64_t tile = first + bid / kXcds;
-  *t = tiles.find((uint32_t)(tile / ntiles));
+  const uint32_t mt = (uint32_t)(tile / ntiles);
   *n = (int)(tile % ntiles);
-  return true;
+  uint32_t before = 0;
+  int c = 0;
+  if (groups > 256) {
+    for (;; c += 256) {
+      const uint32_t all = four(c);
+      if (before + all > mt || c + 256 >= groups) break;
+      before += all;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (mt < before + sums[i]) {
+      const int l = __builtin_ctzll(__ballot(before + (uint32_t)incl[i] > mt));
+      t->g = c + i * 64 + l;
+      t->begin = __builtin_amdgcn_readlane(begin[i], l);
+      t->count = __builtin_amdgcn_readlane(count[i], l);
+      t->m = (int)(mt - before) - (__builtin_amdgcn_readlane(incl[i], l) - (t->count + BM - 1) / BM);
+      return true;
+    }
+    before += sums[i];
+  }
+  return false;
 }
 
 // v, as if computed anew here: what depends on it is not kept in registers across the
