@@ -11,8 +11,11 @@
 namespace ciera {
 namespace {
 
-__device__ __forceinline__ float scale_of(uint32_t bits, int half) {
-  return half ? (float)__builtin_bit_cast(_Float16, (uint16_t)bits) : __builtin_bit_cast(float, bits << 16);
+// A scale's value: fp16, or bf16 in the lower half of a word.  half: all ones or zero.  (A
+// branch on the type would end the counting of loads under way.)
+__device__ __forceinline__ float scale_of(uint32_t bits, uint32_t half) {
+  const uint32_t h = __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)bits));
+  return __builtin_bit_cast(float, (h & half) | (bits << 16 & ~half));
 }
 
 // 8 codes as two-byte floats, in order.

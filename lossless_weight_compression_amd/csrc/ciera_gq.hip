@@ -14,7 +14,7 @@ namespace ciera {
 namespace {
 
 // s rounded to the scales' type, its bits; a scale below 2^-126 becomes 0.
-__device__ __forceinline__ uint32_t scale_bits(float s, int half) {
+__device__ __forceinline__ uint32_t scale_bits(float s, uint32_t half) {
   if (half) return __builtin_bit_cast(uint16_t, (_Float16)s);
   const uint32_t b = __builtin_bit_cast(uint16_t, (__bf16)s);
   return b < 0x80u ? 0u : b;
@@ -33,7 +33,7 @@ struct BlockScale {
   bool bad;
   // of a block with the smallest and the largest value, or (symmetric) the largest magnitude
   // in hi; not finite where one of its values is not
-  __device__ __forceinline__ BlockScale(float lo, float hi, bool zeros, int half) {
+  __device__ __forceinline__ BlockScale(float lo, float hi, bool zeros, uint32_t half) {
     const float range = zeros ? (hi - lo) / 15.f : hi / 7.f;
     bits = scale_bits(range, half);
     s = scale_of(bits, half);

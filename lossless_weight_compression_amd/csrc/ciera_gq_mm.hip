@@ -38,111 +38,126 @@ struct __attribute__((packed, aligned(1))) Raw<2> {
   uint16_t v[1];
 };
 
-// N scales, or zeros, of a row.
+// The zeros of a stack, from memory where it has some: else the scales' bytes are read in
+// their place (a branch would end the counting of loads under way), and 8 taken.
+struct Zeros {
+  const uint8_t* p;
+  uint32_t kept;  // all ones: zeros come from memory
+  __device__ __forceinline__ Zeros(const GqStack& w)
+      : p(w.zeros ? w.zeros : reinterpret_cast<const uint8_t*>(w.scales)), kept(w.zeros ? ~0u : 0u) {}
+  __device__ __forceinline__ float value(uint32_t word, int i) const {
+    return (float)(((word & kept) | (0x08080808u & ~kept)) >> 8 * i & 255u);
+  }
+};
+
+// N scales and zeros of a row.
 template <int N>
 struct Scales {
   Raw<2 * N> s;
   Raw<N> z;
-  __device__ __forceinline__ void load(const GqStack& w, uint64_t at) {
+  __device__ __forceinline__ void load(const GqStack& w, const Zeros& zeros, uint64_t at) {
     s = *reinterpret_cast<const Raw<2 * N>*>(w.scales + at);
-    if (w.zeros) {
-      z = *reinterpret_cast<const Raw<N>*>(w.zeros + at);
-    } else {
-#pragma unroll
-      for (auto& v : z.v) v = (decltype(v + 0))0x08080808u;
-    }
+    z = *reinterpret_cast<const Raw<N>*>(zeros.p + at);
   }
-  __device__ __forceinline__ float scale(int i, int half) const { return scale_of(s.v[i / 2] >> (i & 1 ? 16 : 0) & 0xffffu, half); }
-  __device__ __forceinline__ float zero(int i) const { return (float)((uint32_t)z.v[i / 4] >> 8 * (i & 3) & 255u); }
+  // not taken apart before this
+  __device__ __forceinline__ void wait() {
+#pragma unroll
+    for (auto& v : s.v) in_order(v);
+#pragma unroll
+    for (auto& v : z.v) in_order(v);
+  }
+  __device__ __forceinline__ float scale(int i, uint32_t half) const {
+    return scale_of(s.v[i / 2] >> (i & 1 ? 16 : 0) & 0xffffu, half);
+  }
+  __device__ __forceinline__ float zero(const Zeros& zeros, int i) const { return zeros.value(z.v[i / 4], i & 3); }
 };
 
 // ------------------------------------------------------------------ few rows to a group
 // What counts is how fast the codes are read, once for every 16 rows of a group.  A workgroup
-// takes 16 rows and NF * 16 columns (GLU: 16 of each matrix); its waves take 256 contraction steps in
+// takes 16 rows and 16 columns (GLU: of each matrix); its waves take 256 contraction steps in
 // turn, from memory into registers, the next ones' values under way while these are
 // multiplied: of every column 2 x 16 bytes of codes to a lane, which hold 4 words of 32 steps
 // each, and the scales of those steps in one load.  The waves' sums are joined through LDS in
-// order.  SIDE: each wave has all of the steps, and columns of its own: fewer and longer
-// workgroups where there are enough of them.
+// order.
 constexpr int kGqWaves = 4;
 
-template <typename D, int BLOCK, bool GLU, int NF, bool SIDE>
-__global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
-  constexpr int BN = 16 * NF, LD = BN + 4, M = GLU ? 2 : 1, F = M * NF, S = 256 / BLOCK;
-  constexpr int WIDE = SIDE ? kGqWaves * BN : BN;  // columns of a workgroup
+template <typename D, int BLOCK, bool GLU>
+__global__ __launch_bounds__(64 * kGqWaves) void gq_mm_thin(GqMmArgs a) {
+  constexpr int BN = 16, LD = BN + 4, M = GLU ? 2 : 1, S = 256 / BLOCK;
   __shared__ __attribute__((aligned(16))) float part[M][kGqWaves * 16 * LD];
   GroupTile t;
   int tn;
-  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + WIDE - 1) / WIDE, blockIdx.x, &t, &tn)) return;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + BN - 1) / BN, blockIdx.x, &t, &tn)) return;
   typedef typename D::V V;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = tn * WIDE + (SIDE ? wave * BN : 0), left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
-  if (SIDE && left <= 0) return;
+  const int n0 = tn * BN, left = a.n - n0, rows = t.count - t.m * 16, q = lane >> 4;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
   const int blocks = (a.k + 127) / 128;  // of 128 steps
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + (row + min(lane & 15, rows - 1)) * a.ldx + q * 8;
-  uint64_t wb[NF];  // the lane's rows' first blocks
-#pragma unroll
-  for (int j = 0; j < NF; j++) wb[j] = ((uint64_t)t.g * a.n + n0 + min((lane & 15) + j * 16, left - 1)) * blocks;
+  const Zeros zeros[2] = {a.w[0], a.w[M - 1]};
+  const uint64_t wb = ((uint64_t)t.g * a.n + n0 + min(lane & 15, left - 1)) * blocks;  // the lane's row's first block
   struct Step {
-    i32x4 w[F][2], x[8];
-    Scales<S> s[F];
+    i32x4 w[M][2], x[8];
+    Scales<S> s[M];
   };
   auto load = [&](Step& s, int b) {
-    if (b + 2 <= blocks) {
 #pragma unroll
-      for (int f = 0; f < F; f++) {
-        const i32x4* p = reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + (wb[f % NF] + b) * 4 + q;
-        s.w[f][0] = p[0];
-        s.w[f][1] = p[4];
-        s.s[f].load(a.w[f / NF], (wb[f % NF] + b) * (S / 2));
-      }
-    } else {
-      // one block is left: zeros behind it
+    for (int f = 0; f < M; f++) {
+      const i32x4* p = reinterpret_cast<const i32x4*>(a.w[f].codes) + (wb + b) * 4 + q;
+      s.w[f][0] = p[0];
+      s.w[f][1] = p[4];
+      s.s[f].load(a.w[f], zeros[f], (wb + b) * (S / 2));
+    }
 #pragma unroll
-      for (int f = 0; f < F; f++) {
-        const uint64_t at = wb[f % NF] + b;
-        s.w[f][0] = (reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + at * 4)[q];
-        s.w[f][1] = i32x4{0, 0, 0, 0};
+    for (int u = 0; u < 8; u++) s.x[u] = load16(x + b * 128 + u * 32);
+  };
+  // the last one or two blocks, up to the end of x; zeros behind them
+  auto load_last = [&](Step& s, int b) {
 #pragma unroll
-        for (auto& v : s.s[f].s.v) v = 0;
+    for (int f = 0; f < M; f++) {
 #pragma unroll
-        for (auto& v : s.s[f].z.v) v = 0;
+      for (auto& v : s.s[f].s.v) v = 0;
+#pragma unroll
+      for (auto& v : s.s[f].z.v) v = 0;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        s.w[f][h] = i32x4{0, 0, 0, 0};
+        if (b + h >= blocks) continue;
+        const uint64_t at = wb + b + h;
+        s.w[f][h] = (reinterpret_cast<const i32x4*>(a.w[f].codes) + at * 4)[q];
 #pragma unroll
         for (int i = 0; i < S / 2; i++) {
-          s.s[f].s.v[i / 2] |= (uint32_t)a.w[f / NF].scales[at * (S / 2) + i] << (i & 1 ? 16 : 0);
-          s.s[f].z.v[i / 4] |= (a.w[f / NF].zeros ? (uint32_t)a.w[f / NF].zeros[at * (S / 2) + i] : 8u) << 8 * (i & 3);
+          const int o = h * (S / 2) + i;
+          s.s[f].s.v[o / 2] |= (uint32_t)a.w[f].scales[at * (S / 2) + i] << (o & 1 ? 16 : 0);
+          s.s[f].z.v[o / 4] |= (uint32_t)zeros[f].p[at * (S / 2) + i] << 8 * (o & 3);
         }
       }
     }
-    if (b * 128 + 256 <= a.k) {
 #pragma unroll
-      for (int u = 0; u < 8; u++) s.x[u] = load16(x + b * 128 + u * 32);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 8; u++) s.x[u] = load_some(x + b * 128 + u * 32, a.k - b * 128 - u * 32 - q * 8);
-    }
+    for (int u = 0; u < 8; u++) s.x[u] = load_some(x + b * 128 + u * 32, a.k - b * 128 - u * 32 - q * 8);
   };
   const V one = ones(D());
-  f32x4 acc[F];
+  f32x4 acc[M];
 #pragma unroll
-  for (int f = 0; f < F; f++) acc[f] = f32x4{0, 0, 0, 0};
-  auto multiply = [&](const Step& s) {
-    f32x4 sum[F], xsum = {0, 0, 0, 0};
+  for (int f = 0; f < M; f++) acc[f] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](Step& s) {
 #pragma unroll
-    for (int f = 0; f < F; f++) sum[f] = f32x4{0, 0, 0, 0};
+    for (int f = 0; f < M; f++) s.s[f].wait();
+    f32x4 sum[M], xsum = {0, 0, 0, 0};
+#pragma unroll
+    for (int f = 0; f < M; f++) sum[f] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < 8; u++) {
       V xu = __builtin_bit_cast(V, s.x[u]);
       if (u * 32 % BLOCK == 0) in_order(xu);
 #pragma unroll
-      for (int f = 0; f < F; f++) sum[f] = mfma(xu, expand(s.w[f][u / 4][u % 4], D()), sum[f]);
+      for (int f = 0; f < M; f++) sum[f] = mfma(xu, expand(s.w[f][u / 4][u % 4], D()), sum[f]);
       xsum = mfma(xu, one, xsum);
       if ((u + 1) * 32 % BLOCK == 0) {
         const int i = u * 32 / BLOCK;
 #pragma unroll
-        for (int f = 0; f < F; f++) {
-          add_block(acc[f], sum[f], xsum, s.s[f].scale(i, a.half), s.s[f].zero(i));
+        for (int f = 0; f < M; f++) {
+          add_block(acc[f], sum[f], xsum, s.s[f].scale(i, a.half), s.s[f].zero(zeros[f], i));
           in_order(acc[f]);
           sum[f] = f32x4{0, 0, 0, 0};
         }
@@ -150,42 +165,209 @@ __global__ __launch_bounds__(256) void gq_mm_thin(GqMmArgs a) {
       }
     }
   };
-  constexpr int STEP = SIDE ? 2 : 2 * kGqWaves;
-  int b = SIDE ? 0 : wave * 2;
+  // this wave's whole steps of 256: no branch on the way, so that the loads of the next one stay
+  // under way while one is multiplied
+  const int whole = a.k / 256, many = whole > wave ? (whole - wave + kGqWaves - 1) / kGqWaves : 0;
   Step s[2];
-  if (b < blocks) load(s[0], b);
-  while (b < blocks) {
-    if (b + STEP < blocks) load(s[1], b + STEP);
+  int i = 0;
+  if (many) load(s[0], wave * 2);
+  for (; i + 2 < many; i += 2) {
+    load(s[1], (wave + (i + 1) * kGqWaves) * 2);
     multiply(s[0]);
-    b += STEP;
-    if (b >= blocks) break;
-    if (b + STEP < blocks) load(s[0], b + STEP);
+    load(s[0], (wave + (i + 2) * kGqWaves) * 2);
     multiply(s[1]);
-    b += STEP;
+  }
+  if (i + 1 < many) {
+    load(s[1], (wave + (i + 1) * kGqWaves) * 2);
+    multiply(s[0]);
+    multiply(s[1]);
+  } else if (i < many) {
+    multiply(s[0]);
+  }
+  if (whole * 2 < blocks && whole % kGqWaves == wave) {
+    load_last(s[0], whole * 2);
+    multiply(s[0]);
   }
   // a lane: column lane % 16 of each 16, rows lane / 16 * 4 + e
 #pragma unroll
-  for (int f = 0; f < F; f++)
+  for (int f = 0; f < M; f++)
 #pragma unroll
-    for (int e = 0; e < 4; e++) part[f / NF][(wave * 16 + q * 4 + e) * LD + f % NF * 16 + (lane & 15)] = acc[f][e];
-  if (SIDE) wave_order();
-  else __syncthreads();
-  for (int p = SIDE ? lane : threadIdx.x; p < 4 * BN; p += SIDE ? 64 : 256) {
-  const int r = p / (BN / 4), c = p % (BN / 4) * 4;
-  if (r >= rows || c >= left) continue;
+    for (int e = 0; e < 4; e++) part[f][(wave * 16 + q * 4 + e) * LD + (lane & 15)] = acc[f][e];
+  __syncthreads();
+  const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 4;
+  if (threadIdx.x >= 64 || r >= rows || c >= left) return;
   f32x4 v[M];
 #pragma unroll
   for (int m = 0; m < M; m++) {
     v[m] = f32x4{0, 0, 0, 0};
-    if (SIDE) v[m] = *reinterpret_cast<const f32x4*>(part[m] + (wave * 16 + r) * LD + c);
-    else
 #pragma unroll
-      for (int i = 0; i < kGqWaves; i++) v[m] += *reinterpret_cast<const f32x4*>(part[m] + (i * 16 + r) * LD + c);
+    for (int i = 0; i < kGqWaves; i++) v[m] += *reinterpret_cast<const f32x4*>(part[m] + (i * 16 + r) * LD + c);
   }
   if (GLU) v[0] = gated(v[0], v[M - 1], a.act);
   const uint64_t at = (row + r) * a.ldo + n0;
   if (a.out_f32) store4(static_cast<float*>(a.out) + at, c, left, v[0]);
   else store4(static_cast<typename D::T*>(a.out) + at, c, left, v[0]);
+}
+
+// The same where there are enough columns for the card: every wave has all of the steps of
+// 32 columns of its own (GLU: 16 of each matrix), and x, which the waves share, goes through LDS, 2048 steps at a time.
+// What bounds this is the lines that loads touch, 16 rows each, more than the bytes: so the
+// scales are loaded 8 at a time (64 tokens over 8 of 256 experts, 7168 x 2048, both forms: with x
+// read by each wave and scales by each step 1220 us; without x 1050, without scales 1010).
+constexpr int kSideWaves = 8;
+
+template <typename D, int BLOCK, bool GLU>
+__global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
+  constexpr int NF = GLU ? 1 : 2, BN = 16 * NF, M = GLU ? 2 : 1, F = M * NF, GS = 8 * BLOCK / 256;  // steps of 256 to a group of scales
+  constexpr int CHUNK = 2048, ROW = CHUNK / 8, LD = BN + 4;  // contraction steps in LDS; 16-byte pieces of a row
+  __shared__ i32x4 xs[16 * ROW];
+  static_assert(sizeof(xs) >= M * kSideWaves * 16 * LD * 4, "the results pass through x's memory");
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<16>(a.offsets, a.groups, a.rows, (a.n + kSideWaves * BN - 1) / (kSideWaves * BN), blockIdx.x, &t, &tn))
+    return;
+  typedef typename D::V V;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane >> 4;
+  const int n0 = (tn * kSideWaves + wave) * BN, left = a.n - n0, rows = min(t.count - t.m * 16, 16);
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * 16;
+  const int blocks = (a.k + 127) / 128, many = blocks * (128 / BLOCK);  // of 128 steps; scales of a row
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.ldx;
+  const Zeros zeros[2] = {a.w[0], a.w[M - 1]};
+  uint64_t wr[NF];  // the lane's rows; a wave without columns reads the last row
+#pragma unroll
+  for (int j = 0; j < NF; j++) wr[j] = (uint64_t)t.g * a.n + min(n0 + (lane & 15) + j * 16, a.n - 1);
+  struct Codes {
+    i32x4 w[F][2];
+  };
+  auto load = [&](Codes& c, int b) {
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+      const i32x4* p = reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + (wr[f % NF] * blocks + b) * 4 + q;
+      c.w[f][0] = p[0];
+      c.w[f][1] = p[4];
+    }
+  };
+  auto load_last = [&](Codes& c, int b) {
+#pragma unroll
+    for (int f = 0; f < F; f++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        c.w[f][h] = i32x4{0, 0, 0, 0};
+        if (b + h < blocks)
+          c.w[f][h] = (reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + (wr[f % NF] * blocks + b + h) * 4)[q];
+      }
+  };
+  struct Group {
+    Scales<8> s[F];
+  };
+  auto load_scales = [&](Group& g, int at) {
+#pragma unroll
+    for (int f = 0; f < F; f++) g.s[f].load(a.w[f / NF], zeros[f / NF], wr[f % NF] * many + at);
+  };
+  auto load_scales_last = [&](Group& g, int at) {
+#pragma unroll
+    for (int f = 0; f < F; f++) {
+#pragma unroll
+      for (auto& v : g.s[f].s.v) v = 0;
+#pragma unroll
+      for (auto& v : g.s[f].z.v) v = 0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        if (at + i >= many) continue;
+        g.s[f].s.v[i / 2] |= (uint32_t)a.w[f / NF].scales[wr[f % NF] * many + at + i] << (i & 1 ? 16 : 0);
+        g.s[f].z.v[i / 4] |= (uint32_t)zeros[f / NF].p[wr[f % NF] * many + at + i] << 8 * (i & 3);
+      }
+    }
+  };
+  // x from step k0 on, zeros behind its end; the pieces of a row are permuted by the row, so that
+  // 16 rows lie in different banks
+  auto stage = [&](int k0) {
+    __syncthreads();
+    for (int p = threadIdx.x; p < rows * ROW; p += 64 * kSideWaves) {
+      const int r = p / ROW, c = p % ROW, k = k0 + c * 8;
+      xs[r * ROW + (c ^ r)] = load_some(x + (uint64_t)r * a.ldx + k, a.k - k);
+    }
+    __syncthreads();
+  };
+  const int r = min(lane & 15, rows - 1);
+  const V one = ones(D());
+  f32x4 acc[F];
+#pragma unroll
+  for (int f = 0; f < F; f++) acc[f] = f32x4{0, 0, 0, 0};
+  // step `st` of 256, the i-th of its group of scales
+  auto multiply = [&](const Codes& c, const Group& g, int st, auto i) {
+    const int piece = (st * 32 & (ROW - 1)) + q;
+    f32x4 sum[F], xsum = {0, 0, 0, 0};
+#pragma unroll
+    for (int f = 0; f < F; f++) sum[f] = f32x4{0, 0, 0, 0};
+    each<8>([&](auto u) {
+      V xu = __builtin_bit_cast(V, xs[r * ROW + ((piece + u.v * 4) ^ r)]);
+      if (u.v * 32 % BLOCK == 0) in_order(xu);
+#pragma unroll
+      for (int f = 0; f < F; f++) sum[f] = mfma(xu, expand(c.w[f][u.v / 4][u.v % 4], D()), sum[f]);
+      xsum = mfma(xu, one, xsum);
+      if constexpr ((u.v + 1) * 32 % BLOCK == 0) {
+        constexpr int B = (i.v * 256 + u.v * 32) / BLOCK;
+#pragma unroll
+        for (int f = 0; f < F; f++) {
+          add_block(acc[f], sum[f], xsum, g.s[f].scale(B, a.half), g.s[f].zero(zeros[f / NF], B));
+          in_order(acc[f]);
+          sum[f] = f32x4{0, 0, 0, 0};
+        }
+        xsum = f32x4{0, 0, 0, 0};
+      }
+    });
+  };
+  const int whole = a.k / (8 * BLOCK);  // groups of 8 scales
+  int st = 0;
+  Codes c[2];
+  Group g[2];
+  if (whole) {
+    load(c[0], 0);
+    load_scales(g[0], 0);
+  }
+  // The next group's scales and the next step's codes are under way while a step is
+  // multiplied, without a branch on the way.
+  auto group = [&](int i, auto last) {
+    if (st * 256 % CHUNK == 0) stage(st * 256);
+    if constexpr (!last.v) load_scales(g[1], (i + 1) * 8);
+    each<GS>([&](auto s) {
+      if constexpr (!last.v || s.v + 1 < GS) load(c[1], st * 2 + 2);
+      multiply(c[0], g[0], st, s);
+      c[0] = c[1];
+      st++;
+    });
+    g[0] = g[1];
+  };
+  for (int i = 0; i + 1 < whole; i++) group(i, Int<0>());
+  if (whole) group(whole - 1, Int<1>());
+  if (whole * 8 * BLOCK < a.k) {
+    if (st * 256 % CHUNK == 0) stage(st * 256);
+    load_scales_last(g[0], whole * 8);
+    each<GS>([&](auto s) {
+      if (st * 256 < a.k) {
+        load_last(c[0], st * 2);
+        multiply(c[0], g[0], st, s);
+      }
+      st++;
+    });
+  }
+  // a lane: column lane % 16 of each 16, rows lane / 16 * 4 + e
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(xs) + wave * M * 16 * LD;
+#pragma unroll
+  for (int f = 0; f < F; f++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) part[(f / NF * 16 + q * 4 + e) * LD + f % NF * 16 + (lane & 15)] = acc[f][e];
+  wave_order();
+  for (int p = lane; p < 4 * BN; p += 64) {
+    const int m = p / (BN / 4), col = p % (BN / 4) * 4;
+    if (m >= rows || col >= left) continue;
+    f32x4 v = *reinterpret_cast<const f32x4*>(part + m * LD + col);
+    if (GLU) v = gated(v, *reinterpret_cast<const f32x4*>(part + ((M - 1) * 16 + m) * LD + col), a.act);
+    const uint64_t at = (row + m) * a.ldo + n0;
+    if (a.out_f32) store4(static_cast<float*>(a.out) + at, col, left, v);
+    else store4(static_cast<typename D::T*>(a.out) + at, col, left, v);
   }
 }
 
@@ -216,6 +398,7 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
 #pragma unroll
   for (int j = 0; j < WN; j++) wb[j] = (uint32_t)min(c0 + (GLU ? j % 2 : j) * 16 + (lane & 15), left - 1) * (uint32_t)blocks;
   const uint64_t first = ((uint64_t)t.g * a.n + n0) * blocks;
+  const Zeros zeros[2] = {a.w[0], a.w[GLU ? 1 : 0]};
   // of half a block: two words of every fragment, and its scales and zeros (BLOCK 128: with
   // the second half)
   constexpr int SH = S > 1 ? S / 2 : 1;
@@ -232,11 +415,9 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
       c.w[j] = *reinterpret_cast<const Raw<8>*>(w.codes + first * 64 + (at * 64 + q * 16 + h.v * 8));
       if (S == 1 && h.v == 0) continue;
       c.s[j] = *reinterpret_cast<const Raw<2 * SH>*>(reinterpret_cast<const char*>(w.scales + first * S) + sc * 2);
-      c.z[j] = 0x0808u;
-      if (w.zeros) {
-        if constexpr (SH == 2) c.z[j] = reinterpret_cast<const Raw<2>*>(w.zeros + first * S + sc)->v[0];
-        else c.z[j] = *(w.zeros + first * S + sc);
-      }
+      const uint8_t* z = zeros[GLU ? j / 2 : 0].p + first * S + sc;
+      if constexpr (SH == 2) c.z[j] = reinterpret_cast<const Raw<2>*>(z)->v[0];
+      else c.z[j] = *z;
     }
   };
   i32x4 xr[LA::N];
@@ -287,8 +468,10 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
         constexpr int B = SH == 2 ? part.v : 0;
 #pragma unroll
         for (int j = 0; j < WN; j++) {
-          const float sc = scale_of(B ? c.s[j].v[0] >> 16 : c.s[j].v[0] & 0xffffu, a.half);
-          const float ze = (float)(c.z[j] >> 8 * B & 255u);
+          uint32_t sw = c.s[j].v[0], zw = c.z[j];
+          in_order(sw);
+          in_order(zw);
+          const float sc = scale_of(B ? sw >> 16 : sw & 0xffffu, a.half), ze = zeros[GLU ? j / 2 : 0].value(zw, B);
 #pragma unroll
           for (int i = 0; i < WM; i++) {
             add_block(acc[i][j], sum[i][j], xsum[i], sc, ze);
@@ -306,11 +489,26 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
     put(0);
   }
   __syncthreads();
-  // the codes of a block's first half are here, as is its x
-  for (int b = 0; b < blocks; b++) {
-    load_x(2 * b + 1);
+  // The codes of a block's first half are here, as is its x.  Blocks that another whole one
+  // follows are taken without a branch, so that loads stay under way.
+  int b = 0;
+  for (; b + 1 < a.k / 128; b++) {
+    ga.load(xr, b * 128 + 64);
     load_codes(c[1], b, Int<1>());
     __builtin_amdgcn_sched_barrier(0);
+    multiply(c[0], Int<0>());
+    put(1);
+    __syncthreads();
+    ga.load(xr, b * 128 + 128);
+    load_codes(c[0], b + 1, Int<0>());
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(c[1], Int<1>());
+    put(0);
+    __syncthreads();
+  }
+  for (; b < blocks; b++) {
+    load_x(2 * b + 1);
+    load_codes(c[1], b, Int<1>());
     multiply(c[0], Int<0>());
     put(1);
     __syncthreads();
@@ -318,7 +516,6 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
       load_x(2 * b + 2);
       load_codes(c[0], b + 1, Int<0>());
     }
-    __builtin_amdgcn_sched_barrier(0);
     multiply(c[1], Int<1>());
     if (b + 1 < blocks) put(0);
     __syncthreads();
@@ -352,12 +549,20 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
   }
 }
 
-template <typename D, int BLOCK, bool GLU, int NF, bool SIDE>
+template <typename D, int BLOCK, bool GLU>
 hipError_t run_thin(uint64_t row_tiles, const GqMmArgs& a, hipStream_t s) {
-  constexpr int WIDE = 16 * NF * (SIDE ? kGqWaves : 1);
   dim3 grid;
-  if (hipError_t e = tile_grid(row_tiles * ((a.n + WIDE - 1) / WIDE), 256, &grid)) return e;
-  gq_mm_thin<D, BLOCK, GLU, NF, SIDE><<<grid, dim3(256), 0, s>>>(a);
+  if (hipError_t e = tile_grid(row_tiles * ((a.n + 15) / 16), 64 * kGqWaves, &grid)) return e;
+  gq_mm_thin<D, BLOCK, GLU><<<grid, dim3(64 * kGqWaves), 0, s>>>(a);
+  return hipGetLastError();
+}
+constexpr int side_columns(bool glu) { return (glu ? 16 : 32) * kSideWaves; }
+template <typename D, int BLOCK, bool GLU>
+hipError_t run_side(uint64_t row_tiles, const GqMmArgs& a, hipStream_t s) {
+  constexpr int WIDE = side_columns(GLU);
+  dim3 grid;
+  if (hipError_t e = tile_grid(row_tiles * ((a.n + WIDE - 1) / WIDE), 64 * kSideWaves, &grid)) return e;
+  gq_mm_side<D, BLOCK, GLU><<<grid, dim3(64 * kSideWaves), 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename D, int BLOCK, bool GLU, int BM>
@@ -375,9 +580,9 @@ hipError_t run_gq_mm(const GqMmArgs& a, hipStream_t s) {
   const uint64_t thin = max_row_tiles(rows, groups, 16);
   // (the tiles count blocks of 128 rows in 32 bits)
   if (rows <= 16 * groups || a.k > 1 << 25) {
-    constexpr int NF = GLU ? 1 : 2;
-    if (thin * ((a.n + 64 * NF - 1) / (64 * NF)) >= 8 * kUnits) return run_thin<D, BLOCK, GLU, NF, true>(thin, a, s);
-    return run_thin<D, BLOCK, GLU, 1, false>(thin, a, s);
+    constexpr int WIDE = side_columns(GLU);
+    if (thin * ((a.n + WIDE - 1) / WIDE) >= kUnits) return run_side<D, BLOCK, GLU>(thin, a, s);
+    return run_thin<D, BLOCK, GLU>(thin, a, s);
   }
   if (rows <= 96 * groups) return run_mid<D, BLOCK, GLU, 64>(a, s);
   return run_mid<D, BLOCK, GLU, 128>(a, s);

@@ -88,6 +88,7 @@ bool bad_data(const ciera_gq_t* q, const GqRanges& r) {
                            !aligned(q->zeros, 4));
 }
 bool overlap(Range a, const GqRanges& r) { return overlap(a, r.codes) || overlap(a, r.scales) || overlap(a, r.zeros); }
+uint32_t half_scales(const ciera_gq_t* q) { return q->scale_dtype == CIERA_FP16 ? ~0u : 0u; }
 GqStack gq_stack(const ciera_gq_t* q) {
   return GqStack{q->codes, static_cast<const uint16_t*>(q->scales), q->zeros};
 }
@@ -366,7 +367,7 @@ ciera_status_t ciera_gq_quantize(const ciera_matrix_t* x, uint32_t axis, const c
     return CIERA_ERR_INVALID_ARG;
   const GqQuantArgs a = {x->data, q->codes, static_cast<uint16_t*>(q->scales), q->zeros, x->row_stride,
                          x->group_stride, (int32_t)x->groups, (int32_t)x->rows, (int32_t)x->cols,
-                         q->scale_dtype == CIERA_FP16};
+                         half_scales(q)};
   return launched("4-bit integer quantisation launch",
                   launch_gq_quantize(x->dtype, axis, q->block, a, hip_stream(stream)));
 }
@@ -381,7 +382,7 @@ ciera_status_t ciera_gq_dequantize(const ciera_gq_t* q, const ciera_matrix_t* ou
   if (bad_data(out) || bad_data(q, rq)) return CIERA_ERR_INVALID_ARG;
   if (overlap(ro, rq)) return CIERA_ERR_INVALID_ARG;
   const GqDequantArgs a = {gq_stack(q), out->data, out->row_stride, out->group_stride, (int32_t)out->groups,
-                           (int32_t)out->rows, (int32_t)out->cols, q->scale_dtype == CIERA_FP16};
+                           (int32_t)out->rows, (int32_t)out->cols, half_scales(q)};
   return launched("4-bit integer dequantisation launch",
                   launch_gq_dequantize(out->dtype, q->block, a, hip_stream(stream)));
 }
@@ -407,7 +408,7 @@ static ciera_status_t gq_product(const ciera_matrix_t* x, const ciera_gq_t* w, c
   if (overlap(ro, rx) || overlap(ro, rw) || overlap(ro, rw2)) return CIERA_ERR_INVALID_ARG;
   const GqMmArgs g = {x->data, {gq_stack(w), gq_stack(w2)}, out->data, offsets, x->row_stride, out->row_stride,
                       (int32_t)x->rows, (int32_t)x->cols, (int32_t)w->rows, (int32_t)w->groups, (int32_t)act,
-                      w->scale_dtype == CIERA_FP16, out->dtype == CIERA_FP32};
+                      half_scales(w), out->dtype == CIERA_FP32};
   return launched("4-bit integer product launch", launch_gq_mm(x->dtype, w != w2, w->block, g, hip_stream(stream)));
 }
 

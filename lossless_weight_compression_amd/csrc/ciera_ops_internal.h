@@ -117,7 +117,7 @@ struct GqMmArgs {
   const int32_t* offsets;
   uint64_t ldx, ldo;
   int32_t rows, k, n, groups, act;
-  int32_t half;     // scales are fp16, else bf16
+  uint32_t half;    // all ones: scales are fp16, 0: bf16
   int32_t out_f32;  // else x's type
 };
 struct GqQuantArgs {
@@ -127,14 +127,14 @@ struct GqQuantArgs {
   uint8_t* zeros;
   uint64_t ldx, gsx;
   int32_t groups, rows, cols;  // of x
-  int32_t half;
+  uint32_t half;
 };
 struct GqDequantArgs {
   GqStack q;
   void* out;
   uint64_t ldo, gso;
   int32_t groups, rows, cols;
-  int32_t half;
+  uint32_t half;
 };
 
 // Most row tiles of height bm that ascending offsets can make of `rows` rows.

@@ -168,11 +168,18 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
   int begin[4], count[4], incl[4];
   uint32_t sums[4];
   auto four = [&](int c) {
+    // behind the last group both ends are the last offset
+    int from[4], to[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       const int g = c + i * 64 + (threadIdx.x & 63);
-      begin[i] = count[i] = 0;
-      if (g < groups) group_range(off, g, rows, &begin[i], &count[i]);
+      from[i] = off[min(g, groups)];
+      to[i] = off[min(g + 1, groups)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      begin[i] = min(max(from[i], 0), rows);
+      count[i] = max(min(max(to[i], 0), rows) - begin[i], 0);
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -184,7 +191,9 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
     return sums[0] + sums[1] + sums[2] + sums[3];
   };
   uint32_t total = 0;
-  for (int c = 0; c < groups; c += 256) total += four(c);
+  if (!off) total = (rows + BM - 1) / BM;
+  else
+    for (int c = 0; c < groups; c += 256) total += four(c);
   uint64_t first;
   uint32_t many;
   die_run((uint64_t)total * ntiles, bid % kXcds, &first, &many);
@@ -192,28 +201,37 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
   const uint64_t tile = first + bid / kXcds;
   const uint32_t mt = (uint32_t)(tile / ntiles);
   *n = (int)(tile % ntiles);
-  uint32_t before = 0;
-  int c = 0;
-  if (groups > 256) {
-    for (;; c += 256) {
-      const uint32_t all = four(c);
-      if (before + all > mt || c + 256 >= groups) break;
-      before += all;
+  GroupTile r = {0, (int)mt, 0, rows};
+  if (off) {
+    uint32_t before = 0;
+    int c = 0;
+    if (groups > 256) {
+      for (;; c += 256) {
+        const uint32_t all = four(c);
+        if (before + all > mt || c + 256 >= groups) break;
+        before += all;
+      }
     }
-  }
+    // the chunk of 64 that it is in
+    int i = 0, b = begin[0], k = count[0], up = incl[0];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    if (mt < before + sums[i]) {
-      const int l = __builtin_ctzll(__ballot(before + (uint32_t)incl[i] > mt));
-      t->g = c + i * 64 + l;
-      t->begin = __builtin_amdgcn_readlane(begin[i], l);
-      t->count = __builtin_amdgcn_readlane(count[i], l);
-      t->m = (int)(mt - before) - (__builtin_amdgcn_readlane(incl[i], l) - (t->count + BM - 1) / BM);
-      return true;
+    for (int j = 0; j < 3; j++) {
+      const bool on = i == j && mt >= before + sums[j];
+      before += on ? sums[j] : 0;
+      i = on ? j + 1 : i;
+      b = on ? begin[j + 1] : b;
+      k = on ? count[j + 1] : k;
+      up = on ? incl[j + 1] : up;
     }
-    before += sums[i];
+    const uint64_t hit = __ballot(before + (uint32_t)up > mt);
+    const int l = hit ? __builtin_ctzll(hit) : 0;
+    r.g = c + i * 64 + l;
+    r.begin = __builtin_amdgcn_readlane(b, l);
+    r.count = __builtin_amdgcn_readlane(k, l);
+    r.m = (int)(mt - before) - (__builtin_amdgcn_readlane(up, l) - (r.count + BM - 1) / BM);
   }
-  return false;
+  *t = r;
+  return true;
 }
 
 // v, as if computed anew here: what depends on it is not kept in registers across the
