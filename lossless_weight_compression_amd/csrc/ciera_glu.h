@@ -52,11 +52,12 @@ __device__ __forceinline__ void big_tiles(const int32_t* offsets, int groups, in
   }
 }
 
-// Whether the large tiles take a call: what gives them half the card and can be read straight
-// into LDS.  cols: columns of a tile.
+// Whether the large tiles take a call: more than 128 rows to a group (up to there tiles of that
+// height have one to a group), half the card at least, and rows that can be read straight into
+// LDS.  cols: columns of a tile.
 template <bool TRANS>
 bool big_enough(bool flat, int64_t rows, int64_t groups, int n, int k, int cols) {
-  return flat && k && k % 8 == 0 && (TRANS || n % 8 == 0) && rows >= 256 * groups &&
+  return flat && k && k % 8 == 0 && (TRANS || n % 8 == 0) && rows > 128 * groups &&
          max_row_tiles(rows, groups, 256) * ((n + cols - 1) / cols) >= kUnits / 2;
 }
 

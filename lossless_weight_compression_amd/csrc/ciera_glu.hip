@@ -57,26 +57,53 @@ __global__ __launch_bounds__(512) void glu_mm_thin(GluMmArgs a) {
   part.join(rows, left, [&](int m, int c, const f32x4* v) { out.put4(m, c, left, v[0], v[1]); });
 }
 
+template <typename D, bool TRANS, typename O, int BM, int TEAMS>
+hipError_t run_glu_mm_mid(const GluMmArgs& a, hipStream_t s) {
+  
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + 63) / 64), 256 * TEAMS, &grid)) return e;
+  glu_mm_mid<D, TRANS, O, BM, TEAMS><<<grid, dim3(256 * TEAMS), 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename D, bool TRANS, typename O, int VEC>
+hipError_t run_glu_mm_thin(const GluMmArgs& a, hipStream_t s) {
+  constexpr int BN = TRANS ? 16 : 16 * VEC;
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 16) * ((a.n + BN - 1) / BN), 512, &grid)) return e;
+  glu_mm_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename D, bool TRANS, typename O>
 hipError_t run_glu_mm(bool flat, const GluMmArgs& a, hipStream_t s) {
+  // By rows to a group on average; 64 experts of 2048 x 1024, bf16, us, inputs from call to call
+  // in turn:
+  //   rows                2    8   16   32   64  100  128  192  256
+  //   [K, N] thin       99  100  102  143  254
+  //          64 rows   105  105  107  110  116  151  154  214
+  //          128 rows       103  106  111  119  126  129  184
+  //          256 x 128                                      145
+  //   [N, K] thin           117       239
+  //          64 rows         90       102
+  // The thin kernel takes [N, K], and more rows, only where tiles of 64 rows are too few for the
+  // card (1 token over 8 of the experts, [N, K], 15 us for 17; one matrix 4096 x 1024, 200 rows, 27
+  // for 32), with half the columns where even its workgroups are few (24 rows 20.9 for 23.5).  Two
+  // teams to a tile where there is one tile to a unit at most (900 rows 32 for 36).
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 128) && short_stride(a.ldx) && short_stride(a.ldg) &&
       short_stride(a.ldu)) {
     if (a.gate) glu_mm_big<D, TRANS, O, true><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     else glu_mm_big<D, TRANS, O, false><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
-  const uint64_t thin = max_row_tiles(a.rows, a.groups, 16);
-  if (a.rows <= 16 * (int64_t)a.groups) {
-    constexpr int VEC = 4, BN = TRANS ? 16 : 16 * VEC;
-    dim3 grid;
-    if (hipError_t e = tile_grid(thin * ((a.n + BN - 1) / BN), 512, &grid)) return e;
-    glu_mm_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
-    return hipGetLastError();
+  const int64_t rows = a.rows, groups = a.groups;
+  const uint64_t nt = (a.n + 63) / 64, mid = max_row_tiles(rows, groups, 64) * nt;
+  if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 256 * groups && mid <= kUnits / 4)) {
+    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) <= kUnits / 2) return run_glu_mm_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
+    return run_glu_mm_thin<D, TRANS, O, 4>(a, s);
   }
-  dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 64) * ((a.n + 63) / 64), 256, &grid)) return e;
-  glu_mm_mid<D, TRANS, O, 64, 1><<<grid, dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+  if (mid < kUnits && a.k >= 512) return run_glu_mm_mid<D, TRANS, O, 64, 2>(a, s);
+  if (rows <= 64 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits) return run_glu_mm_mid<D, TRANS, O, 64, 1>(a, s);
+  return run_glu_mm_mid<D, TRANS, O, 128, 1>(a, s);
 }
 
 struct RunMm {

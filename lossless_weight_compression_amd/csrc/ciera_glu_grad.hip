@@ -55,25 +55,49 @@ __global__ __launch_bounds__(512) void glu_grad_thin(GluGradArgs a) {
   part.join(rows, left, [&](int m, int c, const f32x4* v) { out.put(m, c, min(left - c, 4), v[0], f32x4{0, 0, 0, 0}); });
 }
 
+template <typename D, bool TRANS, typename O, int BM, int TEAMS>
+hipError_t run_glu_grad_mid(const GluGradArgs& a, hipStream_t s) {
+  
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + 127) / 128), 256 * TEAMS, &grid)) return e;
+  glu_grad_mid<D, TRANS, O, BM, TEAMS><<<grid, dim3(256 * TEAMS), 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename D, bool TRANS, typename O, int VEC>
+hipError_t run_glu_grad_thin(const GluGradArgs& a, hipStream_t s) {
+  constexpr int BN = TRANS ? 16 : 16 * VEC;
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 16) * ((a.n + BN - 1) / BN), 512, &grid)) return e;
+  glu_grad_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename D, bool TRANS, typename O>
 hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
+  // As in glu_mm; 64 experts of 2048 x 1024, bf16, us:
+  //   rows                2    8   16   32   64  100  128  192  256
+  //   [K, N] thin       51   54   59   80  129
+  //          64 rows    49   48   49   55   62   89   95  126
+  //          128 rows        53   53   56   66   74   82  127
+  //          256 x 256                                       94
+  //   [N, K] thin           74       158
+  //          64 rows        52        57
+  // (One matrix 4096 x 1024, 200 rows, thin 17 for 40; 24 rows, half the columns, 9.9 for 14.9; 900
+  // rows with two teams 33 for 41.)
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 256) && short_stride(a.ldx) && short_stride(a.ldw) &&
       short_stride(a.ldg) && short_stride(a.ldu) && short_stride(a.lddg) && short_stride(a.lddu)) {
     glu_grad_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
-  const uint64_t thin = max_row_tiles(a.rows, a.groups, 16);
-  if (a.rows <= 16 * (int64_t)a.groups) {
-    constexpr int VEC = 4, BN = TRANS ? 16 : 16 * VEC;
-    dim3 grid;
-    if (hipError_t e = tile_grid(thin * ((a.n + BN - 1) / BN), 512, &grid)) return e;
-    glu_grad_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
-    return hipGetLastError();
+  const int64_t rows = a.rows, groups = a.groups;
+  const uint64_t nt = (a.n + 127) / 128, mid = max_row_tiles(rows, groups, 64) * nt;
+  if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 256 * groups && mid <= kUnits / 4)) {
+    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) <= kUnits / 2) return run_glu_grad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
+    return run_glu_grad_thin<D, TRANS, O, 4>(a, s);
   }
-  dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 64) * ((a.n + 127) / 128), 256, &grid)) return e;
-  glu_grad_mid<D, TRANS, O, 64, 1><<<grid, dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+  if (mid < kUnits && a.k >= 512) return run_glu_grad_mid<D, TRANS, O, 64, 2>(a, s);
+  if (rows <= 64 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits) return run_glu_grad_mid<D, TRANS, O, 64, 1>(a, s);
+  return run_glu_grad_mid<D, TRANS, O, 128, 1>(a, s);
 }
 
 struct RunGrad {

@@ -56,26 +56,51 @@ __global__ __launch_bounds__(512) void glu_xgrad_thin(GluXgradArgs a) {
   part.join(rows, left, [&](int m, int c, const f32x4* v) { store4(out + (uint64_t)m * a.ldo, c, left, v[0]); });
 }
 
+template <typename D, bool TRANS, typename O, int BM>
+hipError_t run_glu_xgrad_mid(const GluXgradArgs& a, hipStream_t s) {
+  constexpr int TEAMS = 2;
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + 127) / 128), 256 * TEAMS, &grid)) return e;
+  glu_xgrad_mid<D, TRANS, O, BM><<<grid, dim3(256 * TEAMS), 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename D, bool TRANS, typename O, int VEC>
+hipError_t run_glu_xgrad_thin(const GluXgradArgs& a, hipStream_t s) {
+  constexpr int BN = TRANS ? 16 : 16 * VEC;
+  dim3 grid;
+  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 16) * ((a.n + BN - 1) / BN), 512, &grid)) return e;
+  glu_xgrad_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename D, bool TRANS, typename O>
 hipError_t run_glu_xgrad(bool flat, const GluXgradArgs& a, hipStream_t s) {
   // the second product's operands are addressed with the first one's offsets
+  // As in glu_mm; 64 experts of 2048 x 1024, bf16, us:
+  //   rows                2    8   16   32   64  100  128  192  256
+  //   [K, N] thin       94   99  106  143  236
+  //          64 rows    97   96  100  104  112  150  160  211
+  //          128 rows        99   99  104  114  122  127  193
+  //          256 x 256                                      138
+  //   [N, K] thin          107       238
+  //          64 rows        90       112
+  // Tiles of two teams take a unit each: 128 rows also where those of 64 would be more than one
+  // round of the card (13 groups, 2234 rows, 1447 x 777, 46 for 57; 7 groups, 2006 rows, 515 x 777,
+  // are one round: 17 for 21).
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 256) && short_stride(a.ldxg) && short_stride(a.ldg) &&
       a.ldxg == a.ldxu && a.ldg == a.ldu) {
     glu_xgrad_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
     return hipGetLastError();
   }
-  const uint64_t thin = max_row_tiles(a.rows, a.groups, 16);
-  if (a.rows <= 16 * (int64_t)a.groups) {
-    constexpr int VEC = 4, BN = TRANS ? 16 : 16 * VEC;
-    dim3 grid;
-    if (hipError_t e = tile_grid(thin * ((a.n + BN - 1) / BN), 512, &grid)) return e;
-    glu_xgrad_thin<D, TRANS, O, VEC><<<grid, dim3(512), 0, s>>>(a);
-    return hipGetLastError();
+  const int64_t rows = a.rows, groups = a.groups;
+  const uint64_t nt = (a.n + 127) / 128, mid = max_row_tiles(rows, groups, 64) * nt;
+  if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 256 * groups && mid <= kUnits / 4)) {
+    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) <= kUnits / 2) return run_glu_xgrad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
+    return run_glu_xgrad_thin<D, TRANS, O, 4>(a, s);
   }
-  dim3 grid;
-  if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, 64) * ((a.n + 127) / 128), 512, &grid)) return e;
-  glu_xgrad_mid<D, TRANS, O, 64><<<grid, dim3(512), 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t tiles = (rows / 64 + groups / 2 + 1) * (int64_t)nt;  // of groups that end anywhere
+  if (rows <= 64 * groups || tiles <= (int64_t)kUnits) return run_glu_xgrad_mid<D, TRANS, O, 64>(a, s);
+  return run_glu_xgrad_mid<D, TRANS, O, 128>(a, s);
 }
 
 struct RunXgrad {

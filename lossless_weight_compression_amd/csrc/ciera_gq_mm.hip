@@ -576,16 +576,23 @@ hipError_t run_mid(const GqMmArgs& a, hipStream_t s) {
 
 template <typename D, int BLOCK, bool GLU>
 hipError_t run_gq_mm(const GqMmArgs& a, hipStream_t s) {
+  // By rows to a group on average; 64 experts of 2048 x 1024, blocks of 128, bf16, us, one
+  // product and (GLU) both:
+  //   rows                2        8       16       32       64      100      128      256
+  //   thin           32  58   43  68   49  72   90 132  171 254
+  //   side           15  26   17  28   17  27   26  46   45  85   74 137   85 158  162 304
+  //   64 rows        63 122   60 117   58 110   58 111   60 114  113 217  116 219  225 433
+  //   128 rows                                                    73 133   76 136  146 264
+  // The thin kernel is for calls with few columns to the card (1 token over 8 of the experts 6.0 and
+  // 8.3 for 12 and 12; one matrix 4096 x 1024, 64 rows, 8.8 and 11 for 24 and 22; 200 rows 24 and 32
+  // for 24 and 24), tiles only for what fills the card with them (900 rows 77 and 83 for 25 and 39).
   const int64_t rows = a.rows, groups = a.groups;
-  const uint64_t thin = max_row_tiles(rows, groups, 16);
+  const uint64_t thin = max_row_tiles(rows, groups, 16), wide = side_columns(GLU);
+  const uint64_t mid = max_row_tiles(rows, groups, 128) * ((a.n + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
   // (the tiles count blocks of 128 rows in 32 bits)
-  if (rows <= 16 * groups || a.k > 1 << 25) {
-    constexpr int WIDE = side_columns(GLU);
-    if (thin * ((a.n + WIDE - 1) / WIDE) >= kUnits) return run_side<D, BLOCK, GLU>(thin, a, s);
-    return run_thin<D, BLOCK, GLU>(thin, a, s);
-  }
-  if (rows <= 96 * groups) return run_mid<D, BLOCK, GLU, 64>(a, s);
-  return run_mid<D, BLOCK, GLU, 128>(a, s);
+  if (rows > 112 * groups && mid >= 2 * kUnits && a.k <= 1 << 25) return run_mid<D, BLOCK, GLU, 128>(a, s);
+  if (thin * ((a.n + wide - 1) / wide) >= 3 * kUnits / 8) return run_side<D, BLOCK, GLU>(thin, a, s);
+  return run_thin<D, BLOCK, GLU>(thin, a, s);
 }
 template <typename D, bool GLU>
 hipError_t by_block(int block, const GqMmArgs& a, hipStream_t s) {
