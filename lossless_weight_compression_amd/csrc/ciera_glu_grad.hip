@@ -92,7 +92,7 @@ hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t nt = (a.n + 127) / 128, mid = max_row_tiles(rows, groups, 64) * nt;
   if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 256 * groups && mid <= kUnits / 4)) {
-    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) <= kUnits / 2) return run_glu_grad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
+    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) < kUnits / 2) return run_glu_grad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
     return run_glu_grad_thin<D, TRANS, O, 4>(a, s);
   }
   if (mid < kUnits && a.k >= 512) return run_glu_grad_mid<D, TRANS, O, 64, 2>(a, s);

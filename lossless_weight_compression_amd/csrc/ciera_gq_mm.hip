@@ -373,9 +373,10 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
 
 // ------------------------------------------------------------------------ more rows
 // BM x 128 tiles (GLU: 64 columns of each matrix), 4 waves of BM / 2 x 64.  x goes through
-// LDS, 64 steps at a time, two stages; codes go from memory into the registers of the waves
-// that multiply them, since a code is 4 times smaller than what it expands to and two waves
-// share it at most.  A block's sums are kept apart from the tile's: as many registers again.
+// LDS, 64 steps at a time, two stages; codes and scales of 128 steps too, and are expanded by the
+// waves that multiply them (read from memory by each of these waves, both products of 16384 rows
+// over 64 experts of 2048 x 1024 took 531 us for 491).  A block's sums are kept apart from
+// the tile's: as many registers again.
 template <typename D, int BLOCK, bool GLU, int BM>
 __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
   constexpr int WM = BM / 32, WN = 4, COLUMNS = GLU ? 64 : 128, S = 128 / BLOCK, LD = 68;
@@ -383,6 +384,8 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
   typedef StageLoad<true, BM> LA;
   typedef typename D::V V;
   __shared__ i32x4 lds[2 * TA::kChunks > 4 * 16 * LD / 4 ? 2 * TA::kChunks : 4 * 16 * LD / 4];  // or the results
+  __shared__ i32x4 codes[2][128 * 4];      // [block][column][quarter]
+  __shared__ uint32_t scales[2][S][128];   // scale, and the zero in the upper half
   GroupTile t;
   int tn;
   if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + COLUMNS - 1) / COLUMNS, blockIdx.x, &t, &tn)) return;
@@ -392,32 +395,37 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
   const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * (COLUMNS / 2), blocks = (a.k + 127) / 128;
   LA ga;
   ga.init(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, rows);
-  // fragment j: 16 columns of the matrix j / (WN / 2) (GLU) or the only one; the lane's
-  // row's first block, counted from that of column n0
-  uint32_t wb[WN];
-#pragma unroll
-  for (int j = 0; j < WN; j++) wb[j] = (uint32_t)min(c0 + (GLU ? j % 2 : j) * 16 + (lane & 15), left - 1) * (uint32_t)blocks;
+  // What a thread loads of a block: a quarter of two columns' codes, 64 columns apart, and the
+  // scales of one column.  Blocks are counted from that of column n0.
   const uint64_t first = ((uint64_t)t.g * a.n + n0) * blocks;
-  const Zeros zeros[2] = {a.w[0], a.w[GLU ? 1 : 0]};
-  // of half a block: two words of every fragment, and its scales and zeros (BLOCK 128: with
-  // the second half)
-  constexpr int SH = S > 1 ? S / 2 : 1;
-  struct Codes {
-    Raw<8> w[WN];
-    Raw<2 * SH> s[WN];
-    uint32_t z[WN];
+  const uint32_t c1 = (uint32_t)min(tid >> 2, left - 1) * blocks, c2 = (uint32_t)min((tid >> 2) + (GLU ? 0 : 64), left - 1) * blocks;
+  const uint32_t cs = (uint32_t)min(tid & (COLUMNS - 1), left - 1) * blocks;
+  const GqStack &wa = a.w[0], &wb = a.w[GLU ? 1 : 0];
+  const Zeros za(wa), zb(wb);
+  const bool up = GLU && (tid & 64);
+  const char* ps = reinterpret_cast<const char*>((up ? wb : wa).scales + first * S);
+  const uint8_t* pz = (up ? zb : za).p + first * S;
+  struct Next {
+    i32x4 w[2];
+    Raw<2 * S> s;
+    uint32_t z;
   };
-  auto load_codes = [&](Codes& c, int b, auto h) {
+  auto load_codes = [&](Next& n, int b) {
+    n.w[0] = *reinterpret_cast<const i32x4*>(wa.codes + first * 64 + ((c1 + b) * 64 + (tid & 3) * 16));
+    n.w[1] = *reinterpret_cast<const i32x4*>(wb.codes + first * 64 + ((c2 + b) * 64 + (tid & 3) * 16));
+    n.s = *reinterpret_cast<const Raw<2 * S>*>(ps + (cs + b) * (2 * S));
+    if constexpr (S == 4) n.z = reinterpret_cast<const Raw<4>*>(pz + (cs + b) * S)->v[0];
+    else if constexpr (S == 2) n.z = reinterpret_cast<const Raw<2>*>(pz + (cs + b) * S)->v[0];
+    else n.z = pz[cs + b];
+  };
+  auto put_codes = [&](const Next& n, int h) {
+    codes[h][tid] = n.w[0];
+    codes[h][256 + tid] = n.w[1];
+    if (tid < 128) {
+      const uint32_t z = (n.z & za.kept) | (0x08080808u & ~za.kept);
 #pragma unroll
-    for (int j = 0; j < WN; j++) {
-      const GqStack& w = a.w[GLU ? j / 2 : 0];
-      const uint32_t at = wb[j] + b, sc = at * S + (S > 1 ? h.v * SH : 0);
-      c.w[j] = *reinterpret_cast<const Raw<8>*>(w.codes + first * 64 + (at * 64 + q * 16 + h.v * 8));
-      if (S == 1 && h.v == 0) continue;
-      c.s[j] = *reinterpret_cast<const Raw<2 * SH>*>(reinterpret_cast<const char*>(w.scales + first * S) + sc * 2);
-      const uint8_t* z = zeros[GLU ? j / 2 : 0].p + first * S + sc;
-      if constexpr (SH == 2) c.z[j] = reinterpret_cast<const Raw<2>*>(z)->v[0];
-      else c.z[j] = *z;
+      for (int i = 0; i < S; i++)
+        scales[h][i][tid] = ((uint32_t)n.s.v[i / 2] >> (i & 1 ? 16 : 0) & 0xffffu) | (z >> 8 * i & 255u) << 16;
     }
   };
   i32x4 xr[LA::N];
@@ -445,33 +453,33 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
     }
   };
   clear();
-  // half h of a block of 128 steps, from half h of LDS
-  auto multiply = [&](const Codes& c, auto h) {
+  // fragment j: 16 columns of the matrix j / 2 (GLU) or the only one, from this one of the tile's
+  auto column = [&](int j) { return (GLU ? j / 2 * 64 + c0 + j % 2 * 16 : c0 + j * 16) + (lane & 15); };
+  // half h of a block of 128 steps, from half h of LDS; its codes in buffer `buf`
+  auto multiply = [&](int buf, auto h) {
     const uint32_t pa = TA::place(lds + h.v * TA::kChunks, r0);
+    Raw<8> w[WN];
+#pragma unroll
+    for (int j = 0; j < WN; j++)
+      __builtin_memcpy(&w[j], __builtin_assume_aligned(reinterpret_cast<const char*>(&codes[buf][column(j) * 4 + q]) + h.v * 8, 8), 8);
     each<2>([&](auto part) {
       constexpr int U = h.v * 2 + part.v;
       V fx[WM];
-      each<WM>([&](auto i) {
-        fx[i.v] = __builtin_bit_cast(V, TA::template fragment<i.v, part.v>(pa));
-        in_order(fx[i.v]);
-      });
+      each<WM>([&](auto i) { fx[i.v] = __builtin_bit_cast(V, TA::template fragment<i.v, part.v>(pa)); });
 #pragma unroll
       for (int i = 0; i < WM; i++) xsum[i] = mfma(fx[i], one, xsum[i]);
 #pragma unroll
       for (int j = 0; j < WN; j++) {
-        V fw = expand(c.w[j].v[part.v], D());
+        V fw = expand(w[j].v[part.v], D());
         in_order(fw);
 #pragma unroll
         for (int i = 0; i < WM; i++) sum[i][j] = mfma(fx[i], fw, sum[i][j]);
       }
       if constexpr ((U + 1) * 32 % BLOCK == 0) {
-        constexpr int B = SH == 2 ? part.v : 0;
 #pragma unroll
         for (int j = 0; j < WN; j++) {
-          uint32_t sw = c.s[j].v[0], zw = c.z[j];
-          in_order(sw);
-          in_order(zw);
-          const float sc = scale_of(B ? sw >> 16 : sw & 0xffffu, a.half), ze = zeros[GLU ? j / 2 : 0].value(zw, B);
+          const uint32_t v = scales[buf][U * 32 / BLOCK][column(j)];
+          const float sc = scale_of(v & 0xffffu, a.half), ze = (float)(v >> 16);
 #pragma unroll
           for (int i = 0; i < WM; i++) {
             add_block(acc[i][j], sum[i][j], xsum[i], sc, ze);
@@ -482,42 +490,45 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
       }
     });
   };
-  Codes c[2];
+  Next next;
   if (blocks > 0) {
     load_x(0);
-    load_codes(c[0], 0, Int<0>());
+    load_codes(next, 0);
     put(0);
+    put_codes(next, 0);
   }
   __syncthreads();
-  // The codes of a block's first half are here, as is its x.  Blocks that another whole one
+  // A block's codes and the first half of its x are here.  Blocks that another whole one
   // follows are taken without a branch, so that loads stay under way.
   int b = 0;
   for (; b + 1 < a.k / 128; b++) {
     ga.load(xr, b * 128 + 64);
-    load_codes(c[1], b, Int<1>());
+    load_codes(next, b + 1);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(c[0], Int<0>());
+    multiply(b & 1, Int<0>());
     put(1);
     __syncthreads();
     ga.load(xr, b * 128 + 128);
-    load_codes(c[0], b + 1, Int<0>());
     __builtin_amdgcn_sched_barrier(0);
-    multiply(c[1], Int<1>());
+    multiply(b & 1, Int<1>());
     put(0);
+    put_codes(next, (b + 1) & 1);
     __syncthreads();
   }
   for (; b < blocks; b++) {
     load_x(2 * b + 1);
-    load_codes(c[1], b, Int<1>());
-    multiply(c[0], Int<0>());
+    multiply(b & 1, Int<0>());
     put(1);
     __syncthreads();
     if (b + 1 < blocks) {
       load_x(2 * b + 2);
-      load_codes(c[0], b + 1, Int<0>());
+      load_codes(next, b + 1);
     }
-    multiply(c[1], Int<1>());
-    if (b + 1 < blocks) put(0);
+    multiply(b & 1, Int<1>());
+    if (b + 1 < blocks) {
+      put(0);
+      put_codes(next, (b + 1) & 1);
+    }
     __syncthreads();
   }
   // a lane: column lane % 16 of each fragment, rows lane / 16 * 4 + e; turned around in LDS,
