@@ -7,6 +7,7 @@
 // zero it needs, for 4 rows.
 #include "ciera.h"
 #include "ciera_act.h"
+#include "ciera_big.h"
 #include "ciera_gq.h"
 #include "ciera_mid.h"
 #include "ciera_ops_internal.h"
@@ -373,26 +374,137 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
 
 // ------------------------------------------------------------------------ more rows
 // BM x 128 tiles (GLU: 64 columns of each matrix), 4 waves of BM / 2 x 64.  x goes through
-// LDS, 64 steps at a time, two stages; codes and scales of 128 steps too, and are expanded by the
-// waves that multiply them (read from memory by each of these waves, both products of 16384 rows
-// over 64 experts of 2048 x 1024 took 531 us for 491).  A block's sums are kept apart from
-// the tile's: as many registers again.
+// LDS, 64 steps at a time, codes and scales of 128 steps too, and are expanded by the waves that
+// multiply them.  (16384 rows over 64 experts of 2048 x 1024, both products: codes read from
+// memory by each of these waves 531 us, once to a workgroup 491, x and codes straight into LDS
+// 437.)  A block's sums are kept apart from the tile's: as many registers again.
+template <typename D, int BLOCK, bool GLU, int BM>
+struct GqTile {
+  static constexpr int WM = BM / 32, WN = 4, COLUMNS = GLU ? 64 : 128, S = 128 / BLOCK, LD = 68;
+  typedef StageTile<true, false, 16, BM> TA;
+  typedef typename D::V V;
+  static constexpr int kTurn = 4 * 16 * LD / 4;  // chunks that the results pass through
+  int lane, wave, q, r0, c0;
+  f32x4 acc[WM][WN], sum[WM][WN], xsum[WM];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < WM; i++) {
+      xsum[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < WN; j++) sum[i][j] = f32x4{0, 0, 0, 0};
+    }
+  }
+  __device__ __forceinline__ GqTile() {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    q = lane >> 4;
+    r0 = (wave >> 1) * (BM / 2);
+    c0 = (wave & 1) * (COLUMNS / 2);
+#pragma unroll
+    for (int i = 0; i < WM; i++)
+#pragma unroll
+      for (int j = 0; j < WN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+    clear();
+  }
+  // fragment j: 16 columns of the matrix j / 2 (GLU) or the only one, from this one of the tile's
+  __device__ __forceinline__ int column(int j) const { return (GLU ? j / 2 * 64 + c0 + j % 2 * 16 : c0 + j * 16) + (lane & 15); }
+  // Half H of a block of 128 steps: 64 steps of x, the block's codes [column][quarter] and its
+  // scales, with the zeros in their upper halves.
+  template <int H>
+  __device__ __forceinline__ void multiply(const i32x4* x, const i32x4* codes, const uint32_t (*scales)[128], uint32_t half) {
+    const uint32_t pa = TA::place(x, r0);
+    Raw<8> w[WN];
+#pragma unroll
+    for (int j = 0; j < WN; j++)
+      __builtin_memcpy(&w[j], __builtin_assume_aligned(reinterpret_cast<const char*>(&codes[column(j) * 4 + q]) + H * 8, 8), 8);
+    each<2>([&](auto part) {
+      constexpr int U = H * 2 + part.v;
+      V fx[WM];
+      each<WM>([&](auto i) { fx[i.v] = __builtin_bit_cast(V, TA::template fragment<i.v, part.v>(pa)); });
+      const V one = ones(D());
+#pragma unroll
+      for (int i = 0; i < WM; i++) xsum[i] = mfma(fx[i], one, xsum[i]);
+#pragma unroll
+      for (int j = 0; j < WN; j++) {
+        V fw = expand(w[j].v[part.v], D());
+        in_order(fw);
+#pragma unroll
+        for (int i = 0; i < WM; i++) sum[i][j] = mfma(fx[i], fw, sum[i][j]);
+      }
+      if constexpr ((U + 1) * 32 % BLOCK == 0) {
+#pragma unroll
+        for (int j = 0; j < WN; j++) {
+          const uint32_t v = scales[U * 32 / BLOCK][column(j)];
+          const float sc = scale_of(v & 0xffffu, half), ze = (float)(v >> 16);
+#pragma unroll
+          for (int i = 0; i < WM; i++) {
+            add_block(acc[i][j], sum[i][j], xsum[i], sc, ze);
+            in_order(acc[i][j]);
+          }
+        }
+        clear();
+      }
+    });
+  }
+  // A lane has column lane % 16 of each fragment, rows lane / 16 * 4 + e: turned around in LDS,
+  // 16 rows at a time, to 16 (GLU: 8) consecutive columns of a row.
+  __device__ __forceinline__ void store(const GqMmArgs& a, uint64_t row, int rows, int n0, i32x4* lds) {
+    float* turn = reinterpret_cast<float*>(lds) + wave * 16 * LD;
+    const int left = a.n - n0;
+#pragma unroll
+    for (int i = 0; i < WM; i++) {
+      constexpr int N = GLU ? 2 : 4;
+#pragma unroll
+      for (int j = 0; j < N; j++) {
+        const f32x4 v = GLU ? gated(acc[i][j], acc[i][(j + 2) % WN], a.act) : acc[i][j];
+#pragma unroll
+        for (int e = 0; e < 4; e++) turn[(q * 4 + e) * LD + j * 16 + (lane & 15)] = v[e];
+      }
+      wave_order();
+      const int r = r0 + i * 16 + (lane >> 2), c = (lane & 3) * 4 * N;
+#pragma unroll
+      for (int h = 0; h < N / 2; h++) {
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(turn + (lane >> 2) * LD + c + h * 8);
+        const f32x4 hi = *reinterpret_cast<const f32x4*>(turn + (lane >> 2) * LD + c + h * 8 + 4);
+        const uint64_t at = (row + r) * a.ldo + n0 + c0 + c + h * 8;
+        const int more = left - c0 - c - h * 8;
+        if (r < rows) {
+          if (a.out_f32) store_row8(static_cast<float*>(a.out) + at, more, lo, hi);
+          else store_row8(static_cast<typename D::T*>(a.out) + at, more, lo, hi);
+        }
+      }
+      wave_order();
+    }
+  }
+};
+
+// The scales and zeros of one column for N blocks from memory, packed as the tiles take them.
+template <int N>
+struct ColumnScales {
+  Scales<N> s;
+  __device__ __forceinline__ uint32_t packed(int i, uint32_t kept) const {
+    const uint32_t z = ((uint32_t)s.z.v[i / 4] & kept) | (0x08080808u & ~kept);
+    return (s.s.v[i / 2] >> (i & 1 ? 16 : 0) & 0xffffu) | (z >> 8 * (i & 3) & 255u) << 16;
+  }
+};
+
+// Rows of x that start anywhere: x, codes and scales come through registers, the next ones
+// under way while half a block is multiplied.
 template <typename D, int BLOCK, bool GLU, int BM>
 __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
-  constexpr int WM = BM / 32, WN = 4, COLUMNS = GLU ? 64 : 128, S = 128 / BLOCK, LD = 68;
-  typedef StageTile<true, false, 16, BM> TA;
+  typedef GqTile<D, BLOCK, GLU, BM> Tile;
+  typedef typename Tile::TA TA;
   typedef StageLoad<true, BM> LA;
-  typedef typename D::V V;
-  __shared__ i32x4 lds[2 * TA::kChunks > 4 * 16 * LD / 4 ? 2 * TA::kChunks : 4 * 16 * LD / 4];  // or the results
+  constexpr int COLUMNS = Tile::COLUMNS, S = Tile::S;
+  __shared__ i32x4 lds[2 * TA::kChunks > Tile::kTurn ? 2 * TA::kChunks : Tile::kTurn];  // or the results
   __shared__ i32x4 codes[2][128 * 4];      // [block][column][quarter]
-  __shared__ uint32_t scales[2][S][128];   // scale, and the zero in the upper half
+  __shared__ uint32_t scales[2][S][128];
   GroupTile t;
   int tn;
   if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + COLUMNS - 1) / COLUMNS, blockIdx.x, &t, &tn)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
-  const int n0 = tn * COLUMNS, left = a.n - n0, rows = t.count - t.m * BM;
+  const int tid = threadIdx.x, n0 = tn * COLUMNS, left = a.n - n0, rows = t.count - t.m * BM, blocks = (a.k + 127) / 128;
   const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
-  const int r0 = (wave >> 1) * (BM / 2), c0 = (wave & 1) * (COLUMNS / 2), blocks = (a.k + 127) / 128;
   LA ga;
   ga.init(static_cast<const uint16_t*>(a.x) + row * a.ldx, a.ldx, rows);
   // What a thread loads of a block: a quarter of two columns' codes, 64 columns apart, and the
@@ -437,59 +549,7 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
 #pragma unroll
     for (int i = 0; i < LA::N; i++) lds[h * TA::kChunks + TA::pos(ga.line + i * (256 / TA::kPerRow), ga.col / 8)] = xr[i];
   };
-  f32x4 acc[WM][WN];
-#pragma unroll
-  for (int i = 0; i < WM; i++)
-#pragma unroll
-    for (int j = 0; j < WN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-  const V one = ones(D());
-  f32x4 sum[WM][WN], xsum[WM];
-  auto clear = [&]() {
-#pragma unroll
-    for (int i = 0; i < WM; i++) {
-      xsum[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < WN; j++) sum[i][j] = f32x4{0, 0, 0, 0};
-    }
-  };
-  clear();
-  // fragment j: 16 columns of the matrix j / 2 (GLU) or the only one, from this one of the tile's
-  auto column = [&](int j) { return (GLU ? j / 2 * 64 + c0 + j % 2 * 16 : c0 + j * 16) + (lane & 15); };
-  // half h of a block of 128 steps, from half h of LDS; its codes in buffer `buf`
-  auto multiply = [&](int buf, auto h) {
-    const uint32_t pa = TA::place(lds + h.v * TA::kChunks, r0);
-    Raw<8> w[WN];
-#pragma unroll
-    for (int j = 0; j < WN; j++)
-      __builtin_memcpy(&w[j], __builtin_assume_aligned(reinterpret_cast<const char*>(&codes[buf][column(j) * 4 + q]) + h.v * 8, 8), 8);
-    each<2>([&](auto part) {
-      constexpr int U = h.v * 2 + part.v;
-      V fx[WM];
-      each<WM>([&](auto i) { fx[i.v] = __builtin_bit_cast(V, TA::template fragment<i.v, part.v>(pa)); });
-#pragma unroll
-      for (int i = 0; i < WM; i++) xsum[i] = mfma(fx[i], one, xsum[i]);
-#pragma unroll
-      for (int j = 0; j < WN; j++) {
-        V fw = expand(w[j].v[part.v], D());
-        in_order(fw);
-#pragma unroll
-        for (int i = 0; i < WM; i++) sum[i][j] = mfma(fx[i], fw, sum[i][j]);
-      }
-      if constexpr ((U + 1) * 32 % BLOCK == 0) {
-#pragma unroll
-        for (int j = 0; j < WN; j++) {
-          const uint32_t v = scales[buf][U * 32 / BLOCK][column(j)];
-          const float sc = scale_of(v & 0xffffu, a.half), ze = (float)(v >> 16);
-#pragma unroll
-          for (int i = 0; i < WM; i++) {
-            add_block(acc[i][j], sum[i][j], xsum[i], sc, ze);
-            in_order(acc[i][j]);
-          }
-        }
-        clear();
-      }
-    });
-  };
+  Tile tile;
   Next next;
   if (blocks > 0) {
     load_x(0);
@@ -505,59 +565,146 @@ __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
     ga.load(xr, b * 128 + 64);
     load_codes(next, b + 1);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(b & 1, Int<0>());
+    tile.template multiply<0>(lds, codes[b & 1], scales[b & 1], a.half);
     put(1);
     __syncthreads();
     ga.load(xr, b * 128 + 128);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(b & 1, Int<1>());
+    tile.template multiply<1>(lds + TA::kChunks, codes[b & 1], scales[b & 1], a.half);
     put(0);
     put_codes(next, (b + 1) & 1);
     __syncthreads();
   }
   for (; b < blocks; b++) {
     load_x(2 * b + 1);
-    multiply(b & 1, Int<0>());
+    tile.template multiply<0>(lds, codes[b & 1], scales[b & 1], a.half);
     put(1);
     __syncthreads();
     if (b + 1 < blocks) {
       load_x(2 * b + 2);
       load_codes(next, b + 1);
     }
-    multiply(b & 1, Int<1>());
+    tile.template multiply<1>(lds + TA::kChunks, codes[b & 1], scales[b & 1], a.half);
     if (b + 1 < blocks) {
       put(0);
       put_codes(next, (b + 1) & 1);
     }
     __syncthreads();
   }
-  // a lane: column lane % 16 of each fragment, rows lane / 16 * 4 + e; turned around in LDS,
-  // 16 rows at a time, to 16 (GLU: 8) consecutive columns of a row
-  float* turn = reinterpret_cast<float*>(lds) + wave * 16 * LD;
+  tile.store(a, row, rows, n0, lds);
+}
+
+// Rows of x that start at multiples of 16 bytes and hold multiples of 8 values: x and codes go
+// straight into LDS, two stages of 64 steps ahead (three of x, two blocks of codes in LDS), with
+// counted waits; scales 8 or 16 blocks at a time.
+template <typename D, int BLOCK, bool GLU, int BM>
+__global__ __launch_bounds__(256, 2) void gq_mm_flat(GqMmArgs a) {
+  typedef GqTile<D, BLOCK, GLU, BM> Tile;
+  typedef typename Tile::TA TA;
+  constexpr int COLUMNS = Tile::COLUMNS, S = Tile::S, PARTS = TA::kChunks / 256;
+  constexpr int SN = S == 1 ? 8 : 16, CB = SN / S;  // scales at a time; blocks of 128 that they are for
+  __shared__ i32x4 lds[3 * TA::kChunks > Tile::kTurn ? 3 * TA::kChunks : Tile::kTurn];  // or the results
+  __shared__ i32x4 codes[2][128 * 4];  // [block][column][quarter]
+  __shared__ uint32_t scales[2][SN][128];
+  GroupTile t;
+  int tn;
+  if (!find_group_tile<BM>(a.offsets, a.groups, a.rows, (a.n + COLUMNS - 1) / COLUMNS, blockIdx.x, &t, &tn)) return;
+  const int tid = threadIdx.x, n0 = tn * COLUMNS, left = a.n - n0, rows = t.count - t.m * BM, blocks = (a.k + 127) / 128;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), many = blocks * S;
+  const uint64_t row = (uint64_t)t.begin + (uint64_t)t.m * BM;
+  const uint64_t first = ((uint64_t)t.g * a.n + n0) * blocks;
+  const GqStack &wa = a.w[0], &wb = a.w[GLU ? 1 : 0];
+  const Zeros za(wa), zb(wb);
+  // this lane's chunks: of x, bytes from the stage's first value, and of codes, from the block
+  const char* const px = scalar(reinterpret_cast<const char*>(static_cast<const uint16_t*>(a.x) + row * a.ldx));
+  const char* const pa = scalar(reinterpret_cast<const char*>(wa.codes + first * 64));
+  const char* const pb = scalar(reinterpret_cast<const char*>(wb.codes + first * 64));
+  uint32_t ox[PARTS];
 #pragma unroll
-  for (int i = 0; i < WM; i++) {
-    constexpr int N = GLU ? 2 : 4;
+  for (int i = 0; i < PARTS; i++) {
+    const int p = i * 256 + tid, line = p / TA::kPerRow;
+    ox[i] = 2 * ((uint32_t)min(line, rows - 1) * (uint32_t)a.ldx + TA::swizzle(line, p % TA::kPerRow) * 8);
+  }
+  const uint32_t oa = (uint32_t)min(tid >> 2, left - 1) * blocks * 64 + (tid & 3) * 16;
+  const uint32_t ob = (uint32_t)min((tid >> 2) + (GLU ? 0 : 64), left - 1) * blocks * 64 + (tid & 3) * 16;
+  // stage s of x into its third of LDS; behind the end zeros
+  auto load_x = [&](int s, int buf) {
+    i32x4* at = lds + buf * TA::kChunks + wave * 64;
+    const char* from = scalar(px + (uint64_t)s * 128);
+    if (s * 64 + 64 <= a.k) {
 #pragma unroll
-    for (int j = 0; j < N; j++) {
-      const f32x4 v = GLU ? gated(acc[i][j], acc[i][(j + 2) % WN], a.act) : acc[i][j];
+      for (int i = 0; i < PARTS; i++) load_lds16(from, ox[i], at + i * 256);
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; e++) turn[(q * 4 + e) * LD + j * 16 + (lane & 15)] = v[e];
-    }
-    wave_order();
-    const int r = r0 + i * 16 + (lane >> 2), c = (lane & 3) * 4 * N;
-#pragma unroll
-    for (int h = 0; h < N / 2; h++) {
-      const f32x4 lo = *reinterpret_cast<const f32x4*>(turn + (lane >> 2) * LD + c + h * 8);
-      const f32x4 hi = *reinterpret_cast<const f32x4*>(turn + (lane >> 2) * LD + c + h * 8 + 4);
-      const uint64_t at = (row + r) * a.ldo + n0 + c0 + c + h * 8;
-      const int more = left - c0 - c - h * 8;
-      if (r < rows) {
-        if (a.out_f32) store_row8(static_cast<float*>(a.out) + at, more, lo, hi);
-        else store_row8(static_cast<typename D::T*>(a.out) + at, more, lo, hi);
+      for (int i = 0; i < PARTS; i++) {
+        const int p = i * 256 + tid, k = s * 64 + TA::swizzle(p / TA::kPerRow, p % TA::kPerRow) * 8;
+        load_lds16(k < a.k ? from + ox[i] : reinterpret_cast<const char*>(&kZeros), at + i * 256);
       }
     }
-    wave_order();
+  };
+  auto load_codes = [&](int b) {
+    load_lds16(scalar(pa + (uint64_t)b * 64), oa, codes[b & 1] + wave * 64);
+    load_lds16(scalar(pb + (uint64_t)b * 64), ob, codes[b & 1] + 256 + wave * 64);
+  };
+  // the scales of CB blocks from b on
+  const bool up = GLU && (tid & 64);
+  const uint64_t cs = first * S + (uint64_t)min(tid & (COLUMNS - 1), left - 1) * many;
+  auto fetch_scales = [&](int b) {
+    if (tid >= 128) return;
+    ColumnScales<SN> c;
+    const GqStack& w = up ? wb : wa;
+    const Zeros& z = up ? zb : za;
+    if (b * S + SN <= many) {
+      c.s.load(w, z, cs + b * S);
+    } else {
+#pragma unroll
+      for (auto& v : c.s.s.v) v = 0;
+#pragma unroll
+      for (auto& v : c.s.z.v) v = 0;
+#pragma unroll
+      for (int i = 0; i < SN; i++) {
+        if (b * S + i >= many) continue;
+        c.s.s.v[i / 2] |= (uint32_t)w.scales[cs + b * S + i] << (i & 1 ? 16 : 0);
+        c.s.z.v[i / 4] |= (uint32_t)z.p[cs + b * S + i] << 8 * (i & 3);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < SN; i++) scales[b / CB & 1][i][tid] = c.packed(i, za.kept);
+  };
+  // all but the last N of the wave's loads are there, and its LDS accesses done; then every wave's
+  auto arrive = [&](auto n) {
+    __builtin_amdgcn_s_waitcnt((n.v & 15) | (n.v >> 4 << 14) | 0x0070);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Tile tile;
+  if (blocks > 0) {
+    load_codes(0);
+    load_x(0, 0);
+    load_x(1, 1);
+    fetch_scales(0);
   }
+  arrive(Int<0>());
+  int buf = 0;  // of x, of the stage that is multiplied
+  for (int b = 0; b < blocks; b++) {
+    const bool more = b + 1 < blocks;
+    const uint32_t(*sc)[128] = scales[b / CB & 1] + b % CB * S;
+    if (more) {
+      load_codes(b + 1);
+      load_x(2 * b + 2, buf == 0 ? 2 : buf - 1);
+    }
+    tile.template multiply<0>(lds + buf * TA::kChunks, codes[b & 1], sc, a.half);
+    if (more) arrive(Int<2 + PARTS>());
+    else arrive(Int<0>());
+    buf = buf == 2 ? 0 : buf + 1;
+    if (more) load_x(2 * b + 3, buf == 0 ? 2 : buf - 1);
+    tile.template multiply<1>(lds + buf * TA::kChunks, codes[b & 1], sc, a.half);
+    if (more && (b + 1) % CB == 0) fetch_scales(b + 1);
+    arrive(Int<PARTS>());
+    buf = buf == 2 ? 0 : buf + 1;
+  }
+  tile.store(a, row, rows, n0, lds);
 }
 
 template <typename D, int BLOCK, bool GLU>
@@ -577,50 +724,54 @@ hipError_t run_side(uint64_t row_tiles, const GqMmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 template <typename D, int BLOCK, bool GLU, int BM>
-hipError_t run_mid(const GqMmArgs& a, hipStream_t s) {
+hipError_t run_mid(bool straight, const GqMmArgs& a, hipStream_t s) {
   constexpr int COLUMNS = GLU ? 64 : 128;
   dim3 grid;
   if (hipError_t e = tile_grid(max_row_tiles(a.rows, a.groups, BM) * ((a.n + COLUMNS - 1) / COLUMNS), 256, &grid)) return e;
-  gq_mm_mid<D, BLOCK, GLU, BM><<<grid, dim3(256), 0, s>>>(a);
+  if (straight) gq_mm_flat<D, BLOCK, GLU, BM><<<grid, dim3(256), 0, s>>>(a);
+  else gq_mm_mid<D, BLOCK, GLU, BM><<<grid, dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename D, int BLOCK, bool GLU>
-hipError_t run_gq_mm(const GqMmArgs& a, hipStream_t s) {
+hipError_t run_gq_mm(bool flat, const GqMmArgs& a, hipStream_t s) {
   // By rows to a group on average; 64 experts of 2048 x 1024, blocks of 128, bf16, us, one
-  // product and (GLU) both:
+  // product and (GLU) both; tiles with x straight into LDS.
   //   rows                2        8       16       32       64      100      128      256
   //   thin           32  58   43  68   49  72   90 132  171 254
   //   side           15  26   17  28   17  27   26  46   45  85   74 137   85 158  162 304
-  //   64 rows        63 122   60 117   58 110   58 111   60 114  113 217  116 219  225 433
-  //   128 rows                                                    73 133   76 136  146 264
+  //   tiles                                                       53 101   56 104  105 194
   // The thin kernel is for calls with few columns to the card (1 token over 8 of the experts 6.0 and
   // 8.3 for 12 and 12; one matrix 4096 x 1024, 64 rows, 8.8 and 11 for 24 and 22; 200 rows 24 and 32
-  // for 24 and 24), tiles only for what fills the card with them (900 rows 77 and 83 for 25 and 39).
+  // for 24 and 24), tiles only for what fills the card with them (900 rows 77 and 83 for 25 and 39);
+  // with x through registers they win a little later (100 rows 73 and 133, 128 rows 76 and 136 before
+  // codes came once to a workgroup).
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t thin = max_row_tiles(rows, groups, 16), wide = side_columns(GLU);
   const uint64_t mid = max_row_tiles(rows, groups, 128) * ((a.n + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
   // (the tiles count blocks of 128 rows in 32 bits)
-  if (rows > 112 * groups && mid >= 2 * kUnits && a.k <= 1 << 25) return run_mid<D, BLOCK, GLU, 128>(a, s);
+  const bool straight = flat && a.k % 8 == 0 && short_stride(a.ldx);
+  if (rows > (straight ? 80 : 112) * groups && mid >= 2 * kUnits && a.k <= 1 << 25)
+    return run_mid<D, BLOCK, GLU, 128>(straight, a, s);
   if (thin * ((a.n + wide - 1) / wide) >= 3 * kUnits / 8) return run_side<D, BLOCK, GLU>(thin, a, s);
   return run_thin<D, BLOCK, GLU>(thin, a, s);
 }
 template <typename D, bool GLU>
-hipError_t by_block(int block, const GqMmArgs& a, hipStream_t s) {
-  if (block == 32) return run_gq_mm<D, 32, GLU>(a, s);
-  if (block == 64) return run_gq_mm<D, 64, GLU>(a, s);
-  return run_gq_mm<D, 128, GLU>(a, s);
+hipError_t by_block(int block, bool flat, const GqMmArgs& a, hipStream_t s) {
+  if (block == 32) return run_gq_mm<D, 32, GLU>(flat, a, s);
+  if (block == 64) return run_gq_mm<D, 64, GLU>(flat, a, s);
+  return run_gq_mm<D, 128, GLU>(flat, a, s);
 }
 template <typename D>
-hipError_t by_form(bool glu, int block, const GqMmArgs& a, hipStream_t s) {
-  return glu ? by_block<D, true>(block, a, s) : by_block<D, false>(block, a, s);
+hipError_t by_form(bool glu, int block, bool flat, const GqMmArgs& a, hipStream_t s) {
+  return glu ? by_block<D, true>(block, flat, a, s) : by_block<D, false>(block, flat, a, s);
 }
 
 }  // namespace
 
-hipError_t launch_gq_mm(int dtype, bool glu, int block, const GqMmArgs& a, hipStream_t s) {
+hipError_t launch_gq_mm(int dtype, bool glu, int block, bool flat, const GqMmArgs& a, hipStream_t s) {
   (void)hipGetLastError();
-  return dtype == CIERA_BF16 ? by_form<Bf16>(glu, block, a, s) : by_form<Fp16>(glu, block, a, s);
+  return dtype == CIERA_BF16 ? by_form<Bf16>(glu, block, flat, a, s) : by_form<Fp16>(glu, block, flat, a, s);
 }
 
 }  // namespace ciera

@@ -409,7 +409,7 @@ static ciera_status_t gq_product(const ciera_matrix_t* x, const ciera_gq_t* w, c
   const GqMmArgs g = {x->data, {gq_stack(w), gq_stack(w2)}, out->data, offsets, x->row_stride, out->row_stride,
                       (int32_t)x->rows, (int32_t)x->cols, (int32_t)w->rows, (int32_t)w->groups, (int32_t)act,
                       half_scales(w), out->dtype == CIERA_FP32};
-  return launched("4-bit integer product launch", launch_gq_mm(x->dtype, w != w2, w->block, g, hip_stream(stream)));
+  return launched("4-bit integer product launch", launch_gq_mm(x->dtype, w != w2, w->block, flat(x), g, hip_stream(stream)));
 }
 
 ciera_status_t ciera_gq_mm(const ciera_matrix_t* x, const ciera_gq_t* w, const int32_t* offsets,

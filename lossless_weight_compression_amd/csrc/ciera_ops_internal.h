@@ -164,7 +164,7 @@ hipError_t launch_glu_mm(int dtype, bool out_f32, bool transpose_w, bool flat, c
 hipError_t launch_glu_grad(int dtype, bool out_f32, bool transpose_w, bool flat, const GluGradArgs& a, hipStream_t s);
 hipError_t launch_glu_xgrad(int dtype, bool out_f32, bool transpose_w, bool flat, const GluXgradArgs& a, hipStream_t s);
 // glu: the gated form
-hipError_t launch_gq_mm(int dtype, bool glu, int block, const GqMmArgs& a, hipStream_t s);
+hipError_t launch_gq_mm(int dtype, bool glu, int block, bool flat, const GqMmArgs& a, hipStream_t s);
 hipError_t launch_gq_quantize(int dtype, int axis, int block, const GqQuantArgs& a, hipStream_t s);
 hipError_t launch_gq_dequantize(int dtype, int block, const GqDequantArgs& a, hipStream_t s);
 
