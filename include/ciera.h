@@ -515,12 +515,12 @@ ciera_status_t ciera_gq_sizes(uint32_t groups, uint64_t rows, uint64_t cols, uin
 
 /* ciera_gq_quantize -- x (bf16, fp16 or fp32) to 4 bits, blocks along `axis` as in
  * ciera_mx_quantize.  With zeros, lo = min(block, 0) and hi = max(block, 0): s is
- * (hi - lo) / 15 in fp32, rounded to scale_dtype, z = clamp(rint(-lo / s), 0, 15)
- * and q = clamp(rint(v / s) + z, 0, 15) (quotients in fp32, ties to even).
- * Without, s is max |v| / 7, rounded, and z is 8.  A scale below 2^-126 becomes 0,
- * all codes then z, z 0 if kept.  A block with an infinity, a NaN or a scale past
- * the end of its type gets the scale NaN, codes and zero 0.  The end of a last
- * block, past q.cols, counts as zeros. */
+ * (hi - lo) times 1/15, both in fp32, rounded to scale_dtype, z = clamp(rint(-lo
+ * / s), 0, 15) and q = clamp(rint(v / s) + z, 0, 15) (quotients correctly rounded
+ * in fp32, ties to even).  Without, s is max |v| times 1/7, rounded, and z is 8.
+ * A scale below 2^-126 becomes 0, all codes then z, z 0 if kept.  A block with an
+ * infinity, a NaN or a scale past the end of its type gets the scale NaN, codes
+ * and zero 0.  The end of a last block, past q.cols, counts as zeros. */
 ciera_status_t ciera_gq_quantize(const ciera_matrix_t* x, uint32_t axis, const ciera_gq_t* q, void* stream);
 
 /* ciera_gq_dequantize -- the values q stands for, rounded once to out's type.  out

@@ -2,8 +2,8 @@
 //
 // A block of 32, 64 or 128 values v of a row shares a scale s and a zero z (0 to 15, 8 where
 // none are kept): code q stands for s (q - z).  With zeros s spreads the 16 codes over the
-// block's range, 0 in it: s = (hi - lo) / 15, z = rint(-lo / s), q = rint(v / s) + z, all
-// clamped to 0 ... 15; without, s = max |v| / 7.
+// block's range, 0 in it: s = (hi - lo) (1 / 15), z = rint(-lo / s), q = rint(v / s) + z, both
+// clamped to 0 ... 15; without, s = max |v| (1 / 7).
 #include "ciera.h"
 #include "ciera_gq.h"
 #include "ciera_ops_internal.h"
@@ -34,7 +34,7 @@ struct BlockScale {
   // of a block with the smallest and the largest value, or (symmetric) the largest magnitude
   // in hi; not finite where one of its values is not
   __device__ __forceinline__ BlockScale(float lo, float hi, bool zeros, uint32_t half) {
-    const float range = zeros ? (hi - lo) / 15.f : hi / 7.f;
+    const float range = zeros ? (hi - lo) * (1.f / 15.f) : hi * (1.f / 7.f);
     bits = scale_bits(range, half);
     s = scale_of(bits, half);
     bad = !(s < __builtin_inff());

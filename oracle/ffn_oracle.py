@@ -121,7 +121,8 @@ def gq_quantize(x: np.ndarray, block: int, kind: str, zeros: bool):
     c = np.where(finite[:, :, None], v, np.float32(0))
     lo, hi = np.minimum(c.min(axis=2), 0), np.maximum(c.max(axis=2), 0)
     with np.errstate(over="ignore"):
-        s = (hi - lo) / np.float32(15) if zeros else np.abs(c).max(axis=2) / np.float32(7)
+        s = ((hi - lo) * (np.float32(1) / np.float32(15)) if zeros
+             else np.abs(c).max(axis=2) * (np.float32(1) / np.float32(7)))
     s = to_scale_type(s, kind)
     bad = ~finite | ~np.isfinite(s)
     d = np.where(bad | (s == 0), np.float32(1), s)
