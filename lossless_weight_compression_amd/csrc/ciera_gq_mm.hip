@@ -375,9 +375,11 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
 // ------------------------------------------------------------------------ more rows
 // BM x 128 tiles (GLU: 64 columns of each matrix), 4 waves of BM / 2 x 64.  x goes through
 // LDS, 64 steps at a time, codes and scales of 128 steps too, and are expanded by the waves that
-// multiply them.  (16384 rows over 64 experts of 2048 x 1024, both products: codes read from
+// multiply them.  (16384 rows over 64 experts of 2048 x 1024, both forms: codes read from
 // memory by each of these waves 531 us, once to a workgroup 491, x and codes straight into LDS
-// 437.)  A block's sums are kept apart from the tile's: as many registers again.
+// 437, codes read from there 16 bytes at a time 394.)  A block's sums are kept apart from the
+// tile's: as many registers again.  Matrix instructions are under way 35 to 40 % of the time, as
+// many vector instructions (expansion, scales) beside them.
 template <typename D, int BLOCK, bool GLU, int BM>
 struct GqTile {
   static constexpr int WM = BM / 32, WN = 4, COLUMNS = GLU ? 64 : 128, S = 128 / BLOCK, LD = 68;
@@ -386,15 +388,8 @@ struct GqTile {
   static constexpr int kTurn = 4 * 16 * LD / 4;  // chunks that the results pass through
   int lane, wave, q, r0, c0;
   f32x4 acc[WM][WN], sum[WM][WN], xsum[WM];
+  i32x4 w[WN];  // the block's codes
 
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < WM; i++) {
-      xsum[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < WN; j++) sum[i][j] = f32x4{0, 0, 0, 0};
-    }
-  }
   __device__ __forceinline__ GqTile() {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -405,7 +400,6 @@ struct GqTile {
     for (int i = 0; i < WM; i++)
 #pragma unroll
       for (int j = 0; j < WN; j++) acc[i][j] = f32x4{0, 0, 0, 0};
-    clear();
   }
   // fragment j: 16 columns of the matrix j / 2 (GLU) or the only one, from this one of the tile's
   __device__ __forceinline__ int column(int j) const { return (GLU ? j / 2 * 64 + c0 + j % 2 * 16 : c0 + j * 16) + (lane & 15); }
@@ -414,23 +408,26 @@ struct GqTile {
   template <int H>
   __device__ __forceinline__ void multiply(const i32x4* x, const i32x4* codes, const uint32_t (*scales)[128], uint32_t half) {
     const uint32_t pa = TA::place(x, r0);
-    Raw<8> w[WN];
+    if (H == 0) {
+      // all 16 bytes at once: 8 for each half would use half of the banks
 #pragma unroll
-    for (int j = 0; j < WN; j++)
-      __builtin_memcpy(&w[j], __builtin_assume_aligned(reinterpret_cast<const char*>(&codes[column(j) * 4 + q]) + H * 8, 8), 8);
+      for (int j = 0; j < WN; j++) w[j] = codes[column(j) * 4 + q];
+    }
     each<2>([&](auto part) {
       constexpr int U = H * 2 + part.v;
+      constexpr bool FIRST = U * 32 % BLOCK == 0;  // of a block: its sums begin with the instruction's constant 0
+      constexpr f32x4 zero = {0, 0, 0, 0};
       V fx[WM];
       each<WM>([&](auto i) { fx[i.v] = __builtin_bit_cast(V, TA::template fragment<i.v, part.v>(pa)); });
       const V one = ones(D());
 #pragma unroll
-      for (int i = 0; i < WM; i++) xsum[i] = mfma(fx[i], one, xsum[i]);
+      for (int i = 0; i < WM; i++) xsum[i] = mfma(fx[i], one, FIRST ? zero : xsum[i]);
 #pragma unroll
       for (int j = 0; j < WN; j++) {
-        V fw = expand(w[j].v[part.v], D());
+        V fw = expand(w[j][U], D());
         in_order(fw);
 #pragma unroll
-        for (int i = 0; i < WM; i++) sum[i][j] = mfma(fx[i], fw, sum[i][j]);
+        for (int i = 0; i < WM; i++) sum[i][j] = mfma(fx[i], fw, FIRST ? zero : sum[i][j]);
       }
       if constexpr ((U + 1) * 32 % BLOCK == 0) {
 #pragma unroll
@@ -443,7 +440,6 @@ struct GqTile {
             in_order(acc[i][j]);
           }
         }
-        clear();
       }
     });
   }
@@ -740,7 +736,7 @@ hipError_t run_gq_mm(bool flat, const GqMmArgs& a, hipStream_t s) {
   //   rows                2        8       16       32       64      100      128      256
   //   thin           32  58   43  68   49  72   90 132  171 254
   //   side           15  26   17  28   17  27   26  46   45  85   74 137   85 158  162 304
-  //   tiles                                                       53 101   56 104  105 194
+  //   tiles                                                       47  88   50  89   93 169
   // The thin kernel is for calls with few columns to the card (1 token over 8 of the experts 6.0 and
   // 8.3 for 12 and 12; one matrix 4096 x 1024, 64 rows, 8.8 and 11 for 24 and 22; 200 rows 24 and 32
   // for 24 and 24), tiles only for what fills the card with them (900 rows 77 and 83 for 25 and 39);
