@@ -461,8 +461,9 @@ ciera_status_t ciera_group_wgrad(const ciera_matrix_t* x, const ciera_matrix_t* 
  *   CIERA_ACT_SILU  act(v) = v s(v), s(z) = 1 / (1 + exp(-z))
  *   CIERA_ACT_GELU  act(v) = v s(2 c (v + 0.044715 v^3)), c = sqrt(2 / pi)
  * Results that a call writes together are of one type, and may lie side by side
- * as columns of one buffer (equal row strides); else their address ranges must
- * not overlap, nor overlap an input's: INVALID_ARG. */
+ * as columns of one buffer (equal row strides), in ciera_glu_grad beside gate and
+ * up too; else their address ranges must not overlap, nor overlap an input's:
+ * INVALID_ARG. */
 typedef enum { CIERA_ACT_SILU = 1, CIERA_ACT_GELU = 2 } ciera_act_t;
 
 /* ciera_glu_mm -- out = act(G) U in one pass over x.  w_gate and w_up are of one

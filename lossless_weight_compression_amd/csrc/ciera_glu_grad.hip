@@ -19,6 +19,10 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void glu_grad_mid(GluGradArgs a) {
       out.at(row, n0));
 }
 
+// Large tiles, the gradients in their epilogue: D is neither written nor read again.  65536 rows,
+// 64 experts of 1024 x 2048: 390-415 us; the product alone takes 290, the 540 MB that the epilogue
+// reads and writes 80 at the memory's rate.  Each wave asks for G and U of the next 8 rows while
+// it finishes 8; four ahead took 50 registers more than there are.
 template <typename D, bool TRANS, typename O>
 __global__ __launch_bounds__(512) void glu_grad_big(GluGradArgs a) {
   typedef BigTiles<D, true, TRANS, GradOut<O>, Big::PLAIN, WaveTileGrad<D, true, TRANS>> Tiles;
@@ -27,7 +31,8 @@ __global__ __launch_bounds__(512) void glu_grad_big(GluGradArgs a) {
   big.init(lds);
   const GradOut<O> all = {static_cast<const O*>(a.gate), static_cast<const O*>(a.up), static_cast<O*>(a.dgate),
                           static_cast<O*>(a.dup), a.ldg, a.ldu, a.lddg, a.lddu, a.act};
-  big_tiles<Tiles, GradOut<O>>(a.offsets, a.groups, a.rows, a.n, a.k, big, [&](int g, uint64_t row, int om, int n0, int on, int half) {
+  big_tiles<Tiles, GradOut<O>>(a.offsets, a.groups, a.rows, a.n, a.k, big,
+                               [&](int g, uint64_t row, int om, int n0, int on, int half) {
     big.start(static_cast<const uint16_t*>(a.dy) + row * a.ldx, a.ldx, om, weights<TRANS>(a.w, g, a.gsw, a.ldw, n0), a.ldw, on,
               a.k, half);
     return all.at(row, n0);
@@ -92,11 +97,13 @@ hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t nt = (a.n + 127) / 128, mid = max_row_tiles(rows, groups, 64) * nt;
   if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 256 * groups && mid <= kUnits / 4)) {
-    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) < kUnits / 2) return run_glu_grad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
+    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) < kUnits / 2)
+      return run_glu_grad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
     return run_glu_grad_thin<D, TRANS, O, 4>(a, s);
   }
   if (mid < kUnits && a.k >= 512) return run_glu_grad_mid<D, TRANS, O, 64, 2>(a, s);
-  if (rows <= 64 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits) return run_glu_grad_mid<D, TRANS, O, 64, 1>(a, s);
+  if (rows <= 64 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits)
+    return run_glu_grad_mid<D, TRANS, O, 64, 1>(a, s);
   return run_glu_grad_mid<D, TRANS, O, 128, 1>(a, s);
 }
 

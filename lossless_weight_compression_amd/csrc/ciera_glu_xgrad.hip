@@ -20,6 +20,9 @@ __global__ __launch_bounds__(512, 2) void glu_xgrad_mid(GluXgradArgs a) {
       static_cast<const uint16_t*>(a.xu) + row * a.ldxu, a.ldxu);
 }
 
+// Large tiles over both contractions in turn: the result is written once, and a tile has twice the
+// stages.  65536 rows, 64 experts of 2048 x 1024: 530-580 us, 950-1040 TFLOP/s (two products of
+// ciera_group_mm and the addition would take 560 and 80).  Matrix instructions are busy 54 %.
 template <typename D, bool TRANS, typename O>
 __global__ __launch_bounds__(512) void glu_xgrad_big(GluXgradArgs a) {
   typedef BigTiles<D, true, TRANS, BigOut<O>, Big::SUM> Tiles;
@@ -27,7 +30,8 @@ __global__ __launch_bounds__(512) void glu_xgrad_big(GluXgradArgs a) {
   Tiles big;
   big.init(lds);
   const BigOut<O> all = {static_cast<O*>(a.out), a.ldo};
-  big_tiles<Tiles, BigOut<O>>(a.offsets, a.groups, a.rows, a.n, a.k, big, [&](int g, uint64_t row, int om, int n0, int on, int half) {
+  big_tiles<Tiles, BigOut<O>>(a.offsets, a.groups, a.rows, a.n, a.k, big,
+                              [&](int g, uint64_t row, int om, int n0, int on, int half) {
     big.start(static_cast<const uint16_t*>(a.xg) + row * a.ldxg, a.ldxg, om, weights<TRANS>(a.wg, g, a.gsg, a.ldg, n0), a.ldg, on,
               a.k, half, weights<TRANS>(a.wu, g, a.gsu, a.ldu, n0), a.ldu,
               static_cast<const uint16_t*>(a.xu) + row * a.ldxu);
@@ -75,7 +79,6 @@ hipError_t run_glu_xgrad_thin(const GluXgradArgs& a, hipStream_t s) {
 
 template <typename D, bool TRANS, typename O>
 hipError_t run_glu_xgrad(bool flat, const GluXgradArgs& a, hipStream_t s) {
-  // the second product's operands are addressed with the first one's offsets
   // As in glu_mm; 64 experts of 2048 x 1024, bf16, us:
   //   rows                2    8   16   32   64  100  128  192  256
   //   [K, N] thin       94   99  106  143  236
@@ -86,7 +89,8 @@ hipError_t run_glu_xgrad(bool flat, const GluXgradArgs& a, hipStream_t s) {
   //          64 rows        90       112
   // Tiles of two teams take a unit each: 128 rows also where those of 64 would be more than one
   // round of the card (13 groups, 2234 rows, 1447 x 777, 46 for 57; 7 groups, 2006 rows, 515 x 777,
-  // are one round: 17 for 21).
+  // are one round: 17 for 21).  The large tiles address the second product's operands with the
+  // first one's offsets, so both have to have the same strides.
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 256) && short_stride(a.ldxg) && short_stride(a.ldg) &&
       a.ldxg == a.ldxu && a.ldg == a.ldu) {
     glu_xgrad_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
@@ -95,7 +99,8 @@ hipError_t run_glu_xgrad(bool flat, const GluXgradArgs& a, hipStream_t s) {
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t nt = (a.n + 127) / 128, mid = max_row_tiles(rows, groups, 64) * nt;
   if ((rows <= 16 * groups && (!TRANS || mid < kUnits)) || (rows <= 256 * groups && mid <= kUnits / 4)) {
-    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) < kUnits / 2) return run_glu_xgrad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
+    if (!TRANS && max_row_tiles(rows, groups, 16) * ((a.n + 63) / 64) < kUnits / 2)
+      return run_glu_xgrad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
     return run_glu_xgrad_thin<D, TRANS, O, 4>(a, s);
   }
   const int64_t tiles = (rows / 64 + groups / 2 + 1) * (int64_t)nt;  // of groups that end anywhere

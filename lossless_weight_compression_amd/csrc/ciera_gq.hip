@@ -181,7 +181,9 @@ __global__ __launch_bounds__(256) void gq_quantize_rows(GqQuantArgs a, RowPass p
 // rows of x, 32 to a wave, of 64 words' columns: a wave reads 256 bytes of each row, a lane
 // holds the 32 values of its one or two columns.  The waves of one block exchange their
 // extents, and the codes go through LDS, so that 8 lanes write the 128 bytes of one column.
-// LINES: what a wave reads of a row is whole lines, which nobody reads again.
+// LINES: what a wave reads of a row is whole lines, which nobody reads again.  64 x 2048 x 1024
+// bf16, blocks of 128: 76 us, 4.4 TB/s, of which 12 vector instructions a value are a good part
+// (extents value by value in fp32, two loads to a word: 209).
 template <typename I, int BLOCK, bool LINES>
 __global__ __launch_bounds__(512) void gq_quantize_cols(GqQuantArgs a) {
   constexpr int C = 64 * I::kPer, PER = BLOCK / 32;  // columns; waves to a block
@@ -272,7 +274,8 @@ __device__ __forceinline__ void decode8(uint32_t w, float s, float z, Pack<O, 8>
 }
 
 // Rows without padding or gaps, one after another: every chunk of codes lies where its
-// values go.  A workgroup takes 1024 consecutive chunks, 4 loads to a lane under way.
+// values go.  A workgroup takes 1024 consecutive chunks, 4 loads to a lane under way
+// (64 x 2048 x 1024 bf16: 57 us, 5.9 TB/s; row by row 104).
 template <typename O, int BLOCK>
 __global__ __launch_bounds__(256) void gq_dequantize_flat(GqDequantArgs a, uint64_t chunks) {
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.q.codes);
