@@ -110,7 +110,7 @@ hipError_t run_glu_mm(bool flat, const GluMmArgs& a, hipStream_t s) {
       return run_glu_mm_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
     return run_glu_mm_thin<D, TRANS, O, 4>(a, s);
   }
-  if (mid < kUnits && a.k >= 512) return run_glu_mm_mid<D, TRANS, O, 64, 2>(a, s);
+  if (mid < kUnits && a.k >= 1024) return run_glu_mm_mid<D, TRANS, O, 64, 2>(a, s);
   if (rows <= 64 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits)
     return run_glu_mm_mid<D, TRANS, O, 64, 1>(a, s);
   return run_glu_mm_mid<D, TRANS, O, 128, 1>(a, s);

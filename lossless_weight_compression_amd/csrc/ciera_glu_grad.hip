@@ -88,7 +88,7 @@ hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
   //   [N, K] thin           74       158
   //          64 rows        52        57
   // (One matrix 4096 x 1024, 200 rows, thin 17 for 40; 24 rows, half the columns, 9.9 for 14.9; 900
-  // rows with two teams 33 for 41.)
+  // rows with two teams 33 for 41; but 777 x 515, 2006 rows over 7 groups, 21 for 20.)
   if (big_enough<TRANS>(flat, a.rows, a.groups, a.n, a.k, 256) && short_stride(a.ldx) && short_stride(a.ldw) &&
       short_stride(a.ldg) && short_stride(a.ldu) && short_stride(a.lddg) && short_stride(a.lddu)) {
     glu_grad_big<D, TRANS, O><<<dim3(kUnits), dim3(512), 0, s>>>(a);
@@ -101,7 +101,7 @@ hipError_t run_glu_grad(bool flat, const GluGradArgs& a, hipStream_t s) {
       return run_glu_grad_thin<D, TRANS, O, TRANS ? 4 : 2>(a, s);
     return run_glu_grad_thin<D, TRANS, O, 4>(a, s);
   }
-  if (mid < kUnits && a.k >= 512) return run_glu_grad_mid<D, TRANS, O, 64, 2>(a, s);
+  if (mid < kUnits && a.k >= 1024) return run_glu_grad_mid<D, TRANS, O, 64, 2>(a, s);
   if (rows <= 64 * groups || max_row_tiles(rows, groups, 128) * nt < 2 * kUnits)
     return run_glu_grad_mid<D, TRANS, O, 64, 1>(a, s);
   return run_glu_grad_mid<D, TRANS, O, 128, 1>(a, s);

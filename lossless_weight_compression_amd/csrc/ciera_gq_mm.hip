@@ -261,14 +261,19 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
           c.w[f][h] = (reinterpret_cast<const i32x4*>(a.w[f / NF].codes) + (wr[f % NF] * blocks + b + h) * 4)[q];
       }
   };
+  // scales of 8 blocks, or of one step
   struct Group {
     Scales<8> s[F];
   };
-  auto load_scales = [&](Group& g, int at) {
+  constexpr int S = 256 / BLOCK;
+  struct Single {
+    Scales<S> s[F];
+  };
+  auto load_scales = [&](auto& g, int at) {
 #pragma unroll
     for (int f = 0; f < F; f++) g.s[f].load(a.w[f / NF], zeros[f / NF], wr[f % NF] * many + at);
   };
-  auto load_scales_last = [&](Group& g, int at) {
+  auto load_scales_last = [&](Single& g, int at) {
 #pragma unroll
     for (int f = 0; f < F; f++) {
 #pragma unroll
@@ -276,7 +281,7 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
 #pragma unroll
       for (auto& v : g.s[f].z.v) v = 0;
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
+      for (int i = 0; i < S; i++) {
         if (at + i >= many) continue;
         g.s[f].s.v[i / 2] |= (uint32_t)a.w[f / NF].scales[wr[f % NF] * many + at + i] << (i & 1 ? 16 : 0);
         g.s[f].z.v[i / 4] |= (uint32_t)zeros[f / NF].p[wr[f % NF] * many + at + i] << 8 * (i & 3);
@@ -299,7 +304,7 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
 #pragma unroll
   for (int f = 0; f < F; f++) acc[f] = f32x4{0, 0, 0, 0};
   // step `st` of 256, the i-th of its group of scales
-  auto multiply = [&](const Codes& c, const Group& g, int st, auto i) {
+  auto multiply = [&](const Codes& c, const auto& g, int st, auto i) {
     const int piece = (st * 32 & (ROW - 1)) + q;
     f32x4 sum[F], xsum = {0, 0, 0, 0};
 #pragma unroll
@@ -345,16 +350,30 @@ __global__ __launch_bounds__(64 * kSideWaves) void gq_mm_side(GqMmArgs a) {
   };
   for (int i = 0; i + 1 < whole; i++) group(i, Int<0>());
   if (whole) group(whole - 1, Int<1>());
-  if (whole * 8 * BLOCK < a.k) {
+  // The whole steps that are left, less than a group, in the same way with their own scales, and
+  // what is left then.
+  const int steps = a.k / 256;
+  if (st < steps) {
+    Single one_step[2];
+    load(c[0], st * 2);
+    load_scales(one_step[0], st * S);
+    for (; st + 1 < steps; st++) {
+      if (st * 256 % CHUNK == 0) stage(st * 256);
+      load(c[1], st * 2 + 2);
+      load_scales(one_step[1], (st + 1) * S);
+      multiply(c[0], one_step[0], st, Int<0>());
+      c[0] = c[1];
+      one_step[0] = one_step[1];
+    }
     if (st * 256 % CHUNK == 0) stage(st * 256);
-    load_scales_last(g[0], whole * 8);
-    each<GS>([&](auto s) {
-      if (st * 256 < a.k) {
-        load_last(c[0], st * 2);
-        multiply(c[0], g[0], st, s);
-      }
-      st++;
-    });
+    multiply(c[0], one_step[0], st++, Int<0>());
+  }
+  if (st * 256 < a.k) {
+    Single last;
+    load_last(c[0], st * 2);
+    load_scales_last(last, st * S);
+    if (st * 256 % CHUNK == 0) stage(st * 256);
+    multiply(c[0], last, st, Int<0>());
   }
   // a lane: column lane % 16 of each 16, rows lane / 16 * 4 + e
   __syncthreads();
