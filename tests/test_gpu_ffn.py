@@ -332,6 +332,15 @@ def test_gq_products_in_tiles(shape, dtype, out, block, scales, zeros):
     check_gq(shape, dtype, out, block, scales, zeros)
 
 
+# Contractions longer than what is kept in LDS at a time (x, scales), and shorter than one stage.
+@pytest.mark.parametrize("dtype,out,block,scales,zeros", [(BF, BF, 128, BF, True), (F16, F32, 32, F16, True),
+                                                          (BF, F32, 64, F16, False), (F16, F16, 32, BF, False)])
+@pytest.mark.parametrize("shape", [(9000, 1104, 2056, 14, 1), (9000, 40, 2056, 14, 0), (9000, 8, 2056, 14, 0),
+                                   (700, 4400, 1100, 40, 1), (700, 4397, 300, 60, 0), (500, 2049, 1100, 40, 0)])
+def test_gq_products_long_and_short(shape, dtype, out, block, scales, zeros):
+    check_gq(shape, dtype, out, block, scales, zeros)
+
+
 def inside(shape, dtype, seed, pad=(3, 5), std=1.0):
     """A matrix (or stack) in the middle of a larger buffer of other numbers, and the buffer."""
     wide = list(shape)
