@@ -50,6 +50,11 @@ __device__ __forceinline__ void store_past(O* at, const P& p) {
   __builtin_nontemporal_store(__builtin_bit_cast(i32x4, p), reinterpret_cast<i32x4_any*>(at));
 }
 
+template <typename P>
+__device__ __forceinline__ P load_past(const char* at) {
+  return __builtin_bit_cast(P, (i32x4)__builtin_nontemporal_load(reinterpret_cast<const i32x4_any*>(at)));
+}
+
 // Where a tile's results go.
 template <typename O>
 struct BigOut {
@@ -362,8 +367,11 @@ struct WaveTileGrad : WaveTile16<D, AKC, BKC> {
     const uint32_t odg = (r * (uint32_t)o.lddg + c) * sizeof(O), odu = (r * (uint32_t)o.lddu + c) * sizeof(O);
     Eight<O> g[AHEAD], u[AHEAD];
     auto load = [&](int s) {
-      g[s % AHEAD] = *reinterpret_cast<const Eight<O>*>(pg + og);
-      u[s % AHEAD] = *reinterpret_cast<const Eight<O>*>(pu + ou);
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(O) / 2; i++) {
+        g[s % AHEAD].v[i] = load_past<Pack<O, PER>>(pg + og + i * 16);
+        u[s % AHEAD].v[i] = load_past<Pack<O, PER>>(pu + ou + i * 16);
+      }
       pg += 8 * o.ldg * sizeof(O);
       pu += 8 * o.ldu * sizeof(O);
     };

@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256 * TEAMS, 2) void glu_grad_mid(GluGradArgs a) {
 // Large tiles, the gradients in their epilogue: D is neither written nor read again.  65536 rows,
 // 64 experts of 1024 x 2048: 390-415 us; the product alone takes 290, the 540 MB that the epilogue
 // reads and writes 80 at the memory's rate.  Each wave asks for G and U of the next 8 rows while
-// it finishes 8; four ahead took 50 registers more than there are.
+// it finishes 8 (four ahead took 50 registers more than there are), past the caches (1 %).
 template <typename D, bool TRANS, typename O>
 __global__ __launch_bounds__(512) void glu_grad_big(GluGradArgs a) {
   typedef BigTiles<D, true, TRANS, GradOut<O>, Big::PLAIN, WaveTileGrad<D, true, TRANS>> Tiles;
