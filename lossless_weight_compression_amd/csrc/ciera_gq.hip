@@ -264,13 +264,15 @@ __global__ __launch_bounds__(512) void gq_quantize_cols(GqQuantArgs a) {
   }
 }
 
-// The values of a word: q s - z s, exact up to the rounding to O.
+// The values of a word, (q - z) s.  The difference is exact, and so is its product with a scale
+// of 11 bits: the rounding to O is the only one.  (q s - z s is no way to it: with a scale past
+// 2^128 / 15 its parts overflow where their difference does not.)
 template <typename O>
 __device__ __forceinline__ void decode8(uint32_t w, float s, float z, Pack<O, 8>* out) {
   const uint32_t lo = w & kCodeMask, hi = w >> 4 & kCodeMask;
 #pragma unroll
   for (int j = 0; j < 8; j++)
-    out->v[j] = (O)__builtin_fmaf((float)((j < 4 ? lo : hi) >> 8 * (j & 3) & 255u), s, -z * s);
+    out->v[j] = (O)(((float)((j < 4 ? lo : hi) >> 8 * (j & 3) & 255u) - z) * s);
 }
 
 // Rows without padding or gaps, one after another: every chunk of codes lies where its

@@ -1,0 +1,70 @@
+"""The gated block and the 4-bit integer operators at the ends of their types' range, against the
+definitions in 64 bits of oracle/ffn_oracle.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import ffn_oracle as P
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+from lossless_weight_compression_amd.layer import GqMatrix  # noqa: E402
+from tests.gpu_harness import say  # noqa: E402
+from tests.test_gpu_ffn import BF, F16, F32, host, np64  # noqa: E402
+
+
+# ------------------------------------------------------ 4-bit values of the largest scales
+
+def rounded_once(vals, dtype):
+    """Values in 64 bits, exact products of 5 and 11 bits at most, in a type of the result."""
+    return torch.from_numpy(vals).to(F32).to(dtype)
+
+
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(1, 3, 128), (2, 5, 256), (1, 4, 100), (3, 2, 33)])
+def test_largest_values_come_back(shape, dtype, zeros):
+    """Blocks whose scale is finite while 8 or 15 times the scale is not."""
+    say(f"[gpu] largest values {shape} {dtype} zeros={zeros}")
+    x = torch.zeros(shape, dtype=F32)
+    # with zeros the range, without them the magnitude has to be a number
+    top = (-3.38e38, -3.3e38, -2e38) if zeros else (3e38, -3.38e38, 2.99e38)
+    for r in range(shape[1]):
+        x[:, r, 0] = top[r % 3]
+        x[:, r, 1] = 0.3 * top[r % 3] if zeros else -0.3 * top[r % 3]
+    x = x.to(dtype).cuda()
+    q = GqMatrix(*shape[1:], groups=shape[0], block=32, with_zeros=zeros).quantize(x)
+    codes, s, z = host(q)
+    assert np.isfinite(s).all()
+    with np.errstate(over="ignore"):
+        vals = P.gq_values(codes, s, z, 32)[0][..., :shape[2]]
+    for out in (BF, F16, F32):
+        back = torch.full(shape, 7.0, dtype=out, device="cuda")
+        q.dequantize(back)
+        assert torch.equal(back.cpu(), rounded_once(vals, out)), out
+        assert (back[..., 2:] == 0).all()
+    # half a step and the scale's own rounding
+    assert (np.abs(np64(q.dequantize(torch.empty(shape, dtype=F32, device="cuda"))) - np64(x)) <= 0.51 * s.max()).all()
+
+
+@pytest.mark.parametrize("cols", [128, 160])
+def test_every_code_of_a_large_scale(cols):
+    """All codes with all zeros, scales from the smallest to the largest of their type."""
+    rows = 16
+    codes = np.tile(np.arange(cols) % 16, (1, rows, 1)).astype(np.uint8)
+    codes = np.concatenate([codes, np.zeros((1, rows, P.padded(cols) - cols), np.uint8)], axis=2)
+    zeros = np.tile(np.arange(rows, dtype=np.uint8)[None, :, None], (1, 1, P.padded(cols) // 32))
+    for dtype, some in ((BF, (2.0 ** -133, 2.0 ** -126, 1.5, 2.2e37, 2.4e37, 4e37, 3e38)),
+                        (F16, (2.0 ** -24, 2.0 ** -14, 3.0, 4400.0, 65504.0))):
+        for s in some:
+            scales = torch.full((1, rows, P.padded(cols) // 32), s, dtype=dtype, device="cuda")
+            q = GqMatrix(rows, cols, block=32, codes=torch.from_numpy(P.gq_pack(codes)).cuda(), scales=scales,
+                         zeros=torch.from_numpy(zeros).cuda())
+            vals = P.gq_values(codes, scales.double().cpu().numpy(), zeros, 32)[0][..., :cols]
+            for out in (BF, F16, F32):
+                back = torch.full((1, rows, cols), 7.0, dtype=out, device="cuda")
+                q.dequantize(back)
+                assert torch.equal(back.cpu(), rounded_once(vals, out)), (dtype, s, out)
