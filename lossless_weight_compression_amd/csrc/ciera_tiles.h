@@ -158,33 +158,49 @@ __device__ __forceinline__ void die_run(uint64_t all, uint32_t x, uint64_t* firs
   *n = (uint32_t)(per + (x < rem ? 1 : 0));
 }
 
+// f(0), f(1), ... with the number as a constant.
+template <int I>
+struct Int {
+  static constexpr int v = I;
+};
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (I < N) {
+    f(Int<I>());
+    each<N, I + 1>(f);
+  }
+}
+
 // Row tile and column tile of workgroup `bid`, one tile each; false: beyond the
-// last tile (the grid covers the largest possible number).  Four times 64 groups at a time,
-// whose offsets are loaded at once and, up to 256 groups, once: what a workgroup with little
-// work waits for first.
+// last tile (the grid covers the largest possible number).  Up to 64 groups at a time, or four
+// times 64 whose offsets are loaded at once and, up to 256 groups, once: what a workgroup with
+// little work waits for first.
 template <int BM>
 __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, int rows, int ntiles, uint32_t bid,
                                                 GroupTile* t, int* n) {
   int begin[4], count[4], incl[4];
   uint32_t sums[4];
-  auto four = [&](int c) {
+  auto chunks = [&](int c, auto four) {
+    constexpr int N = decltype(four)::v;  // or one
     // behind the last group both ends are the last offset
-    int from[4], to[4];
+    int from[N], to[N];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < N; i++) {
       const int g = c + i * 64 + (threadIdx.x & 63);
       from[i] = off[min(g, groups)];
       to[i] = off[min(g + 1, groups)];
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
+      begin[i] = count[i] = 0;
+      if (i >= N) continue;
       begin[i] = min(max(from[i], 0), rows);
       count[i] = max(min(max(to[i], 0), rows) - begin[i], 0);
     }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       sums[i] = incl[i] = 0;
-      if (c + i * 64 >= groups) continue;
+      if (i >= N || c + i * 64 >= groups) continue;
       incl[i] = wave_inclusive_sum((count[i] + BM - 1) / BM);
       sums[i] = (uint32_t)__builtin_amdgcn_readlane(incl[i], 63);
     }
@@ -192,8 +208,9 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
   };
   uint32_t total = 0;
   if (!off) total = (rows + BM - 1) / BM;
+  else if (groups <= 64) total = chunks(0, Int<1>());
   else
-    for (int c = 0; c < groups; c += 256) total += four(c);
+    for (int c = 0; c < groups; c += 256) total += chunks(c, Int<4>());
   uint64_t first;
   uint32_t many;
   die_run((uint64_t)total * ntiles, bid % kXcds, &first, &many);
@@ -207,7 +224,7 @@ __device__ __forceinline__ bool find_group_tile(const int32_t* off, int groups, 
     int c = 0;
     if (groups > 256) {
       for (;; c += 256) {
-        const uint32_t all = four(c);
+        const uint32_t all = chunks(c, Int<4>());
         if (before + all > mt || c + 256 >= groups) break;
         before += all;
       }
@@ -299,19 +316,6 @@ struct StageTile {
     return read_transposed((place ^ FLIP) + PART * 32 * kPerRow * 16 + HALF, 4 * kPerRow * 16);
   }
 };
-
-// f(0), f(1), ... with the number as a constant.
-template <int I>
-struct Int {
-  static constexpr int v = I;
-};
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void each(F f) {
-  if constexpr (I < N) {
-    f(Int<I>());
-    each<N, I + 1>(f);
-  }
-}
 
 // The first `left` of 8 two-byte values, zeros behind.  Loads that do not wait for each
 // other: 13 groups of 1447 x 777, fp16, 2234 rows, 29.7 us for 30.9 with a branch to each,

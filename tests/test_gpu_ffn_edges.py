@@ -11,9 +11,10 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("no GPU", allow_module_level=True)
 
+import lossless_weight_compression_amd as L  # noqa: E402
 from lossless_weight_compression_amd.layer import GqMatrix  # noqa: E402
 from tests.gpu_harness import say  # noqa: E402
-from tests.test_gpu_ffn import BF, F16, F32, host, np64  # noqa: E402
+from tests.test_gpu_ffn import BF, F16, F32, close, host, np64, off_dev, rand  # noqa: E402
 
 
 # ------------------------------------------------------ 4-bit values of the largest scales
@@ -68,3 +69,28 @@ def test_every_code_of_a_large_scale(cols):
                 back = torch.full((1, rows, cols), 7.0, dtype=out, device="cuda")
                 q.dequantize(back)
                 assert torch.equal(back.cpu(), rounded_once(vals, out)), (dtype, s, out)
+
+
+# -------------------------------------------------------------- finding a workgroup's group
+
+@pytest.mark.parametrize("groups", [1, 2, 63, 64, 65, 128, 192, 193, 255, 256, 257, 512, 513])
+@pytest.mark.parametrize("most", [2, 40])
+def test_groups_around_whole_waves_of_them(groups, most):
+    """Offsets are looked at 64 or 256 groups at a time; some without rows, the first and last with."""
+    say(f"[gpu] {groups} groups of up to {most} rows")
+    rng = np.random.default_rng(groups * 100 + most)
+    counts = rng.integers(0, most + 1, size=groups)
+    counts[0] = counts[-1] = most
+    if groups > 70:
+        counts[5:70] = 0
+    offsets = [0] + np.cumsum(counts).tolist()
+    rows, k, n = offsets[-1], 24, 40
+    x, w = rand((rows, k), BF, 1), rand((groups, k, n), BF, 2, 0.1)
+    off = off_dev(offsets)
+    want, err = P.sums(np64(x), np64(w), offsets)
+    y, h = (torch.full((rows + 3, n), 7.0, dtype=BF, device="cuda") for _ in range(2))
+    L.ciera_group_mm(x, w, y[:rows], offsets=off)
+    close(y[:rows], want, err, "y")
+    L.ciera_glu_mm(x, w, w, h[:rows], offsets=off)
+    close(h[:rows], *P.gated(want, err, want, err, "silu"), "h")
+    assert (y[rows:] == 7).all() and (h[rows:] == 7).all()
