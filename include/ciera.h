@@ -460,6 +460,7 @@ ciera_status_t ciera_group_wgrad(const ciera_matrix_t* x, const ciera_matrix_t* 
  * unrounded sums:
  *   CIERA_ACT_SILU  act(v) = v s(v), s(z) = 1 / (1 + exp(-z))
  *   CIERA_ACT_GELU  act(v) = v s(2 c (v + 0.044715 v^3)), c = sqrt(2 / pi)
+ * act and its derivative are 0 at -infinity, their limits there.
  * Results that a call writes together are of one type, and may lie side by side
  * as columns of one buffer (equal row strides), in ciera_glu_grad beside gate and
  * up too; else their address ranges must not overlap, nor overlap an input's:

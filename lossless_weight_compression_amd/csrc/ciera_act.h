@@ -16,18 +16,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float act_arg(float v, int act) {
   return act == CIERA_ACT_SILU ? v : kGelu * v * __builtin_fmaf(kGeluCube * v, v, 1.f);
 }
+// v s, where v may be -infinity and s its 0: the limit is 0.  As unsigned numbers only negative
+// NaN lie above -infinity, and a NaN's s is a NaN too: one minimum makes it the lowest number.
+__device__ __forceinline__ float times_logistic(float v, float s) {
+  return __builtin_bit_cast(float, min(__builtin_bit_cast(uint32_t, v), 0xff7fffffu)) * s;
+}
 // act(v).  exp(-z) overflows to infinity for far negative z, whose reciprocal is 0.
 __device__ __forceinline__ float act_value(float v, int act) {
-  return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * act_arg(v, act)));
+  return times_logistic(v, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * act_arg(v, act))));
 }
 // act(v) and act'(v) = s + v s (1 - s) z'(v).  With e = exp(-|z|) <= 1 both s and 1 - s are
 // quotients of e and 1 + e: neither is the difference of near numbers.  Where s (1 - s) is
-// 0 the second term is, also at infinity.
+// 0 the second term is, also at infinity, and at -infinity, what a kept G below the range of its
+// type becomes, both are 0.
 __device__ __forceinline__ void act_grad(float v, int act, float* value, float* slope) {
   const float z = act_arg(v, act), e = __builtin_amdgcn_exp2f(-kLog2e * __builtin_fabsf(z));
   const float r = __builtin_amdgcn_rcpf(1.f + e), s = z < 0.f ? e * r : r, t = e * r * r;
   const float dz = act == CIERA_ACT_SILU ? 1.f : kGelu * __builtin_fmaf(3.f * kGeluCube * v, v, 1.f);
-  *value = v * s;
+  *value = times_logistic(v, s);
   *slope = t > 0.f ? __builtin_fmaf(v * t, dz, s) : s;
 }
 

@@ -31,7 +31,8 @@ def _logistic(z):
 def act_value(v, act):
     """(act(v), error of its evaluation in 32 bits)."""
     z, _ = _z(v, act)
-    a = v * _logistic(z)
+    with np.errstate(invalid="ignore"):
+        a = np.where(v == -np.inf, 0.0, v * _logistic(z))        # its limit
     return a, np.abs(a) * (np.minimum(np.abs(z), 100) + 1) * 2.0 ** -20
 
 

@@ -71,6 +71,56 @@ def test_every_code_of_a_large_scale(cols):
                 assert torch.equal(back.cpu(), rounded_once(vals, out)), (dtype, s, out)
 
 
+# -------------------------------------------------------------- gates without a number
+
+# rows, columns that make few rows to a group, mid and large tiles of one matrix
+PLACES = [(1, 64), (90, 72), (300, 264), (700, 130), (4096, 2304)]
+INF = float("inf")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows,n", PLACES)
+def test_gates_at_infinity(rows, n, act):
+    """act(-inf) and act'(-inf) are 0, their limits; act(inf) is inf, act'(inf) 1; NaN stays."""
+    say(f"[gpu] gates at infinity {rows} {n} {act}")
+    k = 8
+    for dtype, kept in ((BF, BF), (F16, F16), (BF, F32)):
+        dy, w = torch.ones(rows, k, dtype=dtype, device="cuda"), torch.zeros(k, n, dtype=dtype, device="cuda")
+        w[0] = 3.0                                           # D = 3
+        gate, up = torch.full((rows, n), 0.5, dtype=kept, device="cuda"), torch.full((rows, n), 2.0, dtype=kept, device="cuda")
+        gate[:, 0], gate[:, 1], gate[:, 2], gate[:, n - 1] = -INF, INF, float("nan"), -INF
+        dg, du = (torch.full((rows, n), 7.0, dtype=kept, device="cuda") for _ in range(2))
+        L.ciera_glu_grad(dy, w, gate, up, dg, du, act=act)
+        for c in (0, n - 1):
+            assert (dg[:, c] == 0).all() and (du[:, c] == 0).all()
+        assert (dg[:, 1] == 6).all() and (du[:, 1] == INF).all()
+        assert torch.isnan(dg[:, 2]).all() and torch.isnan(du[:, 2]).all()
+        assert torch.isfinite(dg[:, 3:]).all() and torch.isfinite(du[:, 3:]).all()
+        # the same from sums that are not finite
+        wg = torch.zeros(k, n, dtype=dtype, device="cuda")
+        wg[0, 0], wg[0, 1], wg[0, 2], wg[0, n - 1] = -INF, INF, float("nan"), -INF
+        h = torch.full((rows, n), 7.0, dtype=kept, device="cuda")
+        L.ciera_glu_mm(dy, wg, w, h, act=act)
+        assert (h[:, 0] == 0).all() and (h[:, n - 1] == 0).all()
+        assert (h[:, 1] == INF).all() and torch.isnan(h[:, 2]).all() and (h[:, 3:n - 1] == 0).all()
+
+
+@pytest.mark.parametrize("rows,n", PLACES)
+def test_gate_kept_past_the_end_of_its_type(rows, n):
+    """A finite sum below -65504 that is kept in fp16 becomes -inf: h and both gradients are 0."""
+    k = 8
+    x = torch.full((rows, k), 100.0, dtype=F16, device="cuda")
+    wg, wu = torch.full((k, n), -1000.0, dtype=F16, device="cuda"), torch.full((k, n), 0.25, dtype=F16, device="cuda")
+    h, gate, up, dg, du = (torch.full((rows, n), 7.0, dtype=F16, device="cuda") for _ in range(5))
+    L.ciera_glu_mm(x, wg, wu, h, gate=gate, up=up)
+    assert (h == 0).all() and (gate == -INF).all() and (up == 200).all()
+    L.ciera_glu_grad(x, wu, gate, up, dg, du)
+    assert (dg == 0).all() and (du == 0).all()
+    dx = torch.full_like(x, 7.0)
+    L.ciera_glu_xgrad(dg, du, wg, wu, dx, transpose_w=True)
+    assert (dx == 0).all()
+
+
 # -------------------------------------------------------------- finding a workgroup's group
 
 @pytest.mark.parametrize("groups", [1, 2, 63, 64, 65, 128, 192, 193, 255, 256, 257, 512, 513])
