@@ -73,7 +73,8 @@ struct GluOut {
   }
 };
 
-// dG = D U act'(G) and dU = D act(G), G and U from memory.
+// dG = D U act'(G) and dU = D act(G), G and U from memory.  U act'(G) first: D U can be past the
+// range where the result is not, and act' is 1.13 at most.
 template <typename O>
 struct GradOut {
   typedef O T;
@@ -95,7 +96,7 @@ struct GradOut {
       const float d = i < 4 ? lo[i & 3] : hi[i & 3];
       float value, slope;
       act_grad(g[i], act, &value, &slope);
-      dg[i >> 2][i & 3] = d * u[i] * slope;
+      dg[i >> 2][i & 3] = d * (u[i] * slope);
       du[i >> 2][i & 3] = d * value;
     }
     store_row8(dgate + (uint64_t)r * lddg + c, left, dg[0], dg[1]);

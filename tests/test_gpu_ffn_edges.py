@@ -121,6 +121,28 @@ def test_gate_kept_past_the_end_of_its_type(rows, n):
     assert (dx == 0).all()
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows,n", PLACES)
+def test_large_gradients_of_closed_gates(rows, n, act):
+    """D U is past the range of 32 bits, D U act'(G) is not."""
+    k = 8
+    dy, w = torch.zeros(rows, k, dtype=BF, device="cuda"), torch.zeros(1, k, n, dtype=BF, device="cuda")
+    dy[:, 0], w[0, 0] = 1e20, 2.0
+    gate = torch.full((rows, n), -2000.0, dtype=F32, device="cuda")
+    gate[:, 1::3] = -2.0 if act == "gelu" else -30.0
+    up = torch.full((rows, n), 3e18, dtype=F32, device="cuda")
+    up[:, 0::3] = 1e25
+    up[:, 2::3] = -3e38
+    if act == "silu":
+        up[:, 1::3] = 1e25
+    dg, du = (torch.full((rows, n), 7.0, dtype=F32, device="cuda") for _ in range(2))
+    L.ciera_glu_grad(dy, w[0], gate, up, dg, du, act=act)
+    want = P.glu_grad(np64(dy), np64(w), np64(gate), np64(up), [0, rows], act)
+    assert np.isfinite(want[0][0]).all() and np.abs(want[0][0]).max() < 3e38
+    close(dg, *want[0], "dgate")
+    close(du, *want[1], "dup")
+
+
 # -------------------------------------------------------------- finding a workgroup's group
 
 @pytest.mark.parametrize("groups", [1, 2, 63, 64, 65, 128, 192, 193, 255, 256, 257, 512, 513])
