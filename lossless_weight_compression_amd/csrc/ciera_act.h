@@ -37,11 +37,20 @@ __device__ __forceinline__ void act_grad(float v, int act, float* value, float* 
   *slope = t > 0.f ? __builtin_fmaf(v * t, dz, s) : s;
 }
 
+// a b rounded to 32 bits by itself.  The compiler makes some of the products that are then rounded
+// to fp16 one instruction with one rounding, others two: the last bit of an element would go by
+// where in which kernel it is computed, so that h would differ with G and U kept or not.
+__device__ __forceinline__ float product(float a, float b) {
+  float v = a * b;
+  asm("" : "+v"(v));
+  return v;
+}
+
 // act(G) U of 4 columns.
 __device__ __forceinline__ f32x4 gated(f32x4 g, f32x4 u, int act) {
   f32x4 h;
 #pragma unroll
-  for (int i = 0; i < 4; i++) h[i] = act_value(g[i], act) * u[i];
+  for (int i = 0; i < 4; i++) h[i] = product(act_value(g[i], act), u[i]);
   return h;
 }
 
@@ -96,8 +105,8 @@ struct GradOut {
       const float d = i < 4 ? lo[i & 3] : hi[i & 3];
       float value, slope;
       act_grad(g[i], act, &value, &slope);
-      dg[i >> 2][i & 3] = d * (u[i] * slope);
-      du[i >> 2][i & 3] = d * value;
+      dg[i >> 2][i & 3] = product(d, u[i] * slope);
+      du[i >> 2][i & 3] = product(d, value);
     }
     store_row8(dgate + (uint64_t)r * lddg + c, left, dg[0], dg[1]);
     store_row8(dup + (uint64_t)r * lddu + c, left, du[0], du[1]);

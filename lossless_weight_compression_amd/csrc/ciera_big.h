@@ -394,8 +394,8 @@ struct WaveTileGrad : WaveTile16<D, AKC, BKC> {
           const float d = i < 4 ? lo[i & 3] : hi[i & 3];
           float value, slope;
           act_grad(g[s.v % AHEAD][i], o.act, &value, &slope);
-          dg.v[i / PER].v[i % PER] = (O)(d * (u[s.v % AHEAD][i] * slope));
-          du.v[i / PER].v[i % PER] = (O)(d * value);
+          dg.v[i / PER].v[i % PER] = (O)product(d, u[s.v % AHEAD][i] * slope);
+          du.v[i / PER].v[i % PER] = (O)product(d, value);
         }
 #pragma unroll
         for (int i = 0; i < (int)sizeof(O) / 2; i++) {

@@ -14,7 +14,8 @@ if not torch.cuda.is_available():
 import lossless_weight_compression_amd as L  # noqa: E402
 from lossless_weight_compression_amd.layer import GqMatrix  # noqa: E402
 from tests.gpu_harness import say  # noqa: E402
-from tests.test_gpu_ffn import BF, F16, F32, close, host, np64, off_dev, rand  # noqa: E402
+from tests.test_gpu_ffn import (BF, F16, F32, TYPES, check_glu, check_grad, check_xgrad, close, host, np64,  # noqa: E402
+                                off_dev, rand)  # noqa: E402
 
 
 # ------------------------------------------------------ 4-bit values of the largest scales
@@ -141,6 +142,23 @@ def test_large_gradients_of_closed_gates(rows, n, act):
     assert np.isfinite(want[0][0]).all() and np.abs(want[0][0]).max() < 3e38
     close(dg, *want[0], "dgate")
     close(du, *want[1], "dup")
+
+
+# ----------------------------------------------------- large tiles, every type
+
+# Aligned sizes that fill the card with tiles of 256 rows: the last column tile a part, stages of
+# which the last is a part, one matrix, whole tiles only.
+TILES = [(4300, 200, 2056, 14, 3), (4096, 72, 2304, 1, 0), (9000, 256, 2560, 2, 0), (8192, 64, 2048, 4, 0)]
+
+
+@pytest.mark.parametrize("dtype,out", TYPES)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("shape", TILES)
+def test_large_tiles_of_every_type(shape, transpose, dtype, out):
+    check_glu(shape, transpose, dtype, out, act="silu", keep=True)
+    check_glu(shape, transpose, dtype, out, act="gelu", keep=False)
+    check_grad(shape, transpose, dtype, out, act="silu")
+    check_xgrad(shape, transpose, dtype, out)
 
 
 # -------------------------------------------------------------- finding a workgroup's group
