@@ -141,21 +141,29 @@ class LayerCodec:
         q.quantize(w, axis, stream)
         return q
 
-    def quantize_groups(self, indices: Sequence[int], axis: int = 0, block: int = 128,
-                        scale_dtype: torch.dtype = torch.bfloat16, zeros: bool = True,
+    def quantize_groups(self, indices: Sequence[int], axis: int = 0, block: Optional[int] = None,
+                        scale_dtype: Optional[torch.dtype] = None, zeros: Optional[bool] = None,
                         into: Optional["GqMatrix"] = None, stream=None) -> "GqMatrix":
         """4-bit integer copy with a scale (and zero) for every ``block`` values of the rebuilt
         tensors of these indices (one call), as ciera_gq_mm and ciera_gq_glu take it: axis 0 for
-        [in, out] matrices, 1 for [out, in] ones.  Without ``into`` its memory belongs to ``stream``."""
-        w = self.stack(indices)
-        g, r, c = w.shape
+        [in, out] matrices, 1 for [out, in] ones.  ``block`` 128, bf16 scales and zeros unless said
+        otherwise; with ``into`` they are its own, and what is said has to agree with it.  Without
+        ``into`` its memory belongs to ``stream``."""
         if axis not in (0, 1):
             raise ValueError(f"axis: {axis}, expected 0 or 1")
-        shape = (r, c) if axis else (c, r)
         q = into
+        if q is not None:
+            for name, asked, has in (("block", block, q.block), ("scale_dtype", scale_dtype, q.scales.dtype),
+                                     ("zeros", zeros, q.zeros is not None)):
+                if asked is not None and asked != has:
+                    raise ValueError(f"{name}: {asked}, but into has {has}")
+        w = self.stack(indices)
         if q is None:
+            g, r, c = w.shape
             with _memory_of(stream):
-                q = GqMatrix(*shape, groups=g, block=block, dtype=scale_dtype, with_zeros=zeros, device=self.device)
+                q = GqMatrix(*((r, c) if axis else (c, r)), groups=g, block=128 if block is None else block,
+                             dtype=torch.bfloat16 if scale_dtype is None else scale_dtype,
+                             with_zeros=zeros is None or zeros, device=self.device)
         q.quantize(w, axis, stream)
         return q
 
