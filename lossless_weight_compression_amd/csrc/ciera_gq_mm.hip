@@ -508,7 +508,10 @@ struct ColumnScales {
 };
 
 // Rows of x that start anywhere: x, codes and scales come through registers, the next ones
-// under way while half a block is multiplied.
+// under way while half a block is multiplied.  The sums of a block that is longer than 32 stay in
+// registers from one part to the next, and with what is under way beside them there are not enough:
+// 12 to 33 spill (blocks of 32: none), some of them in the loop; blocks of 64, which have most of
+// these, take 1.4 to 1.5 times as long as those of 32.
 template <typename D, int BLOCK, bool GLU, int BM>
 __global__ __launch_bounds__(256, 2) void gq_mm_mid(GqMmArgs a) {
   typedef GqTile<D, BLOCK, GLU, BM> Tile;
@@ -764,15 +767,25 @@ hipError_t run_gq_mm(bool flat, const GqMmArgs& a, hipStream_t s) {
   //   tiles                                                       47  88   50  89   93 169
   // The thin kernel is for calls with few columns to the card (1 token over 8 of the experts 6.0 and
   // 8.3 for 12 and 12; one matrix 4096 x 1024, 64 rows, 8.8 and 11 for 24 and 22; 200 rows 24 and 32
-  // for 24 and 24), tiles only for what fills the card with them (900 rows 77 and 83 for 25 and 39);
-  // with x through registers they win a little later (100 rows 73 and 133, 128 rows 76 and 136 before
-  // codes came once to a workgroup).
+  // for 24 and 24), tiles only for what fills the card with them (900 rows 77 and 83 for 25 and 39).
+  // With x through registers tiles win later, with blocks of 64 hardly at all: those of 64 and 128
+  // spill.  The same experts, rows of x 2 bytes off, groups that end anywhere, side and tiles:
+  //   rows                  64          96         160         256         512        1024
+  //   block  32, one   79   77    109   79    167  146    255  181    494  326    960  602
+  //              both 148  145    200  147    320  276    497  339    966  623   1913 1165
+  //   block 128, one   57   65     75   65    114  120    174  168    340  283    662  510
+  //              both 100  134    135  133    216  252    333  312    658  561   1298 1021
+  //   block  64, one   62  107     84  112    130  197    198  271    383  465    756  846
+  //              both 113  214    151  223    246  409    380  530    759  968   1485 1784
+  // (24 experts 1447 x 1515, blocks of 128 at 192 rows 75 and 76, both 137 and 126; of 64 at 384
+  // rows 158 and 136, 306 and 289; one matrix 2047 x 2048, blocks of 64, 8192 rows, 240 and 171.)
   const int64_t rows = a.rows, groups = a.groups;
   const uint64_t thin = max_row_tiles(rows, groups, 16), wide = side_columns(GLU);
   const uint64_t mid = max_row_tiles(rows, groups, 128) * ((a.n + (GLU ? 63 : 127)) / (GLU ? 64 : 128));
   // (the tiles count blocks of 128 rows in 32 bits)
   const bool straight = flat && a.k % 8 == 0 && short_stride(a.ldx);
-  if (rows > (straight ? 80 : 112) * groups && mid >= 2 * kUnits && a.k <= 1 << 25)
+  constexpr int kThroughRegisters = BLOCK == 32 ? 80 : BLOCK == 64 ? 1024 : 192;
+  if (rows > (straight ? 80 : kThroughRegisters) * groups && mid >= 2 * kUnits && a.k <= 1 << 25)
     return run_mid<D, BLOCK, GLU, 128>(straight, a, s);
   if (thin * ((a.n + wide - 1) / wide) >= 3 * kUnits / 8) return run_side<D, BLOCK, GLU>(thin, a, s);
   return run_thin<D, BLOCK, GLU>(thin, a, s);

@@ -14,8 +14,8 @@ if not torch.cuda.is_available():
 import lossless_weight_compression_amd as L  # noqa: E402
 from lossless_weight_compression_amd.layer import GqMatrix  # noqa: E402
 from tests.gpu_harness import say  # noqa: E402
-from tests.test_gpu_ffn import (BF, F16, F32, TYPES, check_glu, check_grad, check_xgrad, close, host, np64,  # noqa: E402
-                                off_dev, rand)  # noqa: E402
+from tests.test_gpu_ffn import (BF, F16, F32, TYPES, check_glu, check_gq, check_grad, check_xgrad, close, host,  # noqa: E402
+                                np64, off_dev, rand)  # noqa: E402
 
 
 # ------------------------------------------------------ 4-bit values of the largest scales
@@ -159,6 +159,16 @@ def test_large_tiles_of_every_type(shape, transpose, dtype, out):
     check_glu(shape, transpose, dtype, out, act="gelu", keep=False)
     check_grad(shape, transpose, dtype, out, act="silu")
     check_xgrad(shape, transpose, dtype, out)
+
+
+# Rows that are not aligned, in groups long enough for tiles whatever the block, and in groups
+# around the lengths from which on blocks of 32 and 128 take them.
+@pytest.mark.parametrize("dtype,out,block,scales,zeros", [(BF, BF, 128, BF, True), (F16, F32, 32, F16, False),
+                                                          (BF, F32, 64, F16, True), (F16, F16, 64, BF, False)])
+@pytest.mark.parametrize("shape", [(8300, 201, 4100, 7, 3), (9001, 129, 2056, 1, 1), (5000, 77, 2056, 50, 0),
+                                   (9800, 131, 1032, 50, 2), (9300, 63, 1032, 50, 0)])
+def test_4_bit_products_of_rows_anywhere(shape, dtype, out, block, scales, zeros):
+    check_gq(shape, dtype, out, block, scales, zeros)
 
 
 # -------------------------------------------------------------- finding a workgroup's group
