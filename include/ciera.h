@@ -520,9 +520,11 @@ ciera_status_t ciera_gq_sizes(uint32_t groups, uint64_t rows, uint64_t cols, uin
  * (hi - lo) times 1/15, both in fp32, rounded to scale_dtype, z = clamp(rint(-lo
  * / s), 0, 15) and q = clamp(rint(v / s) + z, 0, 15) (quotients correctly rounded
  * in fp32, ties to even).  Without, s is max |v| times 1/7, rounded, and z is 8.
- * A scale below 2^-126 becomes 0, all codes then z, z 0 if kept.  A block with an
- * infinity, a NaN or a scale past the end of its type gets the scale NaN, codes
- * and zero 0.  The end of a last block, past q.cols, counts as zeros. */
+ * Its three roundings put a scale at most 3 2^-24 of itself more than half a step
+ * of its type off the quotient by 15 or 7.  A scale below 2^-126 becomes 0, all
+ * codes then z, z 0 if kept.  A block with an infinity, a NaN or a scale past the
+ * end of its type gets the scale NaN, codes and zero 0.  The end of a last block,
+ * past q.cols, counts as zeros. */
 ciera_status_t ciera_gq_quantize(const ciera_matrix_t* x, uint32_t axis, const ciera_gq_t* q, void* stream);
 
 /* ciera_gq_dequantize -- the values q stands for, rounded once to out's type.  out
