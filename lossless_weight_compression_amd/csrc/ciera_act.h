@@ -9,7 +9,9 @@ namespace {
 
 // Both activations are v s(z(v)) with the logistic s(z) = 1 / (1 + exp(-z)): z = v, or
 // 2 c (v + 0.044715 v^3), which is the tanh form of GELU: (1 + tanh(y)) / 2 = s(2 y).  So
-// far negative v lose no digits to 1 + tanh.
+// far negative v lose no digits to the difference 1 + tanh.  What is left is the rounding of
+// exp2's argument, some 2^-23 |z| of the result (3e-6 at z = -60, where the result is 1e-25), and z's
+// own in GELU, as large.  Where s would be below 2^-126 it may be 0.
 constexpr float kGelu = 1.5957691216057308f, kGeluCube = 0.044715f;  // 2 sqrt(2 / pi)
 constexpr float kLog2e = 1.4426950408889634f;
 

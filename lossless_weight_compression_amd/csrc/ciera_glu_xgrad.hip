@@ -23,6 +23,10 @@ __global__ __launch_bounds__(512, 2) void glu_xgrad_mid(GluXgradArgs a) {
 // Large tiles over both contractions in turn: the result is written once, and a tile has twice the
 // stages.  65536 rows, 64 experts of 2048 x 1024: 530-580 us, 950-1040 TFLOP/s (two products of
 // ciera_group_mm and the addition would take 560 and 80).  Matrix instructions are busy 54 %.
+// A contraction that is not a multiple of 64 is taken without the loop that interleaves loads and
+// products, since a whole stage may follow on a part of one (1024 and 1032 steps: 467 and 547 us,
+// [N, K] 484 and 617; ciera_group_mm, which keeps the loop, loses as much to its last stage: 258 and
+// 302, 265 and 342).
 template <typename D, bool TRANS, typename O>
 __global__ __launch_bounds__(512) void glu_xgrad_big(GluXgradArgs a) {
   typedef BigTiles<D, true, TRANS, BigOut<O>, Big::SUM> Tiles;

@@ -2,9 +2,11 @@
 // What counts then is how fast the weights are read, once for every 16 rows of a group
 // (64 tokens over 8 of 256 experts each, 7168 x 2048, [K, N]: 959 us, 6.0 TB/s).  A
 // workgroup takes 16 rows of a group and some columns; its 8 waves take the contraction steps in turn, so
-// that all of them read at once, from memory into registers, the next step's values
-// under way while this one's are multiplied; their sums are joined through LDS in the
-// order of the waves.
+// that all of them read at once, from memory into registers.  A wave asks for the next step's values
+// before it multiplies one, but each load stands behind a branch (is there a next step, is it a whole
+// one), behind which the compiler waits for all loads: of every two steps the second is multiplied
+// without a wait, the first when the values of both are there, and what hides latency is the other
+// waves.  The waves' sums are joined through LDS in their order.
 #pragma once
 #include "ciera_tiles.h"
 
