@@ -485,7 +485,8 @@ ciera_status_t ciera_glu_grad(const ciera_matrix_t* dy, const ciera_matrix_t* w_
                               void* stream);
 
 /* ciera_glu_xgrad -- the gradient of x: out = dgate w_gate_g + dup w_up_g
- * (transpose_w as in ciera_group_mm), both products in one sum.  The gradients
+ * (transpose_w as in ciera_group_mm), both products in one sum.  dgate and dup in
+ * two bytes, as ciera_glu_grad gives them in dy's type, rounded once.  The gradients
  * of the weights are ciera_group_wgrad(x, dgate) and ciera_group_wgrad(x, dup). */
 ciera_status_t ciera_glu_xgrad(const ciera_matrix_t* dgate, const ciera_matrix_t* dup, const ciera_matrix_t* w_gate,
                                const ciera_matrix_t* w_up, uint32_t transpose_w, const int32_t* offsets,
@@ -540,7 +541,8 @@ ciera_status_t ciera_gq_mm(const ciera_matrix_t* x, const ciera_gq_t* w, const i
 
 /* ciera_gq_glu -- out = act(x w_gate_g^T) (x w_up_g^T), as ciera_gq_mm and
  * ciera_glu_mm.  w_gate and w_up agree in everything but their pointers, and both
- * or neither have zeros. */
+ * or neither have zeros.  ciera_gq_mm takes the result in x's type, rounded
+ * once on the way. */
 ciera_status_t ciera_gq_glu(const ciera_matrix_t* x, const ciera_gq_t* w_gate, const ciera_gq_t* w_up, uint32_t act,
                             const int32_t* offsets, const ciera_matrix_t* out, void* stream);
 

@@ -759,8 +759,9 @@ hipError_t run_mid(bool straight, const GqMmArgs& a, hipStream_t s) {
 
 template <typename D, int BLOCK, bool GLU>
 hipError_t run_gq_mm(bool flat, const GqMmArgs& a, hipStream_t s) {
-  // By rows to a group on average; 64 experts of 2048 x 1024, blocks of 128, bf16, us, one
-  // product and (GLU) both; tiles with x straight into LDS.
+  // By rows to a group on average; 64 experts of 2048 x 1024, as many rows to each, blocks of 128,
+  // bf16, us, one product and (GLU) both; tiles with x straight into LDS (where groups end anywhere
+  // 64 rows take side workgroups 53 and 95, tiles 42 and 83, 48 rows 42 and 76, 42 and 81).
   //   rows                2        8       16       32       64      100      128      256
   //   thin           32  58   43  68   49  72   90 132  171 254
   //   side           15  26   17  28   17  27   26  46   45  85   74 137   85 158  162 304
